@@ -25,12 +25,15 @@ NF4_F32, NF4_BF16, NF4_F16 = 0, 1, 2
 NF4_DQ_INT8, NF4_DQ_FP8 = 0, 1
 NF4_QT_NF4, NF4_QT_FP4 = 0, 1
 BLOCKSIZE, BLOCKSIZE2 = 64, 256
+MAX_EXPERTS = 1024
 
 EXPORTS = (
     "nf4_last_error", "nf4_codebook", "nf4_codebook_fp4", "nf4_quantize", "nf4_quantize_fp4", "nf4_double_quant_workspace",
     "nf4_double_quant", "nf4_e4m3_ratio", "nf4_double_quant_f8", "nf4_dequantize", "nf4_gemv", "nf4_gemm_workspace", "nf4_gemm", "nf4_gemm_dx_workspace",
     "nf4_gemm_dx", "nf4_lora_grads_workspace", "nf4_lora_grads", "nf4_lora_merge", "nf4_double_quant_noalloc",
     "nf4_gemv_batched", "nf4_double_quant_batched_workspace", "nf4_double_quant_batched", "nf4_quantize_batched",
+    "nf4_expert_plan_workspace", "nf4_expert_plan", "nf4_expert_gemm", "nf4_expert_gemm_dx", "nf4_expert_combine",
+    "nf4_expert_combine_backward", "nf4_int4_quantize", "nf4_int4_dequantize", "nf4_int4_gemv",
 )
 
 
@@ -63,6 +66,14 @@ class nf4_weight(ctypes.Structure):
     ]
 
 
+class nf4_int4_weight(ctypes.Structure):
+    """Mirror of `struct nf4_int4_weight` in include/nf4.h."""
+    _fields_ = [
+        ("packed", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("group", ctypes.c_int32),
+        ("scale_dtype", ctypes.c_int32), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+    ]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -76,6 +87,7 @@ def lib() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     wp = ctypes.POINTER(nf4_weight)
+    i4p = ctypes.POINTER(nf4_int4_weight)
     sig = {
         "nf4_last_error": (ctypes.c_char_p, []),
         "nf4_codebook": (ctypes.c_int, [ctypes.POINTER(ctypes.c_float)]),
@@ -100,6 +112,15 @@ def lib() -> ctypes.CDLL:
         "nf4_lora_grads_workspace": (sz, [i64, i64, i64, i32]),
         "nf4_lora_grads": (ctypes.c_int, [vp, vp, i64, i64, i64, vp, vp, i32, ctypes.c_float, vp, vp, vp, sz, vp]),
         "nf4_lora_merge": (ctypes.c_int, [wp, vp, vp, i32, ctypes.c_float, vp, ctypes.c_int, vp]),
+        "nf4_expert_plan_workspace": (sz, [i64, i32]),
+        "nf4_expert_plan": (ctypes.c_int, [vp, i64, i32, vp, vp, vp, vp, sz, vp]),
+        "nf4_expert_gemm": (ctypes.c_int, [wp, i32, vp, i64, vp, i32, vp, i64, vp, vp]),
+        "nf4_expert_gemm_dx": (ctypes.c_int, [wp, i32, vp, vp, i64, vp, vp]),
+        "nf4_expert_combine": (ctypes.c_int, [vp, i64, vp, i64, i32, i64, vp, vp, vp]),
+        "nf4_expert_combine_backward": (ctypes.c_int, [vp, vp, i64, vp, i64, i32, i64, vp, vp, vp, vp]),
+        "nf4_int4_quantize": (ctypes.c_int, [vp, ctypes.c_int, i4p, vp]),
+        "nf4_int4_dequantize": (ctypes.c_int, [i4p, vp, ctypes.c_int, vp]),
+        "nf4_int4_gemv": (ctypes.c_int, [i4p, vp, ctypes.c_int, i64, vp, ctypes.c_int, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -148,6 +169,10 @@ def nf4_gemm_workspace(m: int, rows: int, r: int) -> int:
 
 def nf4_gemm_dx_workspace(m: int, rows: int, r: int) -> int:
     return int(lib().nf4_gemm_dx_workspace(m, rows, r))
+
+
+def nf4_expert_plan_workspace(n: int, experts: int) -> int:
+    return int(lib().nf4_expert_plan_workspace(n, experts))
 
 
 def nf4_lora_grads_workspace(m: int, rows: int, cols: int, r: int) -> int:
@@ -644,3 +669,236 @@ def nf4_lora_merge(w: NF4Weight, lora_a, lora_b, lora_scale: float, out=None, ou
     _check(lib().nf4_lora_merge(ctypes.byref(cs), _ptr(lora_a), _ptr(lora_b), r, float(lora_scale), _ptr(out),
                                 _dtype_code(out), _stream(stream)))
     return out
+
+
+# ------------------------------------------------- mixture-of-experts products
+
+def _call(dev, stream, fn, *args) -> None:
+    """fn(*args, stream) on the tensors' device, whichever is current: on
+    `stream`, which must be one of that device, or on its current stream."""
+    torch = _torch()
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"stream of {stream.device}, tensors on {dev}")
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, stream.cuda_stream))
+
+
+def _need(name, t, dtype, numel, dev):
+    """A contiguous device tensor of that dtype and number of elements."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous device tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"{name} holds {t.numel()} elements, expected {numel}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def nf4_expert_plan(ids, experts: int, order=None, position=None, offsets=None, workspace=None, stream=None):
+    """The slots' expert ids (int32, any shape: n of them) sorted by expert:
+    returns (order [n], position [n], offsets [experts + 1]), int32.  order[p]
+    is the slot at sorted row p (-1 past the last), position[s] the row of slot
+    s (-1 where its id is outside 0 .. experts - 1: a dropped slot)."""
+    torch = _torch()
+    dev, n = ids.device, ids.numel()
+    _need("ids", ids, torch.int32, n, dev)
+    order = _alloc_on(stream, (n,), torch.int32, dev) if order is None else order
+    position = _alloc_on(stream, (n,), torch.int32, dev) if position is None else position
+    offsets = _alloc_on(stream, (max(experts, 0) + 1,), torch.int32, dev) if offsets is None else offsets
+    _need("order", order, torch.int32, n, dev)
+    _need("position", position, torch.int32, n, dev)
+    _need("offsets", offsets, torch.int32, experts + 1, dev)
+    wsb = nf4_expert_plan_workspace(n, experts)
+    if wsb and workspace is None:
+        workspace = _alloc_on(stream, (wsb,), torch.uint8, dev)
+    _need_cuda(workspace)
+    _same_device(dev, workspace)
+    wsn = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(dev, stream, lib().nf4_expert_plan, ids.data_ptr(), n, experts, order.data_ptr(), position.data_ptr(),
+          offsets.data_ptr(), _ptr(workspace), wsn)
+    return order, position, offsets
+
+
+def nf4_expert_gemm(w: NF4Weight, experts: int, x, offsets, index=None, slots: int = 1, y=None, stream=None):
+    """y[p] = x[row(p)] . deq(W_e)^T for the rows p of every expert e; w stacks
+    the experts' weights along its rows.  Without index, row(p) = p; with it
+    (the plan's order), row(p) = index[p] / slots.  bf16 in and out.  Rows of y
+    past offsets[experts] are not written."""
+    torch = _torch()
+    x2 = _as_rows(x, w.cols, stream)
+    cs = w.c_struct()
+    dev = w.device
+    if not 1 <= experts <= MAX_EXPERTS or w.rows % experts:
+        raise ValueError(f"a weight of {w.rows} rows does not stack {experts} experts")
+    m = x2.shape[0] if index is None else index.numel()
+    rows = w.rows // experts
+    _need("x", x2, torch.bfloat16, x2.numel(), dev)
+    _need("offsets", offsets, torch.int32, experts + 1, dev)
+    if index is not None:
+        _need("index", index, torch.int32, m, dev)
+    if y is None:
+        y = _alloc_on(stream, (m, rows), torch.bfloat16, dev)
+    _need("y", y, torch.bfloat16, m * rows, dev)
+    _call(dev, stream, lib().nf4_expert_gemm, ctypes.byref(cs), experts, x2.data_ptr(), x2.shape[0], _ptr(index), slots,
+          offsets.data_ptr(), m, y.data_ptr())
+    return y
+
+
+def nf4_expert_gemm_dx(w: NF4Weight, experts: int, dy, offsets, dx=None, stream=None):
+    """dx[p] = dy[p] . deq(W_e), nf4_expert_gemm's input gradient by sorted row
+    (with a gathered x, nf4_expert_combine of dx adds a row's slots)."""
+    torch = _torch()
+    if not 1 <= experts <= MAX_EXPERTS or w.rows % experts:
+        raise ValueError(f"a weight of {w.rows} rows does not stack {experts} experts")
+    dy2 = _as_rows(dy, w.rows // experts, stream)
+    cs = w.c_struct()
+    dev, m = w.device, dy2.shape[0]
+    _need("dy", dy2, torch.bfloat16, dy2.numel(), dev)
+    _need("offsets", offsets, torch.int32, experts + 1, dev)
+    if dx is None:
+        dx = _alloc_on(stream, (m, w.cols), torch.bfloat16, dev)
+    _need("dx", dx, torch.bfloat16, m * w.cols, dev)
+    _call(dev, stream, lib().nf4_expert_gemm_dx, ctypes.byref(cs), experts, dy2.data_ptr(), offsets.data_ptr(), m,
+          dx.data_ptr())
+    return dx
+
+
+def nf4_expert_combine(y, position, slots: int, weights=None, out=None, stream=None):
+    """out[t] = sum_j weights[t][j] . y[position[t][j]] (weights None: ones);
+    y bf16 [m, cols], position int32 with `slots` entries per token, weights
+    float32.  Positions outside 0 .. m - 1 add nothing."""
+    torch = _torch()
+    dev = y.device
+    if y.dim() != 2 or slots < 1 or position.numel() % slots:
+        raise ValueError("y must be [m, cols], and position hold `slots` entries per token")
+    (m, cols), n = y.shape, position.numel()
+    _need("y", y, torch.bfloat16, m * cols, dev)
+    _need("position", position, torch.int32, n, dev)
+    if weights is not None:
+        _need("weights", weights, torch.float32, n, dev)
+    if out is None:
+        out = _alloc_on(stream, (n // slots, cols), torch.bfloat16, dev)
+    _need("out", out, torch.bfloat16, n // slots * cols, dev)
+    _call(dev, stream, lib().nf4_expert_combine, y.data_ptr(), m, position.data_ptr(), n // slots, slots, cols,
+          _ptr(weights), out.data_ptr())
+    return out
+
+
+def nf4_expert_combine_backward(dout, y, position, slots: int, weights=None, dy=None, dweights=None, want=("dy", "dweights"),
+                                stream=None):
+    """The gradients of nf4_expert_combine: (dy [m, cols] bf16, dweights
+    [tokens, slots] float32); one not in `want` (and not given) is None.  Rows
+    of dy that no position names are not written."""
+    torch = _torch()
+    dev = dout.device
+    if y.dim() != 2 or slots < 1 or position.numel() % slots:
+        raise ValueError("y must be [m, cols], and position hold `slots` entries per token")
+    (m, cols), n = y.shape, position.numel()
+    _need("dout", dout, torch.bfloat16, n // slots * cols, dev)
+    _need("y", y, torch.bfloat16, m * cols, dev)
+    _need("position", position, torch.int32, n, dev)
+    if weights is not None:
+        _need("weights", weights, torch.float32, n, dev)
+    if dy is None and "dy" in want:
+        dy = _alloc_on(stream, (m, cols), torch.bfloat16, dev)
+    if dweights is None and "dweights" in want:
+        dweights = _alloc_on(stream, (n // slots, slots), torch.float32, dev)
+    if dy is not None:
+        _need("dy", dy, torch.bfloat16, m * cols, dev)
+    if dweights is not None:
+        _need("dweights", dweights, torch.float32, n, dev)
+    _call(dev, stream, lib().nf4_expert_combine_backward, dout.data_ptr(), y.data_ptr(), m, position.data_ptr(),
+          n // slots, slots, cols, _ptr(weights), _ptr(dy), _ptr(dweights))
+    return dy, dweights
+
+
+# ------------------------------------ uniform 4-bit weights with group scales
+
+@dataclass
+class Int4Weight:
+    """W[rows][cols] = (q - z) . s with a scale s and a zero point z (None: 8)
+    per `group` columns of a row; codes packed as NF4Weight's."""
+    packed: "object"
+    rows: int
+    cols: int
+    group: int
+    scales: "object"          # [rows][cols / group], float32, bfloat16 or float16
+    zeros: "object" = None    # [rows][cols / group] uint8, or None
+
+    def check(self) -> None:
+        """Host-side check of the buffers against the shape (the C ABI takes
+        bare pointers).  Raises ValueError or TypeError."""
+        torch = _torch()
+        if self.group not in (32, 64, 128):
+            raise ValueError(f"group {self.group}: 32, 64 or 128")
+        if self.rows < 1 or self.cols < 1 or self.cols % self.group:
+            raise ValueError(f"bad shape {self.rows} x {self.cols} for groups of {self.group}")
+        dev, n = self.packed.device, self.rows * self.cols
+        _dtype_code(self.scales)
+        _need("packed", self.packed, torch.uint8, n // 2, dev)
+        _need("scales", self.scales, self.scales.dtype, n // self.group, dev)
+        if self.zeros is not None:
+            _need("zeros", self.zeros, torch.uint8, n // self.group, dev)
+
+    @property
+    def device(self):
+        return self.packed.device
+
+    def c_struct(self) -> nf4_int4_weight:
+        self.check()
+        return nf4_int4_weight(self.packed.data_ptr(), self.rows, self.cols, self.group, _dtype_code(self.scales),
+                               self.scales.data_ptr(), _ptr(self.zeros))
+
+
+def nf4_int4_quantize(x, w: Int4Weight, stream=None) -> Int4Weight:
+    """Quantizes x (float32, bf16 or fp16, rows * cols values) into w's
+    buffers; w.zeros None: symmetric codes."""
+    cs = w.c_struct()
+    _need("x", x, x.dtype, w.rows * w.cols, w.device)
+    _call(w.device, stream, lib().nf4_int4_quantize, x.data_ptr(), _dtype_code(x), ctypes.byref(cs))
+    return w
+
+
+def quantize_int4(w, group: int = 128, symmetric: bool = True, scale_dtype=None, stream=None) -> Int4Weight:
+    """A 2-D weight (float32, bf16 or fp16) as an Int4Weight; scales in
+    scale_dtype (default bf16), with zero points where not symmetric."""
+    torch = _torch()
+    if w.dim() != 2 or group < 1 or w.shape[1] % group:
+        raise ValueError("the weight must be [rows, cols] with cols a multiple of the group")
+    rows, cols = w.shape
+    dev = w.device
+    packed = _alloc_on(stream, (rows * cols // 2,), torch.uint8, dev)
+    scales = _alloc_on(stream, (rows, cols // group), scale_dtype or torch.bfloat16, dev)
+    zeros = None if symmetric else _alloc_on(stream, (rows, cols // group), torch.uint8, dev)
+    return nf4_int4_quantize(w, Int4Weight(packed, rows, cols, group, scales, zeros), stream=stream)
+
+
+def nf4_int4_dequantize(w: Int4Weight, out=None, out_dtype=None, stream=None):
+    """(q - z) . s as a dense [rows, cols] tensor (default bf16)."""
+    torch = _torch()
+    cs = w.c_struct()
+    if out is None:
+        out = _alloc_on(stream, (w.rows, w.cols), out_dtype or torch.bfloat16, w.device)
+    _need("out", out, out.dtype, w.rows * w.cols, w.device)
+    _call(w.device, stream, lib().nf4_int4_dequantize, ctypes.byref(cs), out.data_ptr(), _dtype_code(out))
+    return out
+
+
+def nf4_int4_gemv(w: Int4Weight, x, y=None, y_dtype=None, stream=None):
+    """y = x . W^T for x [m, cols], 1 <= m <= 16, in bf16 or fp16; y in x's
+    dtype unless y_dtype (or y) says otherwise."""
+    x2 = _as_rows(x, w.cols, stream)
+    cs = w.c_struct()
+    m, dev = x2.shape[0], w.device
+    _need("x", x2, x2.dtype, m * w.cols, dev)
+    if y is None:
+        y = _alloc_on(stream, (m, w.rows), y_dtype or x2.dtype, dev)
+    _need("y", y, y.dtype, m * w.rows, dev)
+    _call(dev, stream, lib().nf4_int4_gemv, ctypes.byref(cs), x2.data_ptr(), _dtype_code(x2), m, y.data_ptr(), _dtype_code(y))
+    return y

@@ -100,6 +100,52 @@ hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 const uint8_t* w_packed(const nf4_weight& w) { return w.packed; }
 
+constexpr int64_t kMaxRows = int64_t(1) << 31;  // rows of the grouped products (their indices are int32)
+
+bool known_dtype(int t) { return t == NF4_F32 || t == NF4_BF16 || t == NF4_F16; }
+
+int check_experts(int32_t experts, const char* who) {
+  if (experts < 1 || experts > NF4_MAX_EXPERTS)
+    return fail(NF4_ERR_SIZE, "%s: experts = %d out of range 1..%d", who, (int)experts, NF4_MAX_EXPERTS);
+  return NF4_OK;
+}
+
+// The experts' stacked weight and the product's rows.
+int check_stack(const nf4_weight* w, int32_t experts, int64_t m, const char* who) {
+  if (int rc = check_experts(experts, who)) return rc;
+  if (w->rows % experts)
+    return fail(NF4_ERR_SIZE, "%s: rows = %lld are not a multiple of experts = %d", who, (long long)w->rows, (int)experts);
+  if (w->cols % 64) return fail(NF4_ERR_SIZE, "%s: cols = %lld is not a multiple of 64", who, (long long)w->cols);
+  if (w->cols >= (int64_t(1) << 23)) return fail(NF4_ERR_SIZE, "%s: cols = %lld out of range", who, (long long)w->cols);
+  if (m < 1 || m >= kMaxRows) return fail(NF4_ERR_SIZE, "%s: m = %lld out of range", who, (long long)m);
+  return NF4_OK;
+}
+
+int check_combine(int64_t m, int64_t tokens, int32_t slots, int64_t cols, const char* who) {
+  if (m < 1 || m >= kMaxRows) return fail(NF4_ERR_SIZE, "%s: m = %lld out of range", who, (long long)m);
+  if (tokens < 1 || slots < 1 || tokens >= kMaxRows || tokens * slots >= kMaxRows)
+    return fail(NF4_ERR_SIZE, "%s: tokens = %lld, slots = %d out of range", who, (long long)tokens, (int)slots);
+  if (cols < 8 || cols % 8 || cols >= kMaxRows)
+    return fail(NF4_ERR_SIZE, "%s: cols = %lld is not a positive multiple of 8", who, (long long)cols);
+  return NF4_OK;
+}
+
+int check_int4(const nf4_int4_weight* w, nf4i::Int4Weight* out, const char* who) {
+  if (!w) return fail(NF4_ERR_NULL, "%s: weight descriptor is NULL", who);
+  if (!w->packed || !w->scales) return fail(NF4_ERR_NULL, "%s: the weight's packed and scales are required", who);
+  if (w->group != 32 && w->group != 64 && w->group != 128)
+    return fail(NF4_ERR_BLOCKSIZE, "%s: group %d unsupported (32, 64 or 128)", who, (int)w->group);
+  if (w->rows < 1 || w->cols < 1 || w->rows > kMaxN || w->cols > kMaxN || w->rows > kMaxN / w->cols || w->cols % w->group)
+    return fail(NF4_ERR_SIZE, "%s: bad shape %lld x %lld (cols must be a multiple of the group, %d)", who,
+                (long long)w->rows, (long long)w->cols, (int)w->group);
+  if (!known_dtype(w->scale_dtype)) return fail(NF4_ERR_DTYPE, "%s: scale_dtype %d unknown", who, (int)w->scale_dtype);
+  if (!aligned(w->packed, 16)) return fail(NF4_ERR_ALIGN, "%s: packed must be 16-byte aligned", who);
+  if (!aligned(w->scales, w->scale_dtype == NF4_F32 ? 4 : 2))
+    return fail(NF4_ERR_ALIGN, "%s: scales must be aligned to their type", who);
+  *out = nf4i::Int4Weight{w->packed, w->rows, w->cols, w->group, w->scales, w->scale_dtype, w->zeros};
+  return NF4_OK;
+}
+
 }  // namespace
 
 int nf4i::device_cus() { return t_cus; }
@@ -476,6 +522,146 @@ int nf4_lora_merge(const nf4_weight* w, const void* lora_a, const void* lora_b, 
                                           static_cast<const uint16_t*>(lora_b), r, lora_scale,
                                           static_cast<uint16_t*>(out), out_dtype == NF4_F16, as_stream(stream)),
                   "nf4_lora_merge");
+}
+
+// ---- mixture-of-experts products
+
+size_t nf4_expert_plan_workspace(int64_t n, int32_t experts) {
+  if (n < 1 || n >= kMaxRows || experts < 1 || experts > NF4_MAX_EXPERTS) return 0;
+  return nf4i::expert_plan_workspace(n, experts);
+}
+
+int nf4_expert_plan(const int32_t* ids, int64_t n, int32_t experts, int32_t* order, int32_t* position,
+                    int32_t* offsets, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "nf4_expert_plan";
+  if (!ids || !order || !position || !offsets)
+    return fail(NF4_ERR_NULL, "%s: ids, order, position and offsets are required", who);
+  if (n < 1 || n >= kMaxRows) return fail(NF4_ERR_SIZE, "%s: n = %lld out of range", who, (long long)n);
+  if (int rc = check_experts(experts, who)) return rc;
+  if (!aligned(ids, 4) || !aligned(order, 4) || !aligned(position, 4) || !aligned(offsets, 4) || !aligned(workspace, 4))
+    return fail(NF4_ERR_ALIGN, "%s: arrays must be 4-byte aligned", who);
+  const size_t need = nf4i::expert_plan_workspace(n, experts);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(NF4_ERR_WORKSPACE, "%s: workspace needs %zu bytes", who, need);
+  if (int rc = check_device()) return rc;
+  return launched(nf4i::launch_expert_plan(ids, n, experts, order, position, offsets, workspace, as_stream(stream)), who);
+}
+
+int nf4_expert_gemm(const nf4_weight* w, int32_t experts, const void* x, int64_t x_rows, const int32_t* index,
+                    int32_t slots, const int32_t* offsets, int64_t m, void* y, void* stream) {
+  const char* who = "nf4_expert_gemm";
+  nf4i::Scales sc{};
+  int64_t n = 0;
+  if (int rc = check_weight(w, &sc, &n, who)) return rc;
+  if (!x || !offsets || !y) return fail(NF4_ERR_NULL, "%s: x, offsets and y are required", who);
+  if (int rc = check_stack(w, experts, m, who)) return rc;
+  if (x_rows < 1 || x_rows > kMaxRows) return fail(NF4_ERR_SIZE, "%s: x_rows = %lld out of range", who, (long long)x_rows);
+  if (slots < 1) return fail(NF4_ERR_SIZE, "%s: slots = %d out of range", who, (int)slots);
+  if (!index && x_rows < m)
+    return fail(NF4_ERR_SIZE, "%s: without index, x needs m = %lld rows and has %lld", who, (long long)m, (long long)x_rows);
+  if (!aligned(x, 16) || !aligned(y, 16)) return fail(NF4_ERR_ALIGN, "%s: x and y must be 16-byte aligned", who);
+  if (!aligned(index, 4) || !aligned(offsets, 4))
+    return fail(NF4_ERR_ALIGN, "%s: index and offsets must be 4-byte aligned", who);
+  if (int rc = check_device()) return rc;
+  return launched(nf4i::launch_expert_gemm(w->packed, w->rows / experts, w->cols, sc, nf4i::ExpertRows{offsets, experts, m},
+                                           nf4i::ExpertX{static_cast<const uint16_t*>(x), x_rows, index, slots},
+                                           static_cast<uint16_t*>(y), as_stream(stream)),
+                  who);
+}
+
+int nf4_expert_gemm_dx(const nf4_weight* w, int32_t experts, const void* dy, const int32_t* offsets, int64_t m,
+                       void* dx, void* stream) {
+  const char* who = "nf4_expert_gemm_dx";
+  nf4i::Scales sc{};
+  int64_t n = 0;
+  if (int rc = check_weight(w, &sc, &n, who)) return rc;
+  if (!dy || !offsets || !dx) return fail(NF4_ERR_NULL, "%s: dy, offsets and dx are required", who);
+  if (int rc = check_stack(w, experts, m, who)) return rc;
+  const int64_t rows = w->rows / experts;
+  if (rows % 8) return fail(NF4_ERR_SIZE, "%s: an expert's rows = %lld are not a multiple of 8", who, (long long)rows);
+  if (rows >= (int64_t(1) << 23)) return fail(NF4_ERR_SIZE, "%s: an expert's rows = %lld out of range", who, (long long)rows);
+  if (!aligned(dy, 16) || !aligned(dx, 16)) return fail(NF4_ERR_ALIGN, "%s: dy and dx must be 16-byte aligned", who);
+  if (!aligned(offsets, 4)) return fail(NF4_ERR_ALIGN, "%s: offsets must be 4-byte aligned", who);
+  if (int rc = check_device()) return rc;
+  return launched(nf4i::launch_expert_gemm_dx(w->packed, rows, w->cols, sc, nf4i::ExpertRows{offsets, experts, m},
+                                              static_cast<const uint16_t*>(dy), static_cast<uint16_t*>(dx),
+                                              as_stream(stream)),
+                  who);
+}
+
+int nf4_expert_combine(const void* y, int64_t m, const int32_t* position, int64_t tokens, int32_t slots, int64_t cols,
+                       const float* weights, void* out, void* stream) {
+  const char* who = "nf4_expert_combine";
+  if (!y || !position || !out) return fail(NF4_ERR_NULL, "%s: y, position and out are required", who);
+  if (int rc = check_combine(m, tokens, slots, cols, who)) return rc;
+  if (!aligned(y, 16) || !aligned(out, 16)) return fail(NF4_ERR_ALIGN, "%s: y and out must be 16-byte aligned", who);
+  if (!aligned(position, 4) || !aligned(weights, 4))
+    return fail(NF4_ERR_ALIGN, "%s: position and weights must be 4-byte aligned", who);
+  if (int rc = check_device()) return rc;
+  return launched(nf4i::launch_expert_combine(static_cast<const uint16_t*>(y), m, position, tokens, slots, cols, weights,
+                                              static_cast<uint16_t*>(out), as_stream(stream)),
+                  who);
+}
+
+int nf4_expert_combine_backward(const void* dout, const void* y, int64_t m, const int32_t* position, int64_t tokens,
+                                int32_t slots, int64_t cols, const float* weights, void* dy, float* dweights,
+                                void* stream) {
+  const char* who = "nf4_expert_combine_backward";
+  if (!dout || !position) return fail(NF4_ERR_NULL, "%s: dout and position are required", who);
+  if (!dy && !dweights) return fail(NF4_ERR_NULL, "%s: at least one of dy and dweights is required", who);
+  if (dweights && !y) return fail(NF4_ERR_NULL, "%s: dweights needs y", who);
+  if (int rc = check_combine(m, tokens, slots, cols, who)) return rc;
+  if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16))
+    return fail(NF4_ERR_ALIGN, "%s: dout, y and dy must be 16-byte aligned", who);
+  if (!aligned(position, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
+    return fail(NF4_ERR_ALIGN, "%s: position, weights and dweights must be 4-byte aligned", who);
+  if (int rc = check_device()) return rc;
+  return launched(nf4i::launch_expert_combine_backward(static_cast<const uint16_t*>(dout), static_cast<const uint16_t*>(y),
+                                                       m, position, tokens, slots, cols, weights,
+                                                       static_cast<uint16_t*>(dy), dweights, as_stream(stream)),
+                  who);
+}
+
+// ---- uniform 4-bit weights with group scales
+
+int nf4_int4_quantize(const void* x, int x_dtype, const nf4_int4_weight* w, void* stream) {
+  const char* who = "nf4_int4_quantize";
+  nf4i::Int4Weight iw{};
+  if (int rc = check_int4(w, &iw, who)) return rc;
+  if (!x) return fail(NF4_ERR_NULL, "%s: x is NULL", who);
+  if (!known_dtype(x_dtype)) return fail(NF4_ERR_DTYPE, "%s: x_dtype %d unknown", who, x_dtype);
+  if (!aligned(x, 16)) return fail(NF4_ERR_ALIGN, "%s: x must be 16-byte aligned", who);
+  if (int rc = check_device()) return rc;
+  return launched(nf4i::launch_int4_quantize(x, x_dtype, iw.rows * iw.cols, iw.group, const_cast<uint8_t*>(iw.packed),
+                                             const_cast<void*>(iw.scales), iw.scale_type,
+                                             const_cast<uint8_t*>(iw.zeros), as_stream(stream)),
+                  who);
+}
+
+int nf4_int4_dequantize(const nf4_int4_weight* w, void* out, int out_dtype, void* stream) {
+  const char* who = "nf4_int4_dequantize";
+  nf4i::Int4Weight iw{};
+  if (int rc = check_int4(w, &iw, who)) return rc;
+  if (!out) return fail(NF4_ERR_NULL, "%s: out is NULL", who);
+  if (!known_dtype(out_dtype)) return fail(NF4_ERR_DTYPE, "%s: out_dtype %d unknown", who, out_dtype);
+  if (!aligned(out, 16)) return fail(NF4_ERR_ALIGN, "%s: out must be 16-byte aligned", who);
+  if (int rc = check_device()) return rc;
+  return launched(nf4i::launch_int4_dequantize(iw, out, out_dtype, as_stream(stream)), who);
+}
+
+int nf4_int4_gemv(const nf4_int4_weight* w, const void* x, int x_dtype, int64_t m, void* y, int y_dtype, void* stream) {
+  const char* who = "nf4_int4_gemv";
+  nf4i::Int4Weight iw{};
+  if (int rc = check_int4(w, &iw, who)) return rc;
+  if (!x || !y) return fail(NF4_ERR_NULL, "%s: x and y are required", who);
+  if (m < 1 || m > 16) return fail(NF4_ERR_SIZE, "%s: m = %lld out of range 1..16", who, (long long)m);
+  if (x_dtype != NF4_BF16 && x_dtype != NF4_F16) return fail(NF4_ERR_DTYPE, "%s: x_dtype %d is not NF4_BF16 or NF4_F16", who, x_dtype);
+  if (!known_dtype(y_dtype)) return fail(NF4_ERR_DTYPE, "%s: y_dtype %d unknown", who, y_dtype);
+  if (!aligned(x, 16) || !aligned(y, 16)) return fail(NF4_ERR_ALIGN, "%s: x and y must be 16-byte aligned", who);
+  if (int rc = check_device()) return rc;
+  return launched(nf4i::launch_int4_gemv(iw, static_cast<const uint16_t*>(x), x_dtype == NF4_F16, m, y, y_dtype,
+                                         as_stream(stream)),
+                  who);
 }
 
 }  // extern "C"

@@ -1,0 +1,76 @@
+// Which expert a tile of the grouped products belongs to.  The rows of expert
+// e are offsets[e] .. offsets[e + 1] - 1 (device data), cut into tiles of TM
+// rows; tiles are numbered expert by expert.  Offsets are clamped to 0 .. m
+// and to ascend, so that no offset makes a kernel leave its buffers.
+#pragma once
+
+#include "nf4_device.h"
+
+namespace nf4i {
+
+struct ExpertTile {
+  int e;            // expert, -1: no such tile
+  int64_t lo, hi;   // its rows
+  int64_t row0;     // the tile's first row
+};
+
+// Tiles of the experts 64 c .. 64 c + 63, one expert per lane.
+struct ExpertLane {
+  int64_t lo, hi;
+  int tiles;        // this lane's expert
+  int upto;         // of lanes 0 .. this
+};
+
+__device__ __forceinline__ ExpertLane expert_lane(const ExpertRows& er, int c, int tm, int lane) {
+  ExpertLane r;
+  const int e = 64 * c + lane;
+  const int64_t a = er.offsets[e < er.experts ? e : er.experts];
+  const int64_t b = er.offsets[e < er.experts ? e + 1 : er.experts];
+  r.lo = a < 0 ? 0 : a < er.m ? a : er.m;
+  r.hi = b < r.lo ? r.lo : b < er.m ? b : er.m;
+  r.tiles = static_cast<int>((r.hi - r.lo + tm - 1) / tm);
+  int s = r.tiles;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int t = __shfl_up(s, off, 64);
+    if (lane >= off) s += t;
+  }
+  r.upto = s;
+  return r;
+}
+
+// All tiles of tm rows.  Every lane of a wave calls this (and the next).
+__device__ __forceinline__ int expert_tiles(const ExpertRows& er, int tm, int lane) {
+  int n = 0;
+  for (int c = 0; 64 * c < er.experts; ++c) n += __builtin_amdgcn_readlane(expert_lane(er, c, tm, lane).upto, 63);
+  return n;
+}
+
+__device__ __forceinline__ ExpertTile find_expert_tile(const ExpertRows& er, int tm, int tile, int lane) {
+  ExpertTile t{-1, 0, 0, 0};
+  int before = 0;
+  for (int c = 0; 64 * c < er.experts; ++c) {
+    const ExpertLane r = expert_lane(er, c, tm, lane);
+    const int here = __builtin_amdgcn_readlane(r.upto, 63);
+    if (tile < before + here) {
+      const int l = __builtin_ctzll(__ballot(before + r.upto > tile));
+      t.e = 64 * c + l;
+      t.lo = __builtin_amdgcn_readlane(static_cast<int>(r.lo), l);
+      t.hi = __builtin_amdgcn_readlane(static_cast<int>(r.hi), l);
+      t.row0 = t.lo + static_cast<int64_t>(tile - before - (__builtin_amdgcn_readlane(r.upto, l) - __builtin_amdgcn_readlane(r.tiles, l))) * tm;
+      return t;
+    }
+    before += here;
+  }
+  return t;
+}
+
+// Unit u of n dealt round-robin over the 8 XCDs (as workgroups are): each XCD
+// gets one contiguous run of the units, so that the units it works on at one
+// time are neighbours.
+__device__ __forceinline__ int64_t xcd_run(int64_t u, int64_t n) {
+  const int64_t x = u & 7, q = n >> 3, r = n & 7;
+  return x * q + (x < r ? x : r) + (u >> 3);
+}
+
+}  // namespace nf4i

@@ -46,8 +46,8 @@ struct ActPtrs {
 };
 
 // Global piece index (0..7: reduction indices 8 p .. 8 p + 7 of the step)
-// that the lane's instruction i reads.
-__device__ __forceinline__ int act_piece(int i, int lane) { return (lane & 7) ^ (((8 * i + (lane >> 3)) >> 1) & 7); }
+// that a lane reads for tile rows 8 r8 .. 8 r8 + 7.
+__device__ __forceinline__ int act_piece(int r8, int lane) { return (lane & 7) ^ (((8 * r8 + (lane >> 3)) >> 1) & 7); }
 
 // act: bf16 [m][ld]; the tile's rows start at m0.  Offsets are 32-bit:
 // 256 * ld * 2 < 2^32 (ld < 2^23).
@@ -61,7 +61,7 @@ __device__ __forceinline__ ActPtrs<P> make_act_ptrs(const uint16_t* act, int64_t
   for (int i = 0; i < P; ++i) {
     const int tr = 8 * (P * wave + i) + (lane >> 3);  // tile row
     const int rc = tr < last ? tr : last;
-    p.off[i] = static_cast<uint32_t>(rc) * static_cast<uint32_t>(ld * 2) + (static_cast<uint32_t>(act_piece(i, lane)) << 4);
+    p.off[i] = static_cast<uint32_t>(rc) * static_cast<uint32_t>(ld * 2) + (static_cast<uint32_t>(act_piece(P * wave + i, lane)) << 4);
   }
   return p;
 }

@@ -46,17 +46,15 @@
 // more K steps: the x side through the same staged tile, the W side
 // [B | B | 0] (laid out row by row in the workspace by k_lora_bx) loaded
 // straight into fragments.
-#include "gemm_tiles.h"
+#include "gemm_fwd.h"
 
 namespace nf4i {
 namespace {
 
-using gt::bf16_pair;
 using gt::bf16x8;
 using gt::floatx16;
+using gt::kCopies;
 using gt::kThreads;
-using gt::lds_frag;
-using gt::u32x4;
 
 constexpr int kBN = gt::kTileN, kBK = gt::kStep;
 // The configuration the launcher uses: 256-row tiles and 32 copies of the
@@ -64,7 +62,6 @@ constexpr int kBN = gt::kTileN, kBK = gt::kStep;
 // (128-row tiles with two workgroups per compute unit measured slower: each
 // weight tile is then expanded for half as many rows.)
 constexpr int kMI = 8;
-constexpr int kCopies = 32;
 constexpr int kWgPerCu = 1;
 constexpr int kBM = 32 * kMI;
 constexpr int kStageBytes = gt::act_stage_bytes<kBM>();
@@ -84,112 +81,15 @@ struct GemmArgs {
   Codebook cb;
 };
 
-// The 256 level pairs (element 2j = high nibble first), C interleaved copies:
-// entry e of copy c at byte e * 8 C + c * 8.  Ends with a barrier.
-template <int C>
-__device__ __forceinline__ void fill_level_pairs(float2* tab, const Codebook& cb) {
-  if (threadIdx.x < 256) {
-    const int e = threadIdx.x;
-    const float2 v = make_float2(cb.level[e >> 4], cb.level[e & 15]);
-#pragma unroll
-    for (int c = 0; c < C; ++c) tab[e * C + c] = v;
-  }
-  __syncthreads();
-}
-
-// The codes a lane expands in one K step: for its two W rows (j = 0, 1) the
-// 16 bytes of columns 32 h .. 32 h + 31, and the rows' block scale inputs.
-struct WRegs {
-  u32x4 w[2];
-  float am[2];   // absmax (plain scales)
-  int q[2];      // int8 scale code (double quant)
-  float s2[2];
-};
-
-struct WPtrs {
-  const uint8_t* c[2];    // codes of row j at step 0, lane half's 16 bytes
-  int64_t blk[2];         // block index of row j at step 0
-};
-
-template <bool kDQ>
-__device__ __forceinline__ void load_w(WRegs& r, const WPtrs& p, const GemmArgs& a, int64_t ks) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    r.w[j] = *reinterpret_cast<const u32x4*>(p.c[j] + ks * (kBK / 2));
-    const int64_t blk = p.blk[j] + ks;
-    if constexpr (kDQ) {
-      r.q[j] = a.sc.q[blk];
-      r.s2[j] = a.sc.absmax2[blk >> 8];
-    } else {
-      r.am[j] = a.sc.absmax[blk];
-    }
-  }
-}
-
-// Level pairs of code bytes 4 s .. 4 s + 3 of a lane's 16 bytes (one k step
-// of one W row): four LDS reads.  The byte permute puts the code byte at
-// bits 8..15 next to the lane's slot; a shift scales it to the entry size
-// 8 C (slot = (lane % C) << (8 - log2 C)).
-struct Lookups {
-  float2 l[2][4];
-};
-
-template <int C>
-__device__ __forceinline__ void lookup_step(Lookups& lk, const u32x4 (&w)[2], int s, const char* tab,
-                                            uint32_t slot) {
-  constexpr int kShift = C == 32 ? 0 : C == 16 ? 1 : 2;
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const uint32_t addr = __builtin_amdgcn_perm(w[j][s], slot, 0x0C0C0000u | ((4u + b) << 8)) >> kShift;
-      lk.l[j][b] = *reinterpret_cast<const float2*>(tab + addr);
-    }
-}
-
-// Each level times the block scale, each pair rounded once to bf16.
-__device__ __forceinline__ bf16x8 expand_frag(const float2 (&l)[4], float sa) {
-  const u32x4 v = {bf16_pair(l[0].x * sa, l[0].y * sa), bf16_pair(l[1].x * sa, l[1].y * sa),
-                   bf16_pair(l[2].x * sa, l[2].y * sa), bf16_pair(l[3].x * sa, l[3].y * sa)};
-  return __builtin_bit_cast(bf16x8, v);
-}
-
-// Spreads the work issued next to the MFMAs of one 16-wide k step between
-// them: per MFMA V VALU operations and L LDS accesses.
-template <int N, int V, int L>
-__device__ __forceinline__ void mfma_interleave() {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
-    __builtin_amdgcn_sched_group_barrier(0x002, V, 0);  // VALU
-    __builtin_amdgcn_sched_group_barrier(0x080, L, 0);  // LDS read or write
-  }
-}
-
-// The scale form is a template parameter (plain, int8, float8): a runtime
-// choice would put a global-memory table load behind a branch, and the wait
-// the compiler places after it would also wait for the next step's loads.
-template <bool kDQ, bool kF8>
-__device__ __forceinline__ void block_scales(const WRegs& wr, float mean, float (&sa)[2]) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if constexpr (kDQ) sa[j] = (code_ratio(wr.q[j], kF8 ? 1 : 0) * wr.s2[j]) + mean;  // a_hat, three roundings
-    else sa[j] = wr.am[j];
-  }
-}
-
 // One work unit: the (32 MI) x 256 tile of y at rows m0.., columns n0..
 // (MI = 8: a whole tile; MI = 4: half of one).  Every LDS stage read here is
 // read before a barrier that all waves pass before the unit returns.
 template <int MI, bool kDQ, bool kF8>
 __device__ __forceinline__ void gemm_unit(const GemmArgs& a, int64_t m0, int64_t n0, char* xs0, char* xs1,
                                           const char* tabc, uint32_t slot, float mean, int wave, int lane) {
-  // Per MFMA: the expansion and lookups of the next 16-wide k step are the
-  // same for both tile heights, spread over 2 MI MFMAs.
-  constexpr int kV = MI == 8 ? 3 : 6, kL = MI == 8 ? 1 : 2;
   const int64_t nk = a.cols / kBK;
   const gt::ActPtrs<MI> xp = gt::make_act_ptrs<MI, 32 * MI>(a.x, a.cols, a.m, m0, wave, lane);
-  WPtrs wp;
+  gt::WPtrs wp;
   int64_t nrow[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -202,74 +102,12 @@ __device__ __forceinline__ void gemm_unit(const GemmArgs& a, int64_t m0, int64_t
   floatx16 acc[MI][2];
   gt::zero_acc(acc);
 
-  // K step k: MFMAs from x stage k % 2 and the codes of step k (wc), in
-  // four 16-wide k steps s.  Software pipeline: while the MFMAs of s run,
-  // the wave expands the B fragments of s + 1 (looked up one k step
-  // earlier) and issues the LDS reads of s + 2; during s = 3 it expands
-  // the next step's s = 0, so that after the barrier the MFMAs can start at
-  // once.  The global loads of step k + 1 (clamped on the last step: x to
-  // the other stage, codes to registers) go out at the top of step k.
-  WRegs wc, wnx;
-  gt::dma_act(xp, 0, xs0, wave);
-  load_w<kDQ>(wc, wp, a, 0);
-  float sa[2];
-  bf16x8 bf[2][2];
-  Lookups lk[3];
-  bf16x8 af[3][MI];
-  const uint32_t sw = ((lane & 31) >> 1) & 7, h4 = (lane >> 5) * 4;
-  block_scales<kDQ, kF8>(wc, mean, sa);
-  lookup_step<kCopies>(lk[0], wc.w, 0, tabc, slot);
-  bf[0][0] = expand_frag(lk[0].l[0], sa[0]);
-  bf[0][1] = expand_frag(lk[0].l[1], sa[1]);
-  gt::wait_vmem();
-  __syncthreads();
-  for (int64_t ks = 0; ks < nk; ++ks) {
-    const int64_t kn = ks + 1 < nk ? ks + 1 : ks;
-    gt::dma_act(xp, kn, (ks & 1) ? xs0 : xs1, wave);  // the other stage was last read before the previous barrier
-    load_w<kDQ>(wnx, wp, a, kn);
-    __builtin_amdgcn_sched_barrier(0);
-    const char* xa = ((ks & 1) ? xs1 : xs0) + (lane & 31) * gt::kActRowBytes;
-    gt::read_act(xa, 0, sw, h4, af[0]);
-    gt::read_act(xa, 1, sw, h4, af[1]);
-    lookup_step<kCopies>(lk[1], wc.w, 1, tabc, slot);
-    __builtin_amdgcn_sched_barrier(0);
-    // s = 0
-    gt::mfma16(af[0], bf[0], acc);
-    bf[1][0] = expand_frag(lk[1].l[0], sa[0]);
-    bf[1][1] = expand_frag(lk[1].l[1], sa[1]);
-    gt::read_act(xa, 2, sw, h4, af[2]);
-    lookup_step<kCopies>(lk[2], wc.w, 2, tabc, slot);
-    mfma_interleave<2 * MI, kV, kL>();
-    __builtin_amdgcn_sched_barrier(0);
-    // s = 1
-    gt::mfma16(af[1], bf[1], acc);
-    bf[0][0] = expand_frag(lk[2].l[0], sa[0]);
-    bf[0][1] = expand_frag(lk[2].l[1], sa[1]);
-    gt::read_act(xa, 3, sw, h4, af[0]);
-    lookup_step<kCopies>(lk[0], wc.w, 3, tabc, slot);
-    mfma_interleave<2 * MI, kV, kL>();
-    __builtin_amdgcn_sched_barrier(0);
-    // s = 2
-    gt::mfma16(af[2], bf[0], acc);
-    bf[1][0] = expand_frag(lk[0].l[0], sa[0]);
-    bf[1][1] = expand_frag(lk[0].l[1], sa[1]);
-    mfma_interleave<2 * MI, kV, kL>();
-    __builtin_amdgcn_sched_barrier(0);
-    // s = 3, with the next step's s = 0 expansion
-    gt::mfma16(af[0], bf[1], acc);
-    block_scales<kDQ, kF8>(wnx, mean, sa);
-    lookup_step<kCopies>(lk[1], wnx.w, 0, tabc, slot);
-    bf[0][0] = expand_frag(lk[1].l[0], sa[0]);
-    bf[0][1] = expand_frag(lk[1].l[1], sa[1]);
-    mfma_interleave<2 * MI, kV, kL>();
-    __builtin_amdgcn_sched_barrier(0);
-    gt::wait_vmem();
-    __syncthreads();
-    wc = wnx;
-  }
+  gt::fwd_steps<MI, kDQ, kF8>(
+      a.sc, nk, [&](int64_t ks, char* stage) { gt::dma_act(xp, ks, stage, wave); }, wp, xs0, xs1, tabc, slot, mean, lane, acc);
   if (a.kl > 0) {
     // LoRA K steps: u through the x stage, [B | B | 0] rows straight into fragments
     const gt::ActPtrs<MI> up = gt::make_act_ptrs<MI, 32 * MI>(a.u, a.kl, a.m, m0, wave, lane);
+    const uint32_t sw = ((lane & 31) >> 1) & 7, h4 = (lane >> 5) * 4;
     for (int64_t k0 = 0; k0 < a.kl; k0 += kBK) {
       gt::dma_act(up, k0 / kBK, xs0, wave);  // xs0 was last read before the previous barrier
       bf16x8 bl[4][2];
@@ -283,8 +121,9 @@ __device__ __forceinline__ void gemm_unit(const GemmArgs& a, int64_t m0, int64_t
       const char* xa = xs0 + (lane & 31) * gt::kActRowBytes;
 #pragma unroll
       for (int s4 = 0; s4 < 4; ++s4) {
-        gt::read_act(xa, s4, sw, h4, af[0]);
-        gt::mfma16(af[0], bl[s4], acc);
+        bf16x8 af[MI];
+        gt::read_act(xa, s4, sw, h4, af);
+        gt::mfma16(af, bl[s4], acc);
       }
       __syncthreads();
     }
@@ -304,7 +143,7 @@ __global__ __launch_bounds__(kThreads, kWgPerCu) void k_gemm(GemmArgs a) {
   constexpr int kShift = kCopies == 32 ? 0 : kCopies == 16 ? 1 : 2;
   const uint32_t slot = static_cast<uint32_t>(lane & (kCopies - 1)) << (3 + kShift);
 
-  fill_level_pairs<kCopies>(tab, a.cb);  // once per workgroup; ends with a barrier
+  gt::fill_level_pairs<kCopies>(tab, a.cb);  // once per workgroup; ends with a barrier
   const float mean = kDQ ? *a.sc.mean : 0.0f;
   const int64_t tiles_n = (a.rows + kBN - 1) / kBN;
   const int64_t tiles = tiles_n * ((a.m + kBM - 1) / kBM);

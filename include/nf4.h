@@ -373,6 +373,129 @@ int nf4_lora_grads(const void* x, const void* dy, int64_t m, int64_t rows, int64
 int nf4_lora_merge(const nf4_weight* w, const void* lora_a, const void* lora_b, int32_t r,
                    float lora_scale, void* out, int out_dtype, void* stream);
 
+/* ------------------------------------------------- mixture-of-experts products
+ *
+ * A mixture-of-experts layer sends each token to `slots` of its experts.
+ * Slot t * slots + j is the j-th choice of token t.  The products take the
+ * slots sorted by expert: nf4_expert_plan sorts them, nf4_expert_gemm and
+ * nf4_expert_gemm_dx multiply each expert's rows by its weight, and
+ * nf4_expert_combine adds a token's rows up again.  No row count reaches the
+ * host, so the calls can be captured into a graph.
+ *
+ * The weights of the experts are ONE nf4_weight, stacked along the rows: expert
+ * e is rows e * R .. (e + 1) * R - 1 with R = w->rows / experts (quantize the
+ * [experts * R][cols] matrix; the second level of the scales is then common).
+ * offsets[e] .. offsets[e + 1] - 1 are the product's rows of expert e; offsets
+ * outside 0 .. m or descending are clamped.  Rows of the outputs that belong
+ * to no expert are left as they were. */
+
+#define NF4_MAX_EXPERTS 1024
+
+/* Bytes of device workspace nf4_expert_plan needs (0 for few slots and for
+ * sizes out of range). */
+size_t nf4_expert_plan_workspace(int64_t n, int32_t experts);
+
+/* The plan: a stable sort of n slots by expert.
+ *   ids      : n expert numbers, 1 <= n < 2^31; one outside 0 .. experts - 1
+ *              drops its slot (padding).  1 <= experts <= NF4_MAX_EXPERTS.
+ *   order    : out, n int32: the slot at each sorted row, ascending within an
+ *              expert; -1 past the last kept one.
+ *   position : out, n int32: the sorted row of each slot, -1 where dropped.
+ *   offsets  : out, experts + 1 int32.
+ *   workspace: at least nf4_expert_plan_workspace(n, experts) bytes, 4-byte
+ *              aligned (may be NULL when that is 0); overwritten.
+ * All arrays 4-byte aligned, not overlapping. */
+int nf4_expert_plan(const int32_t* ids, int64_t n, int32_t experts, int32_t* order, int32_t* position,
+                    int32_t* offsets, void* workspace, size_t workspace_bytes, void* stream);
+
+/* y[p] = x[row(p)] . deq(W_e)^T for the rows p of every expert e.
+ *   w      : the stacked weight (any scale form and code book); w->rows a
+ *            multiple of experts, cols % 64 == 0, cols < 2^23.
+ *   x      : bf16 [x_rows][cols], 16-byte aligned, 1 <= x_rows <= 2^31.
+ *   index  : NULL (row(p) = p; x_rows >= m), or m int32: row(p) =
+ *            index[p] / slots (the plan's order and the number of slots of a
+ *            token), clamped to x's rows.  slots >= 1.
+ *   offsets: experts + 1 int32.
+ *   m      : rows of y, 1 <= m < 2^31.
+ *   y      : bf16 [m][R], 16-byte aligned, not overlapping any input.
+ * Sums are float32, y is rounded once to bf16.  For a mean of many rows per
+ * expert the weight is rounded once to bf16 after scaling, as in nf4_gemm; for
+ * few rows per expert the levels are carried as two bf16 parts and the scale
+ * is applied in float32. */
+int nf4_expert_gemm(const nf4_weight* w, int32_t experts, const void* x, int64_t x_rows, const int32_t* index,
+                    int32_t slots, const int32_t* offsets, int64_t m, void* y, void* stream);
+
+/* dx[p] = dy[p] . deq(W_e): the input gradient of nf4_expert_gemm for the rows
+ * p of every expert e (the weights are frozen).
+ *   w      : as there, and R % 8 == 0, R < 2^23.
+ *   dy     : bf16 [m][R], 16-byte aligned;  dx: bf16 [m][cols], 16-byte
+ *            aligned, not overlapping dy.  1 <= m < 2^31.
+ * The gradient of a gathered x is the sum of its slots' rows:
+ * nf4_expert_combine of dx without weights.  The weight is rounded once to bf16
+ * after scaling, sums are float32, dx is rounded once to bf16. */
+int nf4_expert_gemm_dx(const nf4_weight* w, int32_t experts, const void* dy, const int32_t* offsets, int64_t m,
+                       void* dx, void* stream);
+
+/* out[t] = sum_j weights[t][j] . y[position[t][j]], in float32 in the order of
+ * j, rounded once to bf16.
+ *   y       : bf16 [m][cols], 16-byte aligned, 1 <= m < 2^31; cols % 8 == 0.
+ *   position: int32 [tokens][slots], 1 <= tokens * slots < 2^31; a position
+ *             outside 0 .. m - 1 adds nothing (a dropped slot).
+ *   weights : float32 [tokens][slots], or NULL for ones.
+ *   out     : bf16 [tokens][cols], 16-byte aligned, not overlapping y. */
+int nf4_expert_combine(const void* y, int64_t m, const int32_t* position, int64_t tokens, int32_t slots, int64_t cols,
+                       const float* weights, void* out, void* stream);
+
+/* The gradients of nf4_expert_combine for dout, the gradient of its out:
+ *   dy[position[t][j]] = weights[t][j] . dout[t]   (rounded once to bf16)
+ *   dweights[t][j]     = <dout[t], y[position[t][j]]>   (float32; 0 if dropped)
+ *   dout    : bf16 [tokens][cols]; y, dy: bf16 [m][cols]; all 16-byte aligned.
+ *             Rows of dy that no position names are left as they were; a row
+ *             is named at most once (as nf4_expert_plan's positions are).
+ *   dy, dweights: either may be NULL to skip it, not both; y may be NULL
+ *             when dweights is.  dy does not overlap the inputs. */
+int nf4_expert_combine_backward(const void* dout, const void* y, int64_t m, const int32_t* position, int64_t tokens,
+                                int32_t slots, int64_t cols, const float* weights, void* dy, float* dweights,
+                                void* stream);
+
+/* ------------------------------------ uniform 4-bit weights with group scales
+ *
+ * The other common 4-bit weight: integer codes 0 .. 15 with a scale, and often
+ * a zero point, per group of 32, 64 or 128 consecutive columns of a row:
+ *   W[r][c] = (q[r][c] - z[r][c / group]) . s[r][c / group],  z = 8 without zeros. */
+typedef struct nf4_int4_weight {
+  const uint8_t* packed;  /* rows*cols/2 bytes, 16-byte aligned: element 2j of the row-major
+                             matrix in bits 7..4 of byte j, element 2j+1 in bits 3..0       */
+  int64_t rows, cols;     /* rows >= 1; cols a positive multiple of group                   */
+  int32_t group;          /* 32, 64 or 128                                                  */
+  int32_t scale_dtype;    /* NF4_F32, NF4_BF16 or NF4_F16                                   */
+  const void* scales;     /* [rows][cols/group] of scale_dtype, aligned to its type         */
+  const uint8_t* zeros;   /* [rows][cols/group] bytes, or NULL: 8 everywhere                */
+} nf4_int4_weight;
+
+/* Quantization to that form.  The struct's packed, scales and zeros are the
+ * OUTPUTS; zeros == NULL asks for symmetric codes.  x: rows*cols values of
+ * x_dtype (NF4_F32, NF4_BF16 or NF4_F16), 16-byte aligned.  Per group, in float32:
+ *   symmetric : s = rnd(max|x| / 7), q = clamp(rint(x / s) + 8, 0, 15)
+ *   asymmetric: lo = min(0, min x), hi = max(0, max x), s = rnd((hi - lo) / 15),
+ *               z = clamp(rint(-lo / s), 0, 15), q = clamp(rint(x / s) + z, 0, 15)
+ * with rnd() the rounding to scale_dtype (to nearest even; a float16 scale
+ * saturates at 65504), IEEE divisions and rint() to even.  A group whose s is
+ * 0 gets q = z (z = 0 where asymmetric). */
+int nf4_int4_quantize(const void* x, int x_dtype, const nf4_int4_weight* w, void* stream);
+
+/* out[r][c] = (q - z) . s: the product in float32, rounded once to out_dtype
+ * (NF4_F32, NF4_BF16 or NF4_F16).  out: rows*cols values, 16-byte aligned. */
+int nf4_int4_dequantize(const nf4_int4_weight* w, void* out, int out_dtype, void* stream);
+
+/* y = x . W^T for 1 <= m <= 16 rows: the decode product.
+ *   x : [m][cols] of x_dtype (NF4_BF16 or NF4_F16), 16-byte aligned.
+ *   y : [m][rows] of y_dtype (NF4_F32, NF4_BF16 or NF4_F16), 16-byte aligned,
+ *       not overlapping any input.
+ * The codes enter the products exactly; scales and zero points are applied to
+ * the groups' sums in float32; y is rounded once. */
+int nf4_int4_gemv(const nf4_int4_weight* w, const void* x, int x_dtype, int64_t m, void* y, int y_dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
