@@ -655,6 +655,7 @@ int nf4_int4_gemv(const nf4_int4_weight* w, const void* x, int x_dtype, int64_t 
   if (int rc = check_int4(w, &iw, who)) return rc;
   if (!x || !y) return fail(NF4_ERR_NULL, "%s: x and y are required", who);
   if (m < 1 || m > 16) return fail(NF4_ERR_SIZE, "%s: m = %lld out of range 1..16", who, (long long)m);
+  if (iw.cols >= (int64_t(1) << 23)) return fail(NF4_ERR_SIZE, "%s: cols = %lld out of range", who, (long long)iw.cols);
   if (x_dtype != NF4_BF16 && x_dtype != NF4_F16) return fail(NF4_ERR_DTYPE, "%s: x_dtype %d is not NF4_BF16 or NF4_F16", who, x_dtype);
   if (!known_dtype(y_dtype)) return fail(NF4_ERR_DTYPE, "%s: y_dtype %d unknown", who, y_dtype);
   if (!aligned(x, 16) || !aligned(y, 16)) return fail(NF4_ERR_ALIGN, "%s: x and y must be 16-byte aligned", who);

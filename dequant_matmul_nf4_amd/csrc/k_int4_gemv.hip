@@ -57,13 +57,13 @@ __device__ __forceinline__ u32x4 pair_order(const u32x4& v) {
                __builtin_amdgcn_perm(v[3], v[1], 0x07060302u), __builtin_amdgcn_perm(v[3], v[1], 0x05040100u)};
 }
 
-// A scale as it is stored (converted where it is used, so that the load stays in flight).
-__device__ __forceinline__ uint32_t scale_bits(const void* p, int type, int64_t i) {
-  return type == 0 ? static_cast<const uint32_t*>(p)[i] : static_cast<const uint16_t*>(p)[i];
-}
+// The value of a scale as it is stored (converted where it is used, so that
+// its load stays in flight).
+template <bool kWide>
 __device__ __forceinline__ float scale_value(uint32_t b, int type) {
-  const float f16 = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(b)));
-  return type == 0 ? __uint_as_float(b) : type == 1 ? bf16_to_f32(b) : f16;
+  if constexpr (kWide) return __uint_as_float(b);
+  const float f16 = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(b))), bf16 = bf16_to_f32(b);
+  return type == 1 ? bf16 : f16;
 }
 
 __device__ __forceinline__ void store_y(void* y, int type, int64_t i, float v) {
@@ -72,15 +72,35 @@ __device__ __forceinline__ void store_y(void* y, int type, int64_t i, float v) {
   else static_cast<_Float16*>(y)[i] = static_cast<_Float16>(v);
 }
 
-constexpr int kG = 4;  // groups of 16 rows a wave takes per batch: x is read once for all of them
+// What one step brings: codes, and the scales and zero points that the lane
+// converts (row ln, scale groups g kPer .. of the step) in their stored types: a
+// value widened where it is loaded is waited for there.
+template <bool kWide>
+struct ScaleBits { typedef uint16_t type; };
+template <>
+struct ScaleBits<true> { typedef uint32_t type; };
 
-// kGrp: columns per scale.
-template <bool kF16, int kGrp>
-__global__ __launch_bounds__(sk::kThreads) void k_int4_gemv(Int4Args a) {
+template <int kPer, bool kWide>
+struct Step {
+  Codes codes;
+  typename ScaleBits<kWide>::type s[kPer];
+  uint8_t z[kPer];
+};
+
+// kGrp: columns per scale; kWide: float32 scales; kG: groups of 16 rows a wave
+// takes per batch, x being read once for all of them; kOnce: a wave's columns
+// are one segment, whose x is read once for all batches.  In batches of two the
+// next segment's x is on its way while this one is multiplied, where the
+// registers allow it.
+template <bool kF16, int kGrp, bool kWide, int kG, bool kOnce>
+__global__ __launch_bounds__(sk::kThreads, 2) void k_int4_gemv(Int4Args a) {
   constexpr int kPw = kGrp / 32;        // code words a lane takes per scale group
   constexpr int kNs = kSeg / kGrp;      // scale groups per step
+  constexpr int kPer = kNs / 4;
+  constexpr bool kAhead = !kOnce && kG == 2 && kGrp >= 64;
   __shared__ __align__(16) char stage_all[kWaves][sk::kStageBytes];
   __shared__ __align__(16) float2 scl_all[kWaves][sk::kRows * kNs];
+  __shared__ __align__(16) floatx4 xsum_all[kWaves][kNs * 4];
   __shared__ __align__(16) floatx4 part[kWaves * kG * 64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -90,93 +110,114 @@ __global__ __launch_bounds__(sk::kThreads) void k_int4_gemv(Int4Args a) {
   const bool live = rw < pl.rs;
   char* stage = stage_all[wave];
   float2* scl = scl_all[wave];
-  const int64_t row_bytes = a.cols / 2, ngrp = a.cols / kGrp;
+  floatx4* xsum = xsum_all[wave];
+  const uint32_t row_bytes = static_cast<uint32_t>(a.cols / 2);
+  const uint32_t ngrp = static_cast<uint32_t>(a.cols / kGrp);
 
+  // the workgroup's groups, counted from its first; rows are left from there
   const int64_t ngroups = (a.rows + 15) / 16;
-  const int64_t gb = ngroups * blockIdx.x / gridDim.x, ge = ngroups * (blockIdx.x + 1) / gridDim.x;
+  const int64_t gb = ngroups * blockIdx.x / gridDim.x;
+  const int ng = static_cast<int>(ngroups * (blockIdx.x + 1) / gridDim.x - gb);
   const int64_t klo = kw * pl.per, khi = klo + pl.per < a.cols ? klo + pl.per : a.cols;
-  const int nseg = static_cast<int>((khi - klo + kSeg - 1) / kSeg);
+  const int kspan = static_cast<int>(khi - klo);
+  const int nseg = (kspan + kSeg - 1) / kSeg;
+  const int64_t rows_left = a.rows - gb * 16;
+  const int tail = static_cast<int>(rows_left - (ng - 1) * 16 < 16 ? rows_left - (ng - 1) * 16 : 16);  // rows of the last group
+  const uint8_t* codes0 = a.packed + gb * 16 * row_bytes + klo / 2;
+  const int64_t scale0 = gb * 16 * ngrp + klo / kGrp;
+  const int64_t group_bytes = int64_t{16} * row_bytes, group_scales = int64_t{16} * ngrp;
+  const sk::CodeLane cl = sk::code_lane(row_bytes, lane);
+  const uint32_t srow = static_cast<uint32_t>(ln) * ngrp + g * kPer;
 
-  Codes codes;
-  uint32_t sc[kNs >= 4 ? kNs / 4 : 1], zp[kNs >= 4 ? kNs / 4 : 1];
-  // The loads of one step; lane (ln, g) takes the scales of row ln, groups g, g + 4, ...
-  auto load_step = [&](int64_t group, int seg) {
-    const int64_t k0 = klo + static_cast<int64_t>(seg) * kSeg;
-    codes = sk::load_codes(a.packed, row_bytes, group * 16, a.rows, k0, khi, lane);
-    const int64_t row = group * 16 + ln < a.rows ? group * 16 + ln : a.rows - 1;
-    const int64_t last = (khi - k0) / kGrp - 1;
+  Step<kPer, kWide> set[2];
+  auto load_step = [&](Step<kPer, kWide>& st, int group, int seg, bool wanted) {
+    const int rows = group == ng - 1 ? tail : 16;
+    const int left = kspan - seg * kSeg;
+    sk::load_codes(st.codes, codes0 + (group * group_bytes + seg * (kSeg / 2)), cl, row_bytes, rows, left / 32, wanted, lane);
+    const int64_t at = scale0 + (group * group_scales + seg * kNs);  // the step's first scale
+    const bool whole = rows == 16 && left >= kSeg;
+    const int lq = (left < kSeg ? left : kSeg) / kGrp - 1;
+    const uint32_t trow = static_cast<uint32_t>(ln < rows ? ln : rows - 1) * ngrp;
 #pragma unroll
-    for (int j = 0; j < (kNs >= 4 ? kNs / 4 : 1); ++j) {
-      int64_t q = kNs >= 4 ? g + 4 * j : (g % kNs);
-      q = q < last ? q : last;
-      const int64_t at = row * ngrp + k0 / kGrp + q;
-      sc[j] = scale_bits(a.scales, a.scale_type, at);
-      zp[j] = a.zeros ? a.zeros[at] : 8u;
+    for (int j = 0; j < kPer; ++j) {
+      const int q = g * kPer + j;
+      const uint32_t o = (whole ? srow + j : trow + (q < lq ? q : lq)) & (wanted ? ~0u : 0u);
+      if constexpr (kWide) st.s[j] = (static_cast<const uint32_t*>(a.scales) + at)[o];
+      else st.s[j] = (static_cast<const uint16_t*>(a.scales) + at)[o];
+      st.z[j] = (a.zeros ? a.zeros + at : a.packed)[o & (a.zeros ? ~0u : 0u)];
     }
   };
 
-  u32x4 xv[kNs][kPw];
-  floatx4 xsum[kNs];
+  // x of a segment: as it is read, and as the operand with the groups' sums
+  u32x4 xn[kNs][kPw], xv[kNs][kPw];
   auto load_x = [&](int seg) {
-    const int64_t k0 = klo + static_cast<int64_t>(seg) * kSeg;
     // rows past m repeat row m - 1: they reach only rows of the result that are not stored
-    const uint16_t* xr = a.x + static_cast<int64_t>(ln < a.m ? ln : a.m - 1) * a.cols;
-    const u32x4 ones = kF16 ? u32x4{0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u}
-                            : u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    const uint16_t* xr = a.x + (static_cast<int64_t>(ln < a.m ? ln : a.m - 1) * a.cols + klo);
 #pragma unroll
     for (int s = 0; s < kNs; ++s)
 #pragma unroll
       for (int u = 0; u < kPw; ++u) {
-        const int64_t k = k0 + s * kGrp + 8 * kPw * g + 8 * u;
-        xv[s][u] = *reinterpret_cast<const u32x4*>(xr + (k < khi ? k : khi - 8));
+        const int k = seg * kSeg + s * kGrp + 8 * kPw * g + 8 * u;
+        xn[s][u] = *reinterpret_cast<const u32x4*>(xr + (k < kspan ? k : kspan - 8));
       }
+  };
+  auto take_x = [&](int seg) {
+    const u32x4 ones = kF16 ? u32x4{0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u}
+                            : u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
     for (int s = 0; s < kNs; ++s) {
-      xsum[s] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+      floatx4 sum = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int u = 0; u < kPw; ++u) {
-        const bool in = k0 + s * kGrp < khi;
-        const u32x4 v = pair_order(xv[s][u]);
+        const bool in = seg * kSeg + s * kGrp < kspan;
+        const u32x4 v = pair_order(xn[s][u]);
         xv[s][u] = u32x4{in ? v[0] : 0u, in ? v[1] : 0u, in ? v[2] : 0u, in ? v[3] : 0u};
-        xsum[s] = sk::mfma<kF16>(xv[s][u], ones, xsum[s]);
+        sum = sk::mfma<kF16>(xv[s][u], ones, sum);
       }
+      xsum[s * 4 + g] = sum;  // the same in the 16 lanes of g
     }
   };
 
-  int have = -1;  // the segment whose x is held
-  if (live && gb + rw < ge) load_step(gb + rw, 0);
-  for (int64_t base = gb; base < ge; base += static_cast<int64_t>(pl.rs) * kG) {
+  // Position p of a wave's walk is group p % kG of segment p / kG of the batch.
+  // Two steps are on their way at any time, in the two register sets by the
+  // parity of p; a position past the workgroup's groups is not multiplied.
+  const int batch = pl.rs * kG;
+  auto load_at = [&](Step<kPer, kWide>& st, int base, int seg, int gi) {
+    if (seg >= nseg) {
+      seg -= nseg;
+      base += batch;
+    }
+    const int group = base + gi * pl.rs + rw;
+    load_step(st, group < ng ? group : ng - 1, seg, group < ng);
+  };
+  if constexpr (kOnce || kAhead) load_x(0);
+  load_at(set[0], 0, 0, 0);
+  load_at(set[1], 0, 0, 1);
+  if constexpr (kOnce) take_x(0);
+  for (int base = 0; base < ng; base += batch) {
     floatx4 acc[kG];
 #pragma unroll
     for (int i = 0; i < kG; ++i) acc[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     for (int seg = 0; live && seg < nseg; ++seg) {
-      if (seg != have) {
-        load_x(seg);
-        have = seg;
+      if constexpr (!kOnce) {
+        if constexpr (!kAhead) load_x(seg);
+        take_x(seg);
+        if constexpr (kAhead) load_x(seg + 1 < nseg ? seg + 1 : 0);
       }
 #pragma unroll
       for (int gi = 0; gi < kG; ++gi) {
-        const int64_t group = base + static_cast<int64_t>(gi) * pl.rs + rw;
-        if (group >= ge) continue;
-        // this step's codes and scales into LDS, then the next step's loads
-        sk::stage_codes(codes, stage, lane);
+        Step<kPer, kWide>& st = set[gi & 1];
+        const bool here = base + gi * pl.rs + rw < ng;
+        if (here) {
+          // this step's codes and scales into LDS
+          sk::stage_codes(st.codes, stage, lane);
 #pragma unroll
-        for (int j = 0; j < (kNs >= 4 ? kNs / 4 : 1); ++j) {
-          const int q = kNs >= 4 ? g + 4 * j : (g % kNs);
-          scl[ln * kNs + q] = make_float2(16.0f * scale_value(sc[j], a.scale_type), -1.0f - static_cast<float>(zp[j]) * 0.0625f);
+          for (int j = 0; j < kPer; ++j)
+            scl[ln * kNs + g * kPer + j] =
+                make_float2(16.0f * scale_value<kWide>(st.s[j], a.scale_type), a.zeros ? -1.0f - static_cast<float>(st.z[j]) * 0.0625f : -1.5f);
         }
-        {
-          int64_t ng = group + pl.rs;
-          int ns = seg;
-          if (gi + 1 == kG || ng >= ge) {  // the batch's next segment, or the next batch
-            ng = base + rw;
-            if (++ns == nseg) {
-              ns = 0;
-              ng += static_cast<int64_t>(pl.rs) * kG;
-            }
-          }
-          if (ng < ge) load_step(ng, ns);
-        }
+        load_at(st, base, gi + 2 < kG ? seg : seg + 1, (gi + 2) % kG);
+        if (!here) continue;
         sk::wave_lds_order();
 #pragma unroll
         for (int s = 0; s < kNs; ++s) {
@@ -193,11 +234,12 @@ __global__ __launch_bounds__(sk::kThreads) void k_int4_gemv(Int4Args a) {
             for (int u = 0; u < 4; ++u) w[u] = v[u];
           }
           const float2 f = scl[ln * kNs + s];
+          const floatx4 xs = xsum[s * 4 + g];
           floatx4 d = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int u = 0; u < kPw; ++u) d = sk::mfma<kF16>(xv[s][u], expand<kF16>(w[u]), d);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[gi][i] = fmaf(f.x, fmaf(f.y, xsum[s][i], d[i]), acc[gi][i]);
+          for (int i = 0; i < 4; ++i) acc[gi][i] = fmaf(f.x, fmaf(f.y, xs[i], d[i]), acc[gi][i]);
         }
         sk::wave_lds_order();
       }
@@ -208,13 +250,13 @@ __global__ __launch_bounds__(sk::kThreads) void k_int4_gemv(Int4Args a) {
       for (int gi = 0; gi < kG; ++gi) part[(wave * kG + gi) * 64 + lane] = acc[gi];
     }
     sk::lds_barrier();
-    for (int t = threadIdx.x; t < pl.rs * kG * 64; t += sk::kThreads) {
+    for (int t = threadIdx.x; t < batch * 64; t += sk::kThreads) {
       const int l = t & 63, gi = (t >> 6) % kG, r = (t >> 6) / kG;
-      const int64_t group = base + static_cast<int64_t>(gi) * pl.rs + r;
-      if (group >= ge) continue;
+      const int group = base + gi * pl.rs + r;
+      if (group >= ng) continue;
       floatx4 v = part[(r * pl.ks * kG + gi) * 64 + l];
       for (int k = 1; k < pl.ks; ++k) v += part[((r * pl.ks + k) * kG + gi) * 64 + l];
-      const int64_t row = group * 16 + (l & 15);
+      const int64_t row = (gb + group) * 16 + (l & 15);
       if (row >= a.rows) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -226,6 +268,27 @@ __global__ __launch_bounds__(sk::kThreads) void k_int4_gemv(Int4Args a) {
   }
 }
 
+template <bool kF16, int kGrp, bool kWide>
+void launch(const Int4Args& a, dim3 gd, hipStream_t s) {
+  // A wave's columns in one segment: x is read once and the batch only decides
+  // how often partial tiles are added up.  Otherwise x is read once a batch:
+  // as many groups as a wave has, up to 8 (28672x8192 at m = 16, 7 groups a
+  // wave: 36 us with 8, 44 with 4; 8192x28672, 2 groups: 60 us with 4, 65 with 8).
+  const int64_t groups = (a.rows + 15) / 16, each = groups / (static_cast<int64_t>(gd.x) * a.pl.rs);
+  const dim3 bd(sk::kThreads);
+  if (a.pl.per <= kSeg) hipLaunchKernelGGL((k_int4_gemv<kF16, kGrp, kWide, 4, true>), gd, bd, 0, s, a);
+  else if (each >= 3) hipLaunchKernelGGL((k_int4_gemv<kF16, kGrp, kWide, 8, false>), gd, bd, 0, s, a);
+  else hipLaunchKernelGGL((k_int4_gemv<kF16, kGrp, kWide, 2, false>), gd, bd, 0, s, a);
+}
+
+template <bool kF16>
+void launch(const Int4Args& a, int group, dim3 gd, hipStream_t s) {
+  const bool wide = a.scale_type == 0;
+  if (group == 32) wide ? launch<kF16, 32, true>(a, gd, s) : launch<kF16, 32, false>(a, gd, s);
+  else if (group == 64) wide ? launch<kF16, 64, true>(a, gd, s) : launch<kF16, 64, false>(a, gd, s);
+  else wide ? launch<kF16, 128, true>(a, gd, s) : launch<kF16, 128, false>(a, gd, s);
+}
+
 }  // namespace
 
 hipError_t launch_int4_gemv(const Int4Weight& w, const uint16_t* x, int x_f16, int64_t m, void* y, int y_type,
@@ -233,22 +296,15 @@ hipError_t launch_int4_gemv(const Int4Weight& w, const uint16_t* x, int x_f16, i
   Int4Args a{};
   a.packed = w.packed; a.rows = w.rows; a.cols = w.cols; a.scales = w.scales; a.scale_type = w.scale_type;
   a.zeros = w.zeros; a.x = x; a.m = static_cast<int>(m); a.y = y; a.y_type = y_type;
-  const int64_t groups = (w.rows + 15) / 16;
-  // one workgroup per compute unit, fewer where there are not `rs` groups for each
-  sk::Plan pl = sk::make_plan(w.cols, 0);
-  const int64_t want = (groups + pl.rs - 1) / pl.rs;
-  pl.grid = static_cast<int>(want < device_cus() ? want : device_cus());
-  a.pl = pl;
-  const dim3 gd(static_cast<unsigned>(pl.grid)), bd(sk::kThreads);
-#define NF4_INT4(F16) \
-  do { \
-    if (w.group == 32) hipLaunchKernelGGL((k_int4_gemv<F16, 32>), gd, bd, 0, s, a); \
-    else if (w.group == 64) hipLaunchKernelGGL((k_int4_gemv<F16, 64>), gd, bd, 0, s, a); \
-    else hipLaunchKernelGGL((k_int4_gemv<F16, 128>), gd, bd, 0, s, a); \
-  } while (0)
-  if (x_f16) NF4_INT4(true);
-  else NF4_INT4(false);
-#undef NF4_INT4
+  a.pl = sk::make_plan(w.cols);
+  // one workgroup per compute unit, fewer where there are not `rs` groups for
+  // each; more where a workgroup's groups would not be counted in 31 bits
+  const int64_t groups = (w.rows + 15) / 16, want = (groups + a.pl.rs - 1) / a.pl.rs;
+  int64_t grid = want < device_cus() ? want : device_cus();
+  while (groups / grid >= (int64_t{1} << 26)) grid *= 2;
+  const dim3 gd(static_cast<unsigned>(grid));
+  if (x_f16) launch<true>(a, w.group, gd, s);
+  else launch<false>(a, w.group, gd, s);
   return hipGetLastError();
 }
 

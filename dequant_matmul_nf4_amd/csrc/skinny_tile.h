@@ -3,20 +3,20 @@
 // product of few rows (k_expert_skinny.hip).
 //
 // What bounds it is reading the codes, so everything serves keeping reads in
-// flight: a workgroup of 16 waves (the most its registers allow) cuts the
-// columns over its waves, and a wave walks "steps" of 16 weight rows x 256
-// columns (2 KiB of codes), the codes of the next step on their way while it
-// multiplies this one.
+// flight: a workgroup of 8 waves (one per compute unit, as its registers
+// allow) cuts the columns over its waves, and a wave walks "steps" of 16
+// weight rows x 512 columns (4 KiB of codes), the codes of the next two steps
+// on their way while it multiplies this one.
 //
-// A wave loads a step as 16 pieces of 128 contiguous bytes (a whole line per
-// weight row) and turns it in 2 KiB of LDS of its own into the operand's
+// A wave loads a step as 256 contiguous bytes of each weight row (two whole
+// lines) and turns it in 4 KiB of LDS of its own into the operand's
 // order: the weights are the B operand of v_mfma_f32_16x16x32, so lane
 // (row ln = lane % 16, g = lane / 16) needs 8 values of its row per product.
 // One product spans 32 columns, and the products that share one scale run
 // into an accumulator of their own, to which the scale is then applied in
 // float32: the operands are codes or levels alone, and no scaled weight is
-// rounded.  LDS row r holds 16-byte piece p at slot p ^ ((r / 2) % 8), which
-// spreads the reads of 16 rows over the banks.
+// rounded.  LDS row r holds 16-byte piece p at slot p ^ r, which spreads the
+// reads of 16 rows over the banks.
 //
 // The waves of one group of 16 rows leave their partial tiles in LDS; they are
 // added in wave order, so results do not depend on timing.
@@ -32,11 +32,12 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
 
-constexpr int kWaves = 16;
+constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kSeg = 256;              // columns of a step
+constexpr int kSeg = 512;              // columns of a step
 constexpr int kRows = 16;              // weight rows of a step, and the most rows of x
 constexpr int kStageBytes = kRows * kSeg / 2;
+constexpr int kLoads = kStageBytes / 1024;  // 16-byte loads of a lane per step
 
 // x, weights: 8 values of one type each
 template <bool kF16>
@@ -59,48 +60,73 @@ __device__ __forceinline__ void wave_lds_order() {
 }
 
 __device__ __forceinline__ uint32_t slot_of(int row, int piece) {
-  return static_cast<uint32_t>(row * (kSeg / 2) + ((piece ^ ((row >> 1) & 7)) << 4));
+  return static_cast<uint32_t>(row * (kSeg / 2) + ((piece ^ row) << 4));
 }
 
-// The codes a lane moves per step: rows lane / 8 and 8 + lane / 8 of the
-// group, the 16-byte piece that belongs in slot lane % 8 of each.
+// The codes a lane moves per step: load i takes row 4 i + lane / 16 of the
+// group, the 16-byte piece that belongs in slot lane % 16 of it.
 struct Codes {
-  u32x4 c[2];
+  u32x4 c[kLoads];
 };
 
-// One step's loads: weight rows row0 .. row0 + 15 (clamped to the last row),
-// columns k0 .. k0 + 255 (pieces clamped to the last one before kend; the x
-// operand is zero there).  The codes are read once: non-temporal.
-__device__ __forceinline__ Codes load_codes(const uint8_t* packed, int64_t row_bytes, int64_t row0, int64_t rows,
-                                            int64_t k0, int64_t kend, int lane) {
-  Codes r;
-  const int64_t last = (kend - k0) / 32 - 1;
+__device__ __forceinline__ int code_row(int i, int lane) { return 4 * i + (lane >> 4); }
+__device__ __forceinline__ int code_piece(int i, int lane) { return (lane & 15) ^ code_row(i, lane); }
+
+// The offset of load i from the step's first byte (rows of row_bytes < 2^27
+// bytes).  `rows` and `pieces` are left from there, at least one of each: what
+// lies past the last repeats it (such products meet zeros or are not stored).
+__device__ __forceinline__ uint32_t code_offset(int i, uint32_t row_bytes, int rows, int pieces, int lane) {
+  const int tr = code_row(i, lane), tp = code_piece(i, lane);
+  const uint32_t row = tr < rows ? tr : rows - 1, piece = tp < pieces ? tp : pieces - 1;
+  return row * row_bytes + (piece << 4);
+}
+
+// The offsets of whole steps, kept.
+struct CodeLane {
+  uint32_t off[kLoads];
+};
+
+__device__ __forceinline__ CodeLane code_lane(uint32_t row_bytes, int lane) {
+  CodeLane r;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int tr = 8 * i + (lane >> 3);
-    const int64_t row = row0 + tr < rows ? row0 + tr : rows - 1;
-    int64_t piece = (lane & 7) ^ ((tr >> 1) & 7);
-    piece = piece < last ? piece : last;
-    r.c[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(packed + row * row_bytes + k0 / 2 + piece * 16));
-  }
+  for (int i = 0; i < kLoads; ++i) r.off[i] = code_offset(i, row_bytes, kRows, kSeg / 32, lane);
   return r;
+}
+
+// One step's loads.  They are issued whatever the step (no branch around a
+// load): only then does the compiler know how many loads are younger than the
+// ones it waits for, and waits for no more.  One that is not wanted reads 16
+// bytes.  The codes are read once: non-temporal.
+__device__ __forceinline__ void load_codes(Codes& r, const uint8_t* step, const CodeLane& l, uint32_t row_bytes,
+                                           int rows, int pieces, bool wanted, int lane) {
+  const bool whole = rows >= kRows && pieces >= kSeg / 32;
+  uint32_t off[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) off[i] = l.off[i];
+  if (!whole) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) off[i] = code_offset(i, row_bytes, rows, pieces, lane);
+  }
+  const uint32_t keep = wanted ? ~0u : 0u;
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i)
+    r.c[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(step + (off[i] & keep)));
 }
 
 __device__ __forceinline__ void stage_codes(const Codes& r, char* stage, int lane) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(stage + i * 1024 + lane * 16) = r.c[i];
+  for (int i = 0; i < kLoads; ++i) *reinterpret_cast<u32x4*>(stage + i * 1024 + lane * 16) = r.c[i];
 }
 
 // How a launch cuts its work: `ks` waves share a group's columns, the others
 // take other groups (`rs` groups at a time).
 struct Plan {
   int ks, rs;
-  int64_t per;     // columns of a wave (a multiple of kSeg, except where the row ends)
-  int grid;
+  int64_t per;     // columns of a wave (where the row ends: fewer)
 };
 
-// At least one step per wave; ks * rs <= 16.
-inline Plan make_plan(int64_t cols, int grid) {
+// At least one step per wave; ks * rs <= kWaves.
+inline Plan make_plan(int64_t cols) {
   Plan p{};
   const int64_t nseg = (cols + kSeg - 1) / kSeg;
   p.ks = static_cast<int>(nseg < kWaves ? nseg : kWaves);
@@ -109,7 +135,6 @@ inline Plan make_plan(int64_t cols, int grid) {
   p.per = (units + p.ks - 1) / p.ks * unit;
   p.ks = static_cast<int>((cols + p.per - 1) / p.per);
   p.rs = kWaves / p.ks;
-  p.grid = grid;
   return p;
 }
 

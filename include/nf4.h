@@ -488,7 +488,7 @@ int nf4_int4_quantize(const void* x, int x_dtype, const nf4_int4_weight* w, void
  * (NF4_F32, NF4_BF16 or NF4_F16).  out: rows*cols values, 16-byte aligned. */
 int nf4_int4_dequantize(const nf4_int4_weight* w, void* out, int out_dtype, void* stream);
 
-/* y = x . W^T for 1 <= m <= 16 rows: the decode product.
+/* y = x . W^T for 1 <= m <= 16 rows: the decode product.  cols < 2^23.
  *   x : [m][cols] of x_dtype (NF4_BF16 or NF4_F16), 16-byte aligned.
  *   y : [m][rows] of y_dtype (NF4_F32, NF4_BF16 or NF4_F16), 16-byte aligned,
  *       not overlapping any input.
