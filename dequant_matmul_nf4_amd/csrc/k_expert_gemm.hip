@@ -104,6 +104,7 @@ hipError_t launch(const ExpertGemmArgs& a, hipStream_t s) {
 
 hipError_t launch_expert_gemm(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
                               const ExpertX& ex, uint16_t* y, hipStream_t s) {
+  if (er.m <= 8 * static_cast<int64_t>(er.experts)) return launch_expert_skinny(packed, rows, cols, sc, er, ex, y, s);
   ExpertGemmArgs a{};
   a.packed = packed; a.rows = rows; a.cols = cols; a.sc = sc; a.er = er; a.ex = ex; a.y = y;
   a.cb = codebook(sc.fp4);

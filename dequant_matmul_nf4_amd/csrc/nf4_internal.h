@@ -215,6 +215,9 @@ hipError_t launch_expert_plan(const int32_t* ids, int64_t n, int experts, int32_
                               int32_t* offsets, void* ws, hipStream_t s);
 hipError_t launch_expert_gemm(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
                               const ExpertX& ex, uint16_t* y, hipStream_t s);
+// Its form for few rows per expert.
+hipError_t launch_expert_skinny(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
+                                const ExpertX& ex, uint16_t* y, hipStream_t s);
 hipError_t launch_expert_gemm_dx(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
                                  const uint16_t* dy, uint16_t* dx, hipStream_t s);
 hipError_t launch_expert_combine(const uint16_t* y, int64_t m, const int32_t* position, int64_t tokens, int slots,
