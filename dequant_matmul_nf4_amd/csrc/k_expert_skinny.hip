@@ -8,11 +8,14 @@
 // dealt out evenly, one contiguous run to each workgroup (the row counts are
 // device data, so a workgroup finds its run from the offsets).
 //
-// A byte of codes indexes a table of level pairs in LDS, each level as two
-// bfloat16 parts (hi = round(level), lo = round(level - hi): 16 significant
-// bits), and both parts are multiplied: the matrix cores have time for twice
-// the products.  The sums of a 64-block are scaled in float32.  So nothing but
-// the levels' 2^-17 is rounded before y.
+// A byte of codes indexes a table of level pairs in LDS, rounded to float16 (11
+// significant bits: off by at most 2^-12 of a level), and the sums of a
+// 64-block are scaled in float32, so no scaled weight is rounded to 16 bits.
+// x becomes float16 exactly: a wave scales its columns of a row by the power
+// of two that brings their largest value to [2^14, 2^15) and scales the sums
+// back (values 2^-29 of the largest and below lose bits).  Two bfloat16 parts
+// per level instead were exact to 2^-17 but moved two registers per lookup to
+// line up the operands: 66 us against XX (16 rows over 8 experts of 14336x4096).
 #include "expert_tiles.h"
 #include "skinny_tile.h"
 
@@ -47,12 +50,27 @@ struct Step {
   float s[kPer];
 };
 
+__device__ __forceinline__ uint32_t half_pair(float a, float b) {
+  typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, half2_t{static_cast<_Float16>(a), static_cast<_Float16>(b)});
+}
+
+// The level pairs of a lane's 8 code bytes: one permute puts a byte above the
+// lane's copy, a shift makes that the entry's address (128 bytes per code byte).
+__device__ __forceinline__ void look_up(u32x4 (&t)[2], const uint2& w, const char* tab, uint32_t slot) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t at = __builtin_amdgcn_perm(c < 4 ? w.x : w.y, slot, 0x0C0C0000u | ((4u + (c & 3)) << 8)) >> 1;
+    t[c >> 2][c & 3] = *reinterpret_cast<const uint32_t*>(tab + at);
+  }
+}
+
 // kG: groups of 16 weight rows a wave takes per batch, x being read once for
 // all of them; kOnce: a wave's columns are one segment, whose x is read once
 // per tile.
 template <bool kDQ, bool kF8, int kG, bool kOnce>
 __global__ __launch_bounds__(sk::kThreads, 2) void k_expert_skinny(SkinnyArgs a) {
-  __shared__ __align__(16) uint2 tab[256 * kCopies];
+  __shared__ __align__(16) uint32_t tab[256 * kCopies];
   __shared__ __align__(16) char stage_all[kWaves][sk::kStageBytes];
   __shared__ __align__(16) float scl_all[kWaves][sk::kRows * kNb];
   __shared__ __align__(16) floatx4 part[kWaves * kG * 64];
@@ -71,9 +89,7 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_expert_skinny(SkinnyArgs a)
 
   for (int i = threadIdx.x; i < 256 * kCopies; i += sk::kThreads) {
     const int e = i / kCopies;
-    const float l0 = a.cb.level[e >> 4], l1 = a.cb.level[e & 15];
-    const uint32_t h0 = f32_to_bf16(l0), h1 = f32_to_bf16(l1);
-    tab[i] = make_uint2(h0 | (h1 << 16), pack_bf16x2(l0 - bf16_to_f32(h0), l1 - bf16_to_f32(h1)));
+    tab[i] = half_pair(a.cb.level[e >> 4], a.cb.level[e & 15]);
   }
   if constexpr (kF8)
     for (int i = threadIdx.x; i < 256; i += sk::kThreads) rtab[i] = kE4m3Ratio.v[i];
@@ -85,7 +101,7 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_expert_skinny(SkinnyArgs a)
   char* stage = stage_all[wave];
   float* scl = scl_all[wave];
   const char* tabc = reinterpret_cast<const char*>(tab);
-  const uint32_t slot = static_cast<uint32_t>(lane & (kCopies - 1)) << 3;
+  const uint32_t slot = static_cast<uint32_t>(lane & (kCopies - 1)) << 3;  // twice the entry: look_up halves the address
   const uint32_t row_bytes = static_cast<uint32_t>(a.cols / 2), nblk = static_cast<uint32_t>(a.cols / 64);
   const int64_t klo = kw * pl.per, khi = klo + pl.per < a.cols ? klo + pl.per : a.cols;
   const int kspan = static_cast<int>(khi - klo);
@@ -141,7 +157,9 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_expert_skinny(SkinnyArgs a)
     };
 
     u32x4 xv[kNb][2];
+    floatx4 back;  // the powers of two that scale the sums of x rows 4 g .. back
     auto load_x = [&](int seg) {
+      uint32_t top = 0;  // of the row's magnitudes in the segment, as bfloat16 bits
 #pragma unroll
       for (int b = 0; b < kNb; ++b)
 #pragma unroll
@@ -149,13 +167,37 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_expert_skinny(SkinnyArgs a)
           const int k = seg * kSeg + 64 * b + 16 * g + 8 * u;
           xv[b][u] = *reinterpret_cast<const u32x4*>(xr + (k < kspan ? k : kspan - 8));
         }
-      if (seg * kSeg + kSeg > kspan) {
 #pragma unroll
-        for (int b = 0; b < kNb; ++b)
+      for (int b = 0; b < kNb; ++b)
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-            if (seg * kSeg + 64 * b >= kspan) xv[b][u] = u32x4{0u, 0u, 0u, 0u};
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t v = xv[b][u][c], lo = (v << 16) & 0x7FFF0000u, hi = v & 0x7FFF0000u;
+            const uint32_t m = lo > hi ? lo : hi;
+            top = m > top ? m : top;
+          }
+#pragma unroll
+      for (int off = 16; off < 64; off <<= 1) {
+        const uint32_t o = __shfl_xor(top, off, 64);
+        top = o > top ? o : top;
       }
+      // 2^e <= top < 2^(e + 1): the row times 2^(14 - e), its sums times 2^(e - 14).  The exponent
+      // is kept in -112 .. 127, where both factors are normal numbers
+      const int e = static_cast<int>(top >> 23) - 127 < -112 ? -112 : static_cast<int>(top >> 23) - 127;
+      const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+#pragma unroll
+      for (int b = 0; b < kNb; ++b) {
+        const float f = seg * kSeg + 64 * b < kspan ? up : 0.0f;  // zeros past the columns' end
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            xv[b][u][c] = half_pair(bf16_to_f32(xv[b][u][c] & 0xFFFFu) * f, __uint_as_float(xv[b][u][c] & 0xFFFF0000u) * f);
+      }
+      const float down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) back[i] = __shfl(down, 4 * g + i, 64);  // lane 4 g + i holds row 4 g + i
     };
 
     // as in the int4 GEMV: position p of the walk is group p % kG of segment
@@ -195,29 +237,31 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_expert_skinny(SkinnyArgs a)
           load_at(st, base, gi + 2 < kG ? seg : seg + 1, (gi + 2) % kG);
           if (!here) continue;
           sk::wave_lds_order();
+          // the codes of block b + 2 and the lookups of block b + 1 on their
+          // way while block b is multiplied
+          floatx4 sum = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+          uint2 w[3];
+          auto read_codes = [&](int b) {
+            w[b % 3] = *reinterpret_cast<const uint2*>(stage + sk::slot_of(ln, 2 * b + (g >> 1)) + 8 * (g & 1));
+          };
+          read_codes(0);
+          read_codes(1);
           const floatx4 f0 = *reinterpret_cast<const floatx4*>(scl + ln * kNb), f1 = *reinterpret_cast<const floatx4*>(scl + ln * kNb + 4);
+          u32x4 lk[2][2];
+          look_up(lk[0], w[0], tabc, slot);
 #pragma unroll
           for (int b = 0; b < kNb; ++b) {
-            const uint2 w = *reinterpret_cast<const uint2*>(stage + sk::slot_of(ln, 2 * b + (g >> 1)) + 8 * (g & 1));
-            u32x4 hi[2], lo[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint32_t addr = __builtin_amdgcn_perm(u ? w.y : w.x, slot, 0x0C0C0000u | ((4u + c) << 8));
-                const uint2 t = *reinterpret_cast<const uint2*>(tabc + addr);
-                hi[u][c] = t.x;
-                lo[u][c] = t.y;
-              }
-            floatx4 d = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-            d = sk::mfma<false>(xv[b][0], lo[0], d);
-            d = sk::mfma<false>(xv[b][1], lo[1], d);
-            d = sk::mfma<false>(xv[b][0], hi[0], d);
-            d = sk::mfma<false>(xv[b][1], hi[1], d);
+            if (b + 2 < kNb) read_codes(b + 2);
+            if (b + 1 < kNb) look_up(lk[(b + 1) & 1], w[(b + 1) % 3], tabc, slot);
+            __builtin_amdgcn_sched_barrier(0);
+            floatx4 d = sk::mfma<true>(xv[b][0], lk[b & 1][0], floatx4{0.0f, 0.0f, 0.0f, 0.0f});
+            d = sk::mfma<true>(xv[b][1], lk[b & 1][1], d);
             const float f = b < 4 ? f0[b & 3] : f1[b & 3];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[gi][i] = fmaf(f, d[i], acc[gi][i]);
+            for (int i = 0; i < 4; ++i) sum[i] = fmaf(f, d[i], sum[i]);
           }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[gi][i] = fmaf(back[i], sum[i], acc[gi][i]);
           sk::wave_lds_order();
         }
       }
