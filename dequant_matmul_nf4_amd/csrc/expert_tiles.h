@@ -39,18 +39,26 @@ __device__ __forceinline__ ExpertLane expert_lane(const ExpertRows& er, int c, i
   return r;
 }
 
-// All tiles of tm rows.  Every lane of a wave calls this (and the next).
-__device__ __forceinline__ int expert_tiles(const ExpertRows& er, int tm, int lane) {
-  int n = 0;
-  for (int c = 0; 64 * c < er.experts; ++c) n += __builtin_amdgcn_readlane(expert_lane(er, c, tm, lane).upto, 63);
-  return n;
+// The offsets of the first 64 experts stay in the lanes' registers, so that few
+// experts are read once.  Every lane of a wave calls these.
+struct ExpertScan {
+  ExpertLane first;
+  int tiles;  // all tiles
+};
+
+__device__ __forceinline__ ExpertScan scan_experts(const ExpertRows& er, int tm, int lane) {
+  ExpertScan s;
+  s.first = expert_lane(er, 0, tm, lane);
+  s.tiles = __builtin_amdgcn_readlane(s.first.upto, 63);
+  for (int c = 1; 64 * c < er.experts; ++c) s.tiles += __builtin_amdgcn_readlane(expert_lane(er, c, tm, lane).upto, 63);
+  return s;
 }
 
-__device__ __forceinline__ ExpertTile find_expert_tile(const ExpertRows& er, int tm, int tile, int lane) {
+__device__ __forceinline__ ExpertTile find_expert_tile(const ExpertRows& er, const ExpertScan& s, int tm, int tile, int lane) {
   ExpertTile t{-1, 0, 0, 0};
   int before = 0;
-  for (int c = 0; 64 * c < er.experts; ++c) {
-    const ExpertLane r = expert_lane(er, c, tm, lane);
+  ExpertLane r = s.first;
+  for (int c = 0;; r = expert_lane(er, c, tm, lane)) {
     const int here = __builtin_amdgcn_readlane(r.upto, 63);
     if (tile < before + here) {
       const int l = __builtin_ctzll(__ballot(before + r.upto > tile));
@@ -61,8 +69,8 @@ __device__ __forceinline__ ExpertTile find_expert_tile(const ExpertRows& er, int
       return t;
     }
     before += here;
+    if (64 * ++c >= er.experts) return t;
   }
-  return t;
 }
 
 // Unit u of n dealt round-robin over the 8 XCDs (as workgroups are): each XCD

@@ -43,7 +43,8 @@ __global__ __launch_bounds__(kThreads, MI == 2 ? 2 : 1) void k_expert_gemm(Exper
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t slot = static_cast<uint32_t>(lane & (kCopies - 1)) << 3;
   const int64_t tiles_n = (a.rows + kBN - 1) / kBN;
-  const int64_t units = tiles_n * expert_tiles(a.er, kBM, lane);
+  const ExpertScan scan = scan_experts(a.er, kBM, lane);
+  const int64_t units = tiles_n * scan.tiles;
   if (static_cast<int64_t>(blockIdx.x) >= units) return;
   gt::fill_level_pairs<kCopies>(tab, a.cb);  // ends with a barrier
   const float mean = kDQ ? *a.sc.mean : 0.0f;
@@ -51,7 +52,7 @@ __global__ __launch_bounds__(kThreads, MI == 2 ? 2 : 1) void k_expert_gemm(Exper
 
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t id = xcd_run(u, units);
-    const ExpertTile tile = find_expert_tile(a.er, kBM, static_cast<int>(id / tiles_n), lane);
+    const ExpertTile tile = find_expert_tile(a.er, scan, kBM, static_cast<int>(id / tiles_n), lane);
     const int64_t n0 = id % tiles_n * kBN;
 
     // the lane's pieces of the x tile: rows past the expert's last repeat it (never stored)

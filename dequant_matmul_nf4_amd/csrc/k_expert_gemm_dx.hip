@@ -28,10 +28,11 @@ __global__ __launch_bounds__(gt::kDxThreads) void k_expert_gemm_dx(ExpertDxArgs 
   __shared__ __align__(16) float2 pairs[256 * gt::kPairCopies];
   const int lane = threadIdx.x & 63;
   const int64_t tiles_k = (a.d.cols + gt::kTk - 1) / gt::kTk;
-  const int64_t tiles = tiles_k * expert_tiles(a.er, kTm, lane);
+  const ExpertScan scan = scan_experts(a.er, kTm, lane);
+  const int64_t tiles = tiles_k * scan.tiles;
   if (static_cast<int64_t>(blockIdx.x) >= tiles) return;
   const int64_t id = xcd_run(blockIdx.x, tiles);
-  const ExpertTile t = find_expert_tile(a.er, kTm, static_cast<int>(id / tiles_k), lane);
+  const ExpertTile t = find_expert_tile(a.er, scan, kTm, static_cast<int>(id / tiles_k), lane);
   gt::DxArgs d = a.d;
   const int64_t w0 = t.e * d.rows * d.cols;  // the expert's first weight
   d.packed += w0 / 2;

@@ -81,20 +81,25 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_expert_skinny(SkinnyArgs a)
   const sk::Plan& pl = a.pl;
 
   // the workgroup's run of the groups of all tiles
+  const ExpertScan scan = scan_experts(a.er, sk::kRows, lane);
   const int64_t ngr = (a.rows + 15) / 16;  // groups of a tile
-  const int64_t all = ngr * expert_tiles(a.er, sk::kRows, lane);
+  const int64_t all = ngr * scan.tiles;
   int64_t at = all * blockIdx.x / gridDim.x;
   const int64_t end = all * (blockIdx.x + 1) / gridDim.x;
   if (at >= end) return;
 
-  for (int i = threadIdx.x; i < 256 * kCopies; i += sk::kThreads) {
-    const int e = i / kCopies;
-    tab[i] = half_pair(a.cb.level[e >> 4], a.cb.level[e & 15]);
+  // Entry e of the table is levels e / 16 and e % 16: 16 passes of the threads,
+  // pass p writing the entries of first level p, each thread one second level.
+  static_assert(sk::kThreads == 16 * kCopies, "a pass is 16 entries");
+  {
+    const float second = a.cb.level[threadIdx.x / kCopies];
+#pragma unroll
+    for (int p = 0; p < 16; ++p) tab[p * sk::kThreads + threadIdx.x] = half_pair(a.cb.level[p], second);
   }
   if constexpr (kF8)
     for (int i = threadIdx.x; i < 256; i += sk::kThreads) rtab[i] = kE4m3Ratio.v[i];
   const float mean = kDQ ? *a.sc.mean : 0.0f;
-  __syncthreads();
+  sk::lds_barrier();
 
   const int kw = wave % pl.ks, rw = wave / pl.ks;  // the wave's share of the columns, of the groups
   const bool live = rw < pl.rs;
@@ -113,7 +118,7 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_expert_skinny(SkinnyArgs a)
   // the part of the run that lies in one tile
   for (int64_t next; at < end; at = next) {
     const int64_t tid = at / ngr, j0 = at - tid * ngr;
-    const ExpertTile tile = find_expert_tile(a.er, sk::kRows, static_cast<int>(tid), lane);
+    const ExpertTile tile = find_expert_tile(a.er, scan, sk::kRows, static_cast<int>(tid), lane);
     next = at + (ngr - j0) < end ? at + (ngr - j0) : end;
     const int ng = static_cast<int>(next - at);
     const int cnt = static_cast<int>(tile.hi - tile.row0 < sk::kRows ? tile.hi - tile.row0 : sk::kRows);  // rows of x
@@ -160,13 +165,24 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_expert_skinny(SkinnyArgs a)
     floatx4 back;  // the powers of two that scale the sums of x rows 4 g .. back
     auto load_x = [&](int seg) {
       uint32_t top = 0;  // of the row's magnitudes in the segment, as bfloat16 bits
+      const int left = kspan - seg * kSeg;
+      if (left >= kSeg) {
+        const uint16_t* p = xr + (seg * kSeg + 16 * g);
 #pragma unroll
-      for (int b = 0; b < kNb; ++b)
+        for (int b = 0; b < kNb; ++b)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int k = seg * kSeg + 64 * b + 16 * g + 8 * u;
-          xv[b][u] = *reinterpret_cast<const u32x4*>(xr + (k < kspan ? k : kspan - 8));
-        }
+          for (int u = 0; u < 2; ++u) xv[b][u] = *reinterpret_cast<const u32x4*>(p + 64 * b + 8 * u);
+      } else {
+        const uint16_t* p = xr + seg * kSeg;
+        const int g16 = 16 * static_cast<int>(opaque(g));
+#pragma unroll
+        for (int b = 0; b < kNb; ++b)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int k = 64 * b + g16 + 8 * u;
+            xv[b][u] = *reinterpret_cast<const u32x4*>(p + (k < left ? k : left - 8));
+          }
+      }
 #pragma unroll
       for (int b = 0; b < kNb; ++b)
 #pragma unroll
@@ -271,7 +287,7 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_expert_skinny(SkinnyArgs a)
         for (int gi = 0; gi < kG; ++gi) part[(wave * kG + gi) * 64 + lane] = acc[gi];
       }
       sk::lds_barrier();
-      for (int t = threadIdx.x; t < batch * 64; t += sk::kThreads) {
+      for (int t = opaque(threadIdx.x); t < batch * 64; t += sk::kThreads) {
         const int l = t & 63, gi = (t >> 6) % kG, r = (t >> 6) / kG;
         const int group = base + gi * pl.rs + r;
         if (group >= ng) continue;

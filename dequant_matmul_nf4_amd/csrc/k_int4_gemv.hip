@@ -153,13 +153,24 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_int4_gemv(Int4Args a) {
   auto load_x = [&](int seg) {
     // rows past m repeat row m - 1: they reach only rows of the result that are not stored
     const uint16_t* xr = a.x + (static_cast<int64_t>(ln < a.m ? ln : a.m - 1) * a.cols + klo);
+    const int left = kspan - seg * kSeg;
+    if (left >= kSeg) {
+      const uint16_t* p = xr + (seg * kSeg + 8 * kPw * g);
 #pragma unroll
-    for (int s = 0; s < kNs; ++s)
+      for (int s = 0; s < kNs; ++s)
 #pragma unroll
-      for (int u = 0; u < kPw; ++u) {
-        const int k = seg * kSeg + s * kGrp + 8 * kPw * g + 8 * u;
-        xn[s][u] = *reinterpret_cast<const u32x4*>(xr + (k < kspan ? k : kspan - 8));
-      }
+        for (int u = 0; u < kPw; ++u) xn[s][u] = *reinterpret_cast<const u32x4*>(p + s * kGrp + 8 * u);
+    } else {
+      const uint16_t* p = xr + seg * kSeg;
+      const int gk = 8 * kPw * static_cast<int>(opaque(g));
+#pragma unroll
+      for (int s = 0; s < kNs; ++s)
+#pragma unroll
+        for (int u = 0; u < kPw; ++u) {
+          const int k = s * kGrp + gk + 8 * u;
+          xn[s][u] = *reinterpret_cast<const u32x4*>(p + (k < left ? k : left - 8));
+        }
+    }
   };
   auto take_x = [&](int seg) {
     const u32x4 ones = kF16 ? u32x4{0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u}
@@ -250,7 +261,7 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_int4_gemv(Int4Args a) {
       for (int gi = 0; gi < kG; ++gi) part[(wave * kG + gi) * 64 + lane] = acc[gi];
     }
     sk::lds_barrier();
-    for (int t = threadIdx.x; t < batch * 64; t += sk::kThreads) {
+    for (int t = opaque(threadIdx.x); t < batch * 64; t += sk::kThreads) {
       const int l = t & 63, gi = (t >> 6) % kG, r = (t >> 6) / kG;
       const int group = base + gi * pl.rs + r;
       if (group >= ng) continue;

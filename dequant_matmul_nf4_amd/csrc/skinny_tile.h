@@ -104,8 +104,9 @@ __device__ __forceinline__ void load_codes(Codes& r, const uint8_t* step, const 
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) off[i] = l.off[i];
   if (!whole) {
+    const int l2 = opaque(lane);  // rare: nothing of this is worth keeping in registers
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) off[i] = code_offset(i, row_bytes, rows, pieces, lane);
+    for (int i = 0; i < kLoads; ++i) off[i] = code_offset(i, row_bytes, rows, pieces, l2);
   }
   const uint32_t keep = wanted ? ~0u : 0u;
 #pragma unroll

@@ -21,6 +21,11 @@ from tests.gpu_common import need_gpu, say
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def _seed():
+    need_gpu().manual_seed(21)
+
+
 def _types(torch):
     return {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 
