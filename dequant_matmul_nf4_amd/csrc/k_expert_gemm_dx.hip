@@ -58,6 +58,7 @@ hipError_t launch(const ExpertDxArgs& a, hipStream_t s) {
 
 hipError_t launch_expert_gemm_dx(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
                                  const uint16_t* dy, uint16_t* dx, hipStream_t s) {
+  if (er.m < 96 * static_cast<int64_t>(er.experts)) return launch_expert_skinny_dx(packed, rows, cols, sc, er, dy, dx, s);
   ExpertDxArgs a{};
   a.d.packed = packed; a.d.rows = rows; a.d.cols = cols; a.d.sc = sc; a.d.dy = dy; a.d.m = er.m; a.d.dx = dx;
   a.cb = codebook(sc.fp4);

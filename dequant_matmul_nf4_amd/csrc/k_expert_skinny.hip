@@ -30,7 +30,7 @@ using sk::u32x4;
 
 constexpr int kNb = kSeg / 64;   // blocks of a weight row per step
 constexpr int kPer = kNb / 4;    // of which a lane brings the scales
-constexpr int kCopies = 32;      // of the level table: lane l reads copy l % 32
+constexpr int kCopies = 64;      // of the level table (64 KB): each lane has its own, no two meet in a bank
 
 struct SkinnyArgs {
   const uint8_t* packed;
@@ -56,11 +56,11 @@ __device__ __forceinline__ uint32_t half_pair(float a, float b) {
 }
 
 // The level pairs of a lane's 8 code bytes: one permute puts a byte above the
-// lane's copy, a shift makes that the entry's address (128 bytes per code byte).
+// lane's copy (an entry is 256 bytes), one LDS read brings the pair.
 __device__ __forceinline__ void look_up(u32x4 (&t)[2], const uint2& w, const char* tab, uint32_t slot) {
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    const uint32_t at = __builtin_amdgcn_perm(c < 4 ? w.x : w.y, slot, 0x0C0C0000u | ((4u + (c & 3)) << 8)) >> 1;
+    const uint32_t at = __builtin_amdgcn_perm(c < 4 ? w.x : w.y, slot, 0x0C0C0000u | ((4u + (c & 3)) << 8));
     t[c >> 2][c & 3] = *reinterpret_cast<const uint32_t*>(tab + at);
   }
 }
@@ -88,13 +88,13 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_expert_skinny(SkinnyArgs a)
   const int64_t end = all * (blockIdx.x + 1) / gridDim.x;
   if (at >= end) return;
 
-  // Entry e of the table is levels e / 16 and e % 16: 16 passes of the threads,
-  // pass p writing the entries of first level p, each thread one second level.
-  static_assert(sk::kThreads == 16 * kCopies, "a pass is 16 entries");
+  // Entry e of the table is levels e / 16 and e % 16: two passes of the threads
+  // write the 16 entries of one first level.
+  static_assert(sk::kThreads == 8 * kCopies, "a pass is 8 entries");
   {
-    const float second = a.cb.level[threadIdx.x / kCopies];
+    const float second[2] = {a.cb.level[threadIdx.x / kCopies], a.cb.level[8 + threadIdx.x / kCopies]};
 #pragma unroll
-    for (int p = 0; p < 16; ++p) tab[p * sk::kThreads + threadIdx.x] = half_pair(a.cb.level[p], second);
+    for (int p = 0; p < 32; ++p) tab[p * sk::kThreads + threadIdx.x] = half_pair(a.cb.level[p >> 1], second[p & 1]);
   }
   if constexpr (kF8)
     for (int i = threadIdx.x; i < 256; i += sk::kThreads) rtab[i] = kE4m3Ratio.v[i];
@@ -106,7 +106,7 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_expert_skinny(SkinnyArgs a)
   char* stage = stage_all[wave];
   float* scl = scl_all[wave];
   const char* tabc = reinterpret_cast<const char*>(tab);
-  const uint32_t slot = static_cast<uint32_t>(lane & (kCopies - 1)) << 3;  // twice the entry: look_up halves the address
+  const uint32_t slot = static_cast<uint32_t>(lane & (kCopies - 1)) << 2;
   const uint32_t row_bytes = static_cast<uint32_t>(a.cols / 2), nblk = static_cast<uint32_t>(a.cols / 64);
   const int64_t klo = kw * pl.per, khi = klo + pl.per < a.cols ? klo + pl.per : a.cols;
   const int kspan = static_cast<int>(khi - klo);

@@ -220,6 +220,8 @@ hipError_t launch_expert_skinny(const uint8_t* packed, int64_t rows, int64_t col
                                 const ExpertX& ex, uint16_t* y, hipStream_t s);
 hipError_t launch_expert_gemm_dx(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
                                  const uint16_t* dy, uint16_t* dx, hipStream_t s);
+hipError_t launch_expert_skinny_dx(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
+                                   const uint16_t* dy, uint16_t* dx, hipStream_t s);
 hipError_t launch_expert_combine(const uint16_t* y, int64_t m, const int32_t* position, int64_t tokens, int slots,
                                  int64_t cols, const float* weights, uint16_t* out, hipStream_t s);
 hipError_t launch_expert_combine_backward(const uint16_t* dout, const uint16_t* y, int64_t m, const int32_t* position,
