@@ -15,9 +15,9 @@
 // cannot wait for the sums).
 //
 // Bound: reading the codes, so waves work on their own (no barrier in the loop)
-// with the next two steps' loads on their way; a workgroup's 8 waves are 2
-// column chunks x 4 slices of the reduction, whose partial tiles are added in
-// slice order at the end.
+// with the next steps' loads on their way; a workgroup's 8 waves are 1 or 2
+// column chunks x 8 or 4 slices of the reduction, whose partial tiles are added
+// in slice order at the end.
 #include "expert_tiles.h"
 #include "skinny_tile.h"
 
@@ -28,10 +28,7 @@ using sk::floatx4;
 using sk::u32x4;
 
 constexpr int kDxThreads = 512;
-constexpr int kSlices = 4;             // of the reduction
-constexpr int kChunks = 2;             // of columns
 constexpr int kChunkCols = 128;        // columns of a wave
-constexpr int kUnitCols = kChunks * kChunkCols;
 constexpr int kStepRows = 32;
 constexpr int kCopies = 32;            // of the pair table: 64 KB, lane l reads copy l % 32
 
@@ -43,6 +40,7 @@ struct SkinnyDxArgs {
   const uint16_t* dy;  // [m][rows]
   uint16_t* dx;        // [m][cols]
   Codebook cb;
+  int chunks;          // column chunks of a workgroup: 1 or 2; its 8 waves are chunks x slices of the reduction
 };
 
 // One step's loads: 8 weight rows x 8 columns, kRt x 8 values of dy, and the
@@ -66,13 +64,15 @@ __global__ __launch_bounds__(kDxThreads, 2) void k_expert_skinny_dx(SkinnyDxArgs
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ln = lane & 15, g = lane >> 4;
-  const int chunk = wave & (kChunks - 1), slice = wave / kChunks;
+  const int chunks = a.chunks, slices = 8 / chunks;
+  const int chunk = wave & (chunks - 1), slice = wave / chunks;
+  const int64_t unit_cols = chunks * kChunkCols;
   float* scl = scl_all[wave];
   const char* tabc = reinterpret_cast<const char*>(tab);
   const uint32_t slot = static_cast<uint32_t>(lane & (kCopies - 1)) << 3;
 
   const ExpertScan scan = scan_experts(a.er, kTm, lane);
-  const int64_t per_tile = (a.cols + kUnitCols - 1) / kUnitCols;
+  const int64_t per_tile = (a.cols + unit_cols - 1) / unit_cols;
   const int64_t units = per_tile * scan.tiles;
   if (static_cast<int64_t>(blockIdx.x) >= units) return;
   {
@@ -89,51 +89,69 @@ __global__ __launch_bounds__(kDxThreads, 2) void k_expert_skinny_dx(SkinnyDxArgs
 
   const uint32_t row_bytes = static_cast<uint32_t>(a.cols / 2), nblk = static_cast<uint32_t>(a.cols / 64);
   const int64_t steps_all = (a.rows + kStepRows - 1) / kStepRows;
-  const int64_t per_slice = (steps_all + kSlices - 1) / kSlices;
+  const int64_t per_slice = (steps_all + slices - 1) / slices;
   const int64_t n_lo = slice * per_slice * kStepRows;
   const int64_t n_hi = n_lo + per_slice * kStepRows < a.rows ? n_lo + per_slice * kStepRows : a.rows;
   const int nsteps = n_lo < n_hi ? static_cast<int>((n_hi - n_lo + kStepRows - 1) / kStepRows) : 0;
 
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+  const int nrows = n_lo < n_hi ? static_cast<int>(n_hi - n_lo) : 0;
+  const int chunk0 = chunk * kChunkCols;
+
+  // A unit: one tile's rows, unit_cols columns.
+  int64_t row0, col0, w0;  // its first row of dx, first column, the wave's first weight row
+  int cnt;                 // its rows
+  uint32_t cl, cb, dyo[kRt];
+  auto take_unit = [&](int64_t u) {
     const int64_t id = xcd_run(u, units);
     const ExpertTile tile = find_expert_tile(a.er, scan, kTm, static_cast<int>(id / per_tile), lane);
-    const int64_t c0 = id % per_tile * kUnitCols + chunk * kChunkCols;  // the wave's first column
-    const int cnt = static_cast<int>(tile.hi - tile.row0 < kTm ? tile.hi - tile.row0 : kTm);
+    row0 = tile.row0;
+    col0 = id % per_tile * unit_cols;
+    w0 = tile.e * a.rows + n_lo;
+    cnt = static_cast<int>(tile.hi - tile.row0 < kTm ? tile.hi - tile.row0 : kTm);
     // columns past the end read the last ones and are not stored
-    const uint32_t cl = static_cast<uint32_t>(c0 + 8 * ln < a.cols ? c0 + 8 * ln : a.cols - 8);
-    const uint32_t cb = static_cast<uint32_t>(c0 / 64) + (lane >> 5) < nblk ? static_cast<uint32_t>(c0 / 64) + (lane >> 5) : nblk - 1;
-    const int64_t w0 = tile.e * a.rows + n_lo;  // the wave's first weight row
-    const uint16_t* dy0 = a.dy + tile.row0 * a.rows + n_lo;
-    uint32_t dyo[kRt];
+    const int64_t c0 = col0 + chunk0;
+    cl = static_cast<uint32_t>(c0 + 8 * ln < a.cols ? c0 + 8 * ln : a.cols - 8);
+    cb = static_cast<uint32_t>(c0 / 64) + (lane >> 5) < nblk ? static_cast<uint32_t>(c0 / 64) + (lane >> 5) : nblk - 1;
 #pragma unroll
     for (int r = 0; r < kRt; ++r)  // rows past the tile's repeat its last: not stored
       dyo[r] = static_cast<uint32_t>(16 * r + ln < cnt ? 16 * r + ln : cnt - 1) * static_cast<uint32_t>(a.rows);
-    const int nrows = static_cast<int>(n_hi - n_lo);
+  };
 
-    DxStep<kRt, kDQ> set[2];
-    auto load_step = [&](DxStep<kRt, kDQ>& st, int step) {
-      // steps past the slice's last repeat it (no branch around a load).  The
-      // expert's rows are a multiple of 8: a lane group's 8 exist or none does, and
-      // then it reads the last 8, which meet zeros of dy.
-      const int n = (step < nsteps ? step : nsteps - 1) * kStepRows;
-      const int left = nrows - n, k = 8 * g < left ? 8 * g : left - 8;
-      const uint8_t* p = a.packed + (w0 + n) * row_bytes;
-      const uint32_t wo = static_cast<uint32_t>(k) * row_bytes + (cl >> 1);
+  constexpr int kDepth = kRt == 4 ? 2 : 4;  // steps on their way
+  DxStep<kRt, kDQ> set[kDepth];
+  auto load_step = [&](DxStep<kRt, kDQ>& st, int step) {
+    // steps past the slice's last repeat it (no branch around a load).  The
+    // expert's rows are a multiple of 8: a lane group's 8 exist or none does, and
+    // then it reads the last 8, which meet zeros of dy.
+    const int n = (step < nsteps ? step : nsteps - 1) * kStepRows;
+    const int left = nrows - n, k = 8 * g < left ? 8 * g : left - 8;
+    const uint8_t* p = a.packed + (w0 + n) * row_bytes;
+    const uint16_t* dy0 = a.dy + (row0 * a.rows + n_lo + n);
+    const uint32_t wo = static_cast<uint32_t>(k) * row_bytes + (cl >> 1);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        st.w[i] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p + static_cast<int64_t>(i) * row_bytes + wo));
+    for (int i = 0; i < 8; ++i)
+      st.w[i] = *reinterpret_cast<const uint32_t*>(p + static_cast<int64_t>(i) * row_bytes + wo);
 #pragma unroll
-      for (int r = 0; r < kRt; ++r) st.dy[r] = *reinterpret_cast<const u32x4*>(dy0 + n + (dyo[r] + k));
-      const int64_t b0 = (w0 + n) * nblk;
-      const uint32_t bo = static_cast<uint32_t>((lane & 31) < left ? (lane & 31) : left - 1) * nblk + cb;
-      if constexpr (kDQ) {
-        st.q = (a.sc.q + b0)[bo];
-        st.s = a.sc.absmax2[(static_cast<uint32_t>(b0) + bo) >> 8];  // fewer than 2^31 blocks
-      } else {
-        st.s = (a.sc.absmax + b0)[bo];
-      }
-    };
+    for (int r = 0; r < kRt; ++r) st.dy[r] = *reinterpret_cast<const u32x4*>(dy0 + (dyo[r] + k));
+    const int64_t b0 = (w0 + n) * nblk;
+    const uint32_t bo = static_cast<uint32_t>((lane & 31) < left ? (lane & 31) : left - 1) * nblk + cb;
+    if constexpr (kDQ) {
+      st.q = (a.sc.q + b0)[bo];
+      st.s = a.sc.absmax2[(static_cast<uint32_t>(b0) + bo) >> 8];  // fewer than 2^31 blocks
+    } else {
+      st.s = (a.sc.absmax + b0)[bo];
+    }
+  };
+  auto start_unit = [&](int64_t u) {
+    take_unit(u);
+    if (nsteps > 0) {
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i) load_step(set[i], i);
+    }
+  };
 
+  start_unit(blockIdx.x);
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     floatx4 acc[kRt][8];
 #pragma unroll
     for (int r = 0; r < kRt; ++r)
@@ -190,37 +208,41 @@ __global__ __launch_bounds__(kDxThreads, 2) void k_expert_skinny_dx(SkinnyDxArgs
       sk::wave_lds_order();
     };
 
-    if (nsteps > 0) {
-      load_step(set[0], 0);
-      load_step(set[1], 1);
-      for (int step = 0; step < nsteps; step += 2) {
-        multiply(set[0], step, step + 2);
-        if (step + 1 < nsteps) multiply(set[1], step + 1, step + 3);
-      }
+    for (int step = 0; step < nsteps; step += kDepth) {
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i)
+        if (step + i < nsteps) multiply(set[i], step + i, step + i + kDepth);
     }
-    // The slices' partial tiles, 16 rows at a time: lane (ln, g) holds rows 4 g .. + 3
-    // of columns 8 ln + j.
+    // The next unit's first loads, then this one's slices added up, 16 rows at a
+    // time: lane (ln, g) holds rows 4 g .. + 3 of columns 8 ln + j.
+    const int64_t out_row = row0, out_col = col0;
+    const int out_cnt = cnt;
+    if (u + gridDim.x < units) start_unit(u + gridDim.x);
 #pragma unroll
     for (int r = 0; r < kRt; ++r) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) part[wave][j * 64 + lane] = acc[r][j];
       sk::lds_barrier();
-      for (int t = opaque(threadIdx.x); t < kChunks * 256; t += kDxThreads) {
+      for (int t = opaque(threadIdx.x); t < chunks * 256; t += kDxThreads) {
         const int ch = t >> 8, l = t & 63, i = (t >> 6) & 3;
         const int row = 16 * r + 4 * (l >> 4) + i;
-        const int64_t col = id % per_tile * kUnitCols + ch * kChunkCols + 8 * (l & 15);
-        if (row < cnt && col < a.cols) {
-          uint32_t o[4];
+        const int64_t col = out_col + ch * kChunkCols + 8 * (l & 15);
+        if (row < out_cnt && col < a.cols) {
           float v[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            v[j] = 0.0f;
+            v[j] = part[ch][j * 64 + l][i];
 #pragma unroll
-            for (int k = 0; k < kSlices; ++k) v[j] += part[k * kChunks + ch][j * 64 + l][i];
+            for (int k = 1; k < 4; ++k) v[j] += part[k * chunks + ch][j * 64 + l][i];
           }
+          if (chunks == 1) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-          *reinterpret_cast<u32x4*>(a.dx + (tile.row0 + row) * a.cols + col) = u32x4{o[0], o[1], o[2], o[3]};
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+              for (int k = 4; k < 8; ++k) v[j] += part[k][j * 64 + l][i];
+          }
+          *reinterpret_cast<u32x4*>(a.dx + (out_row + row) * a.cols + col) =
+              u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
         }
       }
       sk::lds_barrier();
@@ -229,9 +251,10 @@ __global__ __launch_bounds__(kDxThreads, 2) void k_expert_skinny_dx(SkinnyDxArgs
 }
 
 template <int kRt>
-void launch(const SkinnyDxArgs& a, hipStream_t s) {
-  const int64_t tiles = (a.er.m + 16 * kRt - 1) / (16 * kRt) + (a.er.m < a.er.experts ? a.er.m : a.er.experts);
-  const int64_t most = tiles * ((a.cols + kUnitCols - 1) / kUnitCols);
+void launch(SkinnyDxArgs a, hipStream_t s) {
+  const int64_t tiles = (a.er.m + 16 * kRt - 1) / (16 * kRt) + (a.er.m < a.er.experts ? a.er.m : a.er.experts);  // at most
+  a.chunks = tiles * ((a.cols + 255) / 256) >= 2 * device_cus() ? 2 : 1;
+  const int64_t most = tiles * ((a.cols + a.chunks * kChunkCols - 1) / (a.chunks * kChunkCols));
   const dim3 gd(static_cast<unsigned>(most < device_cus() ? most : device_cus())), bd(kDxThreads);
   if (a.sc.absmax) hipLaunchKernelGGL((k_expert_skinny_dx<kRt, false, false>), gd, bd, 0, s, a);
   else if (a.sc.f8) hipLaunchKernelGGL((k_expert_skinny_dx<kRt, true, true>), gd, bd, 0, s, a);
@@ -246,8 +269,9 @@ hipError_t launch_expert_skinny_dx(const uint8_t* packed, int64_t rows, int64_t 
   a.packed = packed; a.rows = rows; a.cols = cols; a.sc = sc; a.er = er; a.dy = dy; a.dx = dx;
   a.cb = codebook(sc.fp4);
   const int64_t mean = er.m / er.experts;
-  if (mean < 12) launch<1>(a, s);
-  else if (mean < 28) launch<2>(a, s);
+  // while reading the codes is what takes the time, taller tiles are free, and an
+  // expert of more rows than the mean should not need a second one
+  if (mean < 16) launch<2>(a, s);
   else launch<4>(a, s);
   return hipGetLastError();
 }
