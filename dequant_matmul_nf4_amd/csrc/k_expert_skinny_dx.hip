@@ -43,14 +43,18 @@ struct SkinnyDxArgs {
   int chunks;          // column chunks of a workgroup: 1 or 2; its 8 waves are chunks x slices of the reduction
 };
 
-// One step's loads: 8 weight rows x 8 columns, kRt x 8 values of dy, and the
-// scale of weight row lane % 32 in block lane / 32 of the chunk.
-template <int kRt, bool kDQ>
+// One step's loads: 8 weight rows x 8 columns, and the scale of weight row
+// lane % 32 in block lane / 32 of the chunk.
+template <bool kDQ>
 struct DxStep {
   uint32_t w[8];
-  u32x4 dy[kRt];
   int8_t q;
   float s;
+};
+// Its kRt x 8 values of dy.
+template <int kRt>
+struct DxRows {
+  u32x4 v[kRt];
 };
 
 // kRt: tiles of 16 rows of dy.
@@ -117,22 +121,28 @@ __global__ __launch_bounds__(kDxThreads, 2) void k_expert_skinny_dx(SkinnyDxArgs
       dyo[r] = static_cast<uint32_t>(16 * r + ln < cnt ? 16 * r + ln : cnt - 1) * static_cast<uint32_t>(a.rows);
   };
 
-  constexpr int kDepth = kRt == 4 ? 2 : 4;  // steps on their way
-  DxStep<kRt, kDQ> set[kDepth];
-  auto load_step = [&](DxStep<kRt, kDQ>& st, int step) {
+  constexpr int kDepth = kRt == 4 ? 2 : 4;    // steps of codes on their way
+  constexpr int kDyDepth = kRt == 4 ? 1 : 4;  // and of dy, which the caches hold
+  DxStep<kDQ> set[kDepth];
+  DxRows<kRt> dys[kDyDepth];
+  auto load_dy = [&](DxRows<kRt>& st, int step) {
+    const int n = (step < nsteps ? step : nsteps - 1) * kStepRows;
+    const int left = nrows - n, k = 8 * g < left ? 8 * g : left - 8;
+    const uint16_t* dy0 = a.dy + (row0 * a.rows + n_lo + n);
+#pragma unroll
+    for (int r = 0; r < kRt; ++r) st.v[r] = *reinterpret_cast<const u32x4*>(dy0 + (dyo[r] + k));
+  };
+  auto load_step = [&](DxStep<kDQ>& st, int step) {
     // steps past the slice's last repeat it (no branch around a load).  The
     // expert's rows are a multiple of 8: a lane group's 8 exist or none does, and
     // then it reads the last 8, which meet zeros of dy.
     const int n = (step < nsteps ? step : nsteps - 1) * kStepRows;
     const int left = nrows - n, k = 8 * g < left ? 8 * g : left - 8;
     const uint8_t* p = a.packed + (w0 + n) * row_bytes;
-    const uint16_t* dy0 = a.dy + (row0 * a.rows + n_lo + n);
     const uint32_t wo = static_cast<uint32_t>(k) * row_bytes + (cl >> 1);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       st.w[i] = *reinterpret_cast<const uint32_t*>(p + static_cast<int64_t>(i) * row_bytes + wo);
-#pragma unroll
-    for (int r = 0; r < kRt; ++r) st.dy[r] = *reinterpret_cast<const u32x4*>(dy0 + (dyo[r] + k));
     const int64_t b0 = (w0 + n) * nblk;
     const uint32_t bo = static_cast<uint32_t>((lane & 31) < left ? (lane & 31) : left - 1) * nblk + cb;
     if constexpr (kDQ) {
@@ -146,7 +156,10 @@ __global__ __launch_bounds__(kDxThreads, 2) void k_expert_skinny_dx(SkinnyDxArgs
     take_unit(u);
     if (nsteps > 0) {
 #pragma unroll
-      for (int i = 0; i < kDepth; ++i) load_step(set[i], i);
+      for (int i = 0; i < kDepth; ++i) {
+        if (i < kDyDepth) load_dy(dys[i], i);
+        load_step(set[i], i);
+      }
     }
   };
 
@@ -158,7 +171,7 @@ __global__ __launch_bounds__(kDxThreads, 2) void k_expert_skinny_dx(SkinnyDxArgs
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[r][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto multiply = [&](DxStep<kRt, kDQ>& st, int step, int ahead) {
+    auto multiply = [&](DxStep<kDQ>& st, DxRows<kRt>& dy, int step) {
       // codes of rows 2 t, 2 t + 1 as bytes: even columns, odd columns
       uint32_t ev[4], od[4];
 #pragma unroll
@@ -171,12 +184,13 @@ __global__ __launch_bounds__(kDxThreads, 2) void k_expert_skinny_dx(SkinnyDxArgs
 #pragma unroll
       for (int r = 0; r < kRt; ++r)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) af[r][c] = in ? st.dy[r][c] : 0u;
+        for (int c = 0; c < 4; ++c) af[r][c] = in ? dy.v[r][c] : 0u;
       float s;
       if constexpr (kDQ) s = (kF8 ? rtab[st.q & 0xFF] : div127(st.q)) * st.s + mean;  // a_hat, three roundings
       else s = st.s;
       scl[lane] = s;
-      load_step(st, ahead);
+      load_dy(dy, step + kDyDepth);
+      load_step(st, step + kDepth);
       sk::wave_lds_order();
       // the scales of rows 8 g .. in the lane's block
       const floatx4 s0 = *reinterpret_cast<const floatx4*>(scl + (ln >> 3) * 32 + 8 * g);
@@ -211,7 +225,7 @@ __global__ __launch_bounds__(kDxThreads, 2) void k_expert_skinny_dx(SkinnyDxArgs
     for (int step = 0; step < nsteps; step += kDepth) {
 #pragma unroll
       for (int i = 0; i < kDepth; ++i)
-        if (step + i < nsteps) multiply(set[i], step + i, step + i + kDepth);
+        if (step + i < nsteps) multiply(set[i], dys[i % kDyDepth], step + i);
     }
     // The next unit's first loads, then this one's slices added up, 16 rows at a
     // time: lane (ln, g) holds rows 4 g .. + 3 of columns 8 ln + j.
