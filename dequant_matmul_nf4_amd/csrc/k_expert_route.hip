@@ -77,9 +77,12 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_place(const int32_t* __re
   __shared__ int base[kMaxExperts];                  // the next row of each expert
   __shared__ uint16_t wcnt[kPlanWaves][kMaxExperts + 1];
   __shared__ int wsum[kPlanWaves];
+  __shared__ int sums[2][kOne ? 1 : kPlanThreads];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int64_t lo = blockIdx.x * chunk, hi = lo + chunk < n ? lo + chunk : n;
-  int mine = 0, before = 0;  // expert t: all slots, those of earlier blocks
+  int next = lo + t < hi ? ids[lo + t] : -1;  // this thread's id of the next round
+  int mine = 0, before = 0;                   // expert t: all slots, those of earlier blocks
+  for (int w = 0; t < experts && w < kPlanWaves; ++w) wcnt[w][t] = 0;
   if constexpr (kOne) {
     base[t] = 0;
     __syncthreads();
@@ -90,11 +93,24 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_place(const int32_t* __re
     __syncthreads();
     mine = base[t];
     __syncthreads();
-  } else if (t < experts) {
-    for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-      const int c = counts[static_cast<int64_t>(b) * experts + t];
-      mine += c;
-      before += b < static_cast<int>(blockIdx.x) ? c : 0;
+  } else {
+    // the threads read the blocks' counts, 2^bits of them one block at a time
+    const int e = t & ((1 << bits) - 1), lanes = kPlanThreads >> bits;
+    int all = 0, early = 0;
+    if (e < experts) {
+#pragma unroll 4
+      for (int b = t >> bits; b < static_cast<int>(gridDim.x); b += lanes) {
+        const int c = counts[static_cast<int64_t>(b) * experts + e];
+        all += c;
+        early += b < static_cast<int>(blockIdx.x) ? c : 0;
+      }
+    }
+    sums[0][t] = all;
+    sums[1][t] = early;
+    __syncthreads();
+    for (int k = t; t < experts && k < kPlanThreads; k += 1 << bits) {
+      mine += sums[0][k];
+      before += sums[1][k];
     }
   }
   int total;
@@ -109,13 +125,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_place(const int32_t* __re
     if (i >= total) order[i] = -1;
   for (int64_t i0 = lo; i0 < hi; i0 += kPlanThreads) {
     const int64_t i = i0 + t;
-    int key = kMaxExperts;
-    if (i < hi) {
-      const int id = ids[i];
-      if (id >= 0 && id < experts) key = id;
-    }
-    for (int e = t; e < kPlanWaves * (kMaxExperts + 1); e += kPlanThreads) (&wcnt[0][0])[e] = 0;
-    __syncthreads();
+    const int key = next >= 0 && next < experts ? next : kMaxExperts;
+    next = i + kPlanThreads < hi ? ids[i + kPlanThreads] : -1;
     const uint64_t kept = __ballot(key < kMaxExperts);
     const uint64_t mask = same_key(key, bits) & kept;
     const int rank = __popcll(mask & ((uint64_t(1) << lane) - 1));
@@ -141,13 +152,15 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_place(const int32_t* __re
       position[i] = p;
     }
     __syncthreads();
-    if (t < experts) base[t] += sum;
+    if (t < experts) {
+      base[t] += sum;
+      for (int w = 0; w < kPlanWaves; ++w) wcnt[w][t] = 0;
+    }
+    __syncthreads();
   }
 }
 
 // ----------------------------------------------------------------- combine
-
-typedef float floatx8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ void unpack8(const u32x4& v, float (&f)[8]) {
 #pragma unroll

@@ -65,7 +65,7 @@ __device__ __forceinline__ void store_scale(void* scales, int type, int64_t i, f
 }
 
 template <int kType>
-__global__ __launch_bounds__(256) void k_int4_quantize(const void* __restrict__ x, int64_t n, int group,
+__global__ __launch_bounds__(256) void k_int4_quantize(const void* __restrict__ x, int64_t n, int shift,
                                                        uint8_t* __restrict__ packed, void* __restrict__ scales,
                                                        int scale_type, uint8_t* __restrict__ zeros) {
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 16;
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(256) void k_int4_quantize(const void* __restrict__ 
     lo = fminf(lo, v[k]);
     hi = fmaxf(hi, v[k]);
   }
-  for (int off = 1; off < group / 16; off <<= 1) {
+  for (int off = 1; off < 1 << (shift - 4); off <<= 1) {
     lo = fminf(lo, __shfl_xor(lo, off, kWave));
     hi = fmaxf(hi, __shfl_xor(hi, off, kWave));
   }
@@ -94,16 +94,27 @@ __global__ __launch_bounds__(256) void k_int4_quantize(const void* __restrict__ 
     z = 8.0f;
   }
   uint32_t w[2] = {0u, 0u};
+  // rint(x / s): with r = fl32(1 / s), q0 = fl32(x r) and the exact remainder
+  // x - q0 s, fl32(q0 + (x - q0 s) r) is the IEEE quotient (Markstein) while
+  // nothing under- or overflows on the way; smaller quotients round to 0 both ways.
+  const bool fast = s >= 0x1p-80f && s <= 0x1p100f;
+  const float r = 1.0f / s;
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
-    const float t = s > 0.0f ? rintf(v[k] / s) : 0.0f;
+    float t;
+    if (fast) {
+      const float q0 = v[k] * r;
+      t = rintf(fmaf(fmaf(-q0, s, v[k]), r, q0));
+    } else {
+      t = s > 0.0f ? rintf(v[k] / s) : 0.0f;
+    }
     const uint32_t q = static_cast<uint32_t>(fminf(fmaxf(t + z, 0.0f), 15.0f));
     w[k >> 3] |= q << (8 * ((k & 7) >> 1) + ((k & 1) ? 0 : 4));
   }
   *reinterpret_cast<u32x2*>(packed + i / 2) = u32x2{w[0], w[1]};
-  if ((i & (group - 1)) == 0) {
-    store_scale(scales, scale_type, i / group, s);
-    if (zeros) zeros[i / group] = static_cast<uint8_t>(z);
+  if ((i & ((1 << shift) - 1)) == 0) {
+    store_scale(scales, scale_type, i >> shift, s);
+    if (zeros) zeros[i >> shift] = static_cast<uint8_t>(z);
   }
 }
 
@@ -116,13 +127,13 @@ __device__ __forceinline__ float scale_at(const void* p, int type, int64_t i) {
 // Eight values per lane for the 16-bit types, four for float32: one 16-byte
 // store either way.
 template <int kType>
-__global__ __launch_bounds__(256) void k_int4_dequantize(Int4Weight w, int64_t n, void* __restrict__ out) {
+__global__ __launch_bounds__(256) void k_int4_dequantize(Int4Weight w, int shift, int64_t n, void* __restrict__ out) {
   constexpr int kPer = kType == 0 ? 4 : 8;
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * kPer;
   if (i >= n) return;
   const uint32_t c = kType == 0 ? *reinterpret_cast<const uint16_t*>(w.packed + i / 2)
                                 : *reinterpret_cast<const uint32_t*>(w.packed + i / 2);
-  const int64_t gi = i / w.group;
+  const int64_t gi = i >> shift;
   const float s = scale_at(w.scales, w.scale_type, gi);
   const int z = w.zeros ? w.zeros[gi] : 8;
   float v[kPer];
@@ -151,14 +162,17 @@ __global__ __launch_bounds__(256) void k_int4_dequantize(Int4Weight w, int64_t n
 
 }  // namespace
 
+static int shift_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
+
 hipError_t launch_int4_quantize(const void* x, int x_type, int64_t n, int group, uint8_t* packed, void* scales,
                                 int scale_type, uint8_t* zeros, hipStream_t s) {
   const int64_t blocks = (n + 4095) / 4096;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const int shift = shift_of(group);
   const dim3 gd(static_cast<unsigned>(blocks)), bd(256);
-  if (x_type == 0) hipLaunchKernelGGL((k_int4_quantize<0>), gd, bd, 0, s, x, n, group, packed, scales, scale_type, zeros);
-  else if (x_type == 1) hipLaunchKernelGGL((k_int4_quantize<1>), gd, bd, 0, s, x, n, group, packed, scales, scale_type, zeros);
-  else hipLaunchKernelGGL((k_int4_quantize<2>), gd, bd, 0, s, x, n, group, packed, scales, scale_type, zeros);
+  if (x_type == 0) hipLaunchKernelGGL((k_int4_quantize<0>), gd, bd, 0, s, x, n, shift, packed, scales, scale_type, zeros);
+  else if (x_type == 1) hipLaunchKernelGGL((k_int4_quantize<1>), gd, bd, 0, s, x, n, shift, packed, scales, scale_type, zeros);
+  else hipLaunchKernelGGL((k_int4_quantize<2>), gd, bd, 0, s, x, n, shift, packed, scales, scale_type, zeros);
   return hipGetLastError();
 }
 
@@ -168,9 +182,9 @@ hipError_t launch_int4_dequantize(const Int4Weight& w, void* out, int out_type, 
   const int64_t blocks = (n + per - 1) / per;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   const dim3 gd(static_cast<unsigned>(blocks)), bd(256);
-  if (out_type == 0) hipLaunchKernelGGL((k_int4_dequantize<0>), gd, bd, 0, s, w, n, out);
-  else if (out_type == 1) hipLaunchKernelGGL((k_int4_dequantize<1>), gd, bd, 0, s, w, n, out);
-  else hipLaunchKernelGGL((k_int4_dequantize<2>), gd, bd, 0, s, w, n, out);
+  if (out_type == 0) hipLaunchKernelGGL((k_int4_dequantize<0>), gd, bd, 0, s, w, shift_of(w.group), n, out);
+  else if (out_type == 1) hipLaunchKernelGGL((k_int4_dequantize<1>), gd, bd, 0, s, w, shift_of(w.group), n, out);
+  else hipLaunchKernelGGL((k_int4_dequantize<2>), gd, bd, 0, s, w, shift_of(w.group), n, out);
   return hipGetLastError();
 }
 
