@@ -195,7 +195,7 @@ __global__ __launch_bounds__(256) void k_combine(const uint16_t* __restrict__ y,
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k] = fmaf(w, f[k], acc[k]);
     }
-    *reinterpret_cast<u32x4*>(out + token * cols + c) = pack8(acc);
+    __builtin_nontemporal_store(pack8(acc), reinterpret_cast<u32x4*>(out + token * cols + c));
   }
 }
 
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(256) void k_combine_backward(const uint16_t* __rest
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) d[k] = w * g[k];
-      if (dy) *reinterpret_cast<u32x4*>(dy + p * cols + c) = pack8(d);
+      if (dy) __builtin_nontemporal_store(pack8(d), reinterpret_cast<u32x4*>(dy + p * cols + c));
     }
   }
   if (dweights) {
