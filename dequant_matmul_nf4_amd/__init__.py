@@ -181,9 +181,15 @@ def nf4_lora_grads_workspace(m: int, rows: int, cols: int, r: int) -> int:
 
 # ------------------------------------------------------------- torch glue
 
+_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _module
+    if _module is None:
+        import torch
+        _module = torch
+    return _module
 
 
 def _stream(stream=None) -> int:
@@ -678,26 +684,32 @@ def _call(dev, stream, fn, *args) -> None:
     `stream`, which must be one of that device, or on its current stream."""
     torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        # (the handle alone: a Stream object costs several times as much)
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
     elif stream.device != dev:
         raise ValueError(f"stream of {stream.device}, tensors on {dev}")
+    else:
+        handle = stream.cuda_stream
     if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, stream.cuda_stream))
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, stream.cuda_stream))
+            rc = fn(*args, handle)
+    if rc != NF4_OK:
+        _check(rc)
 
 
 def _need(name, t, dtype, numel, dev):
     """A contiguous device tensor of that dtype and number of elements."""
+    if t.is_cuda and t.is_contiguous() and t.dtype == dtype and t.numel() == numel and t.device == dev:
+        return
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous device tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.numel() != numel:
         raise ValueError(f"{name} holds {t.numel()} elements, expected {numel}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
 def nf4_expert_plan(ids, experts: int, order=None, position=None, offsets=None, workspace=None, stream=None):
@@ -708,18 +720,24 @@ def nf4_expert_plan(ids, experts: int, order=None, position=None, offsets=None, 
     torch = _torch()
     dev, n = ids.device, ids.numel()
     _need("ids", ids, torch.int32, n, dev)
-    order = _alloc_on(stream, (n,), torch.int32, dev) if order is None else order
-    position = _alloc_on(stream, (n,), torch.int32, dev) if position is None else position
-    offsets = _alloc_on(stream, (max(experts, 0) + 1,), torch.int32, dev) if offsets is None else offsets
-    _need("order", order, torch.int32, n, dev)
-    _need("position", position, torch.int32, n, dev)
-    _need("offsets", offsets, torch.int32, experts + 1, dev)
-    wsb = nf4_expert_plan_workspace(n, experts)
-    if wsb and workspace is None:
-        workspace = _alloc_on(stream, (wsb,), torch.uint8, dev)
-    _need_cuda(workspace)
-    _same_device(dev, workspace)
-    wsn = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if not 1 <= experts <= MAX_EXPERTS:
+        raise ValueError(f"experts = {experts}: 1 to {MAX_EXPERTS}")
+
+    def out(name, t, count):
+        if t is None:
+            return _alloc_on(stream, (count,), torch.int32, dev)
+        _need(name, t, torch.int32, count, dev)
+        return t
+
+    order, position, offsets = out("order", order, n), out("position", position, n), out("offsets", offsets, experts + 1)
+    if workspace is None:
+        wsn = nf4_expert_plan_workspace(n, experts)
+        if wsn:
+            workspace = _alloc_on(stream, (wsn,), torch.uint8, dev)
+    else:
+        _need_cuda(workspace)
+        _same_device(dev, workspace)
+        wsn = workspace.numel() * workspace.element_size()
     _call(dev, stream, lib().nf4_expert_plan, ids.data_ptr(), n, experts, order.data_ptr(), position.data_ptr(),
           offsets.data_ptr(), _ptr(workspace), wsn)
     return order, position, offsets
@@ -744,7 +762,8 @@ def nf4_expert_gemm(w: NF4Weight, experts: int, x, offsets, index=None, slots: i
         _need("index", index, torch.int32, m, dev)
     if y is None:
         y = _alloc_on(stream, (m, rows), torch.bfloat16, dev)
-    _need("y", y, torch.bfloat16, m * rows, dev)
+    else:
+        _need("y", y, torch.bfloat16, m * rows, dev)
     _call(dev, stream, lib().nf4_expert_gemm, ctypes.byref(cs), experts, x2.data_ptr(), x2.shape[0], _ptr(index), slots,
           offsets.data_ptr(), m, y.data_ptr())
     return y
@@ -763,7 +782,8 @@ def nf4_expert_gemm_dx(w: NF4Weight, experts: int, dy, offsets, dx=None, stream=
     _need("offsets", offsets, torch.int32, experts + 1, dev)
     if dx is None:
         dx = _alloc_on(stream, (m, w.cols), torch.bfloat16, dev)
-    _need("dx", dx, torch.bfloat16, m * w.cols, dev)
+    else:
+        _need("dx", dx, torch.bfloat16, m * w.cols, dev)
     _call(dev, stream, lib().nf4_expert_gemm_dx, ctypes.byref(cs), experts, dy2.data_ptr(), offsets.data_ptr(), m,
           dx.data_ptr())
     return dx
@@ -784,7 +804,8 @@ def nf4_expert_combine(y, position, slots: int, weights=None, out=None, stream=N
         _need("weights", weights, torch.float32, n, dev)
     if out is None:
         out = _alloc_on(stream, (n // slots, cols), torch.bfloat16, dev)
-    _need("out", out, torch.bfloat16, n // slots * cols, dev)
+    else:
+        _need("out", out, torch.bfloat16, n // slots * cols, dev)
     _call(dev, stream, lib().nf4_expert_combine, y.data_ptr(), m, position.data_ptr(), n // slots, slots, cols,
           _ptr(weights), out.data_ptr())
     return out
@@ -885,7 +906,8 @@ def nf4_int4_dequantize(w: Int4Weight, out=None, out_dtype=None, stream=None):
     cs = w.c_struct()
     if out is None:
         out = _alloc_on(stream, (w.rows, w.cols), out_dtype or torch.bfloat16, w.device)
-    _need("out", out, out.dtype, w.rows * w.cols, w.device)
+    else:
+        _need("out", out, out.dtype, w.rows * w.cols, w.device)
     _call(w.device, stream, lib().nf4_int4_dequantize, ctypes.byref(cs), out.data_ptr(), _dtype_code(out))
     return out
 
@@ -899,6 +921,7 @@ def nf4_int4_gemv(w: Int4Weight, x, y=None, y_dtype=None, stream=None):
     _need("x", x2, x2.dtype, m * w.cols, dev)
     if y is None:
         y = _alloc_on(stream, (m, w.rows), y_dtype or x2.dtype, dev)
-    _need("y", y, y.dtype, m * w.rows, dev)
+    else:
+        _need("y", y, y.dtype, m * w.rows, dev)
     _call(dev, stream, lib().nf4_int4_gemv, ctypes.byref(cs), x2.data_ptr(), _dtype_code(x2), m, y.data_ptr(), _dtype_code(y))
     return y
