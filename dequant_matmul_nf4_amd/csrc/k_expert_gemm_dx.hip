@@ -58,10 +58,10 @@ hipError_t launch(const ExpertDxArgs& a, hipStream_t s) {
 
 hipError_t launch_expert_gemm_dx(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
                                  const uint16_t* dy, uint16_t* dx, hipStream_t s) {
-  // Means of few rows go without turning weights on chip (64 experts of 1024x2048:
-  // at a mean of 187 rows 145 us so, at 256 rows 183 us against 134 us here;
-  // 8 experts of 14336x4096 at 256 rows: 568 against 468 us).
-  if (er.m < 192 * static_cast<int64_t>(er.experts)) return launch_expert_skinny_dx(packed, rows, cols, sc, er, dy, dx, s);
+  // Fewer rows on the mean than a tile go without turning weights on chip: at 256
+  // rows it takes 161 against 134 us here (64 experts of 1024x2048), and 464
+  // against 468 us (8 experts of 14336x4096).
+  if (er.m < 256 * static_cast<int64_t>(er.experts)) return launch_expert_skinny_dx(packed, rows, cols, sc, er, dy, dx, s);
   ExpertDxArgs a{};
   a.d.packed = packed; a.d.rows = rows; a.d.cols = cols; a.d.sc = sc; a.d.dy = dy; a.d.m = er.m; a.d.dx = dx;
   a.cb = codebook(sc.fp4);
