@@ -105,13 +105,23 @@ hipError_t launch(const ExpertGemmArgs& a, hipStream_t s) {
 
 hipError_t launch_expert_gemm(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
                               const ExpertX& ex, uint16_t* y, hipStream_t s) {
-  if (er.m <= 8 * static_cast<int64_t>(er.experts)) return launch_expert_skinny(packed, rows, cols, sc, er, ex, y, s);
+  // By the mean number of rows of an expert (the only one known here).  Measured in
+  // us: streaming tiles of 16 rows, then tiles of 64, 128 and 256 rows here:
+  //   8 experts of 14336x4096, mean  10:   67  106  169  223
+  //                                  32:  136  181  175  227
+  //                                  64:  241  189  250  236
+  //                                 150:  507  316  260  351
+  //                                 256:  854  441  424  371
+  //   64 experts of 1024x2048, mean  32:   49   55   53   67
+  //                                  64:   81   55   93   71
+  //                                 128:  138   96   95  128
+  //                                 256:  258  149  137  135
+  const int64_t experts = er.experts;
+  if (er.m <= 40 * experts) return launch_expert_skinny(packed, rows, cols, sc, er, ex, y, s);
   ExpertGemmArgs a{};
   a.packed = packed; a.rows = rows; a.cols = cols; a.sc = sc; a.er = er; a.ex = ex; a.y = y;
   a.cb = codebook(sc.fp4);
-  // tiles as tall as the experts' mean number of rows
-  const int64_t mean = er.m / er.experts;
-  return mean >= 256 ? launch<8>(a, s) : launch<2>(a, s);
+  return er.m <= 112 * experts ? launch<2>(a, s) : er.m <= 224 * experts ? launch<4>(a, s) : launch<8>(a, s);
 }
 
 }  // namespace nf4i
