@@ -563,7 +563,7 @@ int nf4_expert_gemm(const nf4_weight* w, int32_t experts, const void* x, int64_t
   if (!aligned(index, 4) || !aligned(offsets, 4))
     return fail(NF4_ERR_ALIGN, "%s: index and offsets must be 4-byte aligned", who);
   if (int rc = check_device()) return rc;
-  return launched(nf4i::launch_expert_gemm(w->packed, w->rows / experts, w->cols, sc, nf4i::ExpertRows{offsets, experts, m},
+  return launched(nf4i::launch_expert_gemm(w->packed, w->rows / experts, w->cols, sc, nf4i::ExpertRows{offsets, experts, m, 0, 0},
                                            nf4i::ExpertX{static_cast<const uint16_t*>(x), x_rows, index, slots},
                                            static_cast<uint16_t*>(y), as_stream(stream)),
                   who);
@@ -583,7 +583,7 @@ int nf4_expert_gemm_dx(const nf4_weight* w, int32_t experts, const void* dy, con
   if (!aligned(dy, 16) || !aligned(dx, 16)) return fail(NF4_ERR_ALIGN, "%s: dy and dx must be 16-byte aligned", who);
   if (!aligned(offsets, 4)) return fail(NF4_ERR_ALIGN, "%s: offsets must be 4-byte aligned", who);
   if (int rc = check_device()) return rc;
-  return launched(nf4i::launch_expert_gemm_dx(w->packed, rows, w->cols, sc, nf4i::ExpertRows{offsets, experts, m},
+  return launched(nf4i::launch_expert_gemm_dx(w->packed, rows, w->cols, sc, nf4i::ExpertRows{offsets, experts, m, 0, 0},
                                               static_cast<const uint16_t*>(dy), static_cast<uint16_t*>(dx),
                                               as_stream(stream)),
                   who);

@@ -14,6 +14,40 @@ struct ExpertTile {
   int64_t row0;     // the tile's first row
 };
 
+__device__ __forceinline__ int wave_prefix(int v, int lane) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int t = __shfl_up(v, off, 64);
+    if (lane >= off) v += t;
+  }
+  return v;
+}
+
+// Rows of expert 64 c + lane (none past the last expert).
+__device__ __forceinline__ void expert_range(const ExpertRows& er, int c, int lane, int64_t& lo, int64_t& hi) {
+  const int e = 64 * c + lane;
+  const int64_t a = er.offsets[e < er.experts ? e : er.experts];
+  const int64_t b = er.offsets[e < er.experts ? e + 1 : er.experts];
+  lo = a < 0 ? 0 : a < er.m ? a : er.m;
+  hi = b < lo ? lo : b < er.m ? b : er.m;
+}
+
+// Tiles of kCoverRows rows, the last one more than half full.
+__device__ __forceinline__ int cover_tiles(int64_t rows) { return static_cast<int>((rows + kCoverRows / 2 - 1) / kCoverRows); }
+
+// How many of these the first of two kernels takes: full rounds of its
+// workgroups, and a last round that fills most of them.
+__device__ __forceinline__ int covered_tiles(const ExpertRows& er, int lane) {
+  int64_t all = 0;
+  for (int c = 0; 64 * c < er.experts; ++c) {
+    int64_t lo, hi;
+    expert_range(er, c, lane, lo, hi);
+    all += __builtin_amdgcn_readlane(wave_prefix(cover_tiles(hi - lo), lane), 63);
+  }
+  const int64_t units = all * er.cover_units, full = units / er.cover_slots * er.cover_slots;
+  return static_cast<int>(3 * (units - full) > 2 * er.cover_slots ? all : full / er.cover_units);
+}
+
 // Tiles of the experts 64 c .. 64 c + 63, one expert per lane.
 struct ExpertLane {
   int64_t lo, hi;
@@ -21,21 +55,27 @@ struct ExpertLane {
   int upto;         // of lanes 0 .. this
 };
 
-__device__ __forceinline__ ExpertLane expert_lane(const ExpertRows& er, int c, int tm, int lane) {
+// covered: of the cover_tiles, counted expert by expert, the first ones that
+// another kernel takes; the expert's rows begin behind them.
+__device__ __forceinline__ ExpertLane expert_lane(const ExpertRows& er, int c, int tm, int lane, int covered = 0) {
   ExpertLane r;
-  const int e = 64 * c + lane;
-  const int64_t a = er.offsets[e < er.experts ? e : er.experts];
-  const int64_t b = er.offsets[e < er.experts ? e + 1 : er.experts];
-  r.lo = a < 0 ? 0 : a < er.m ? a : er.m;
-  r.hi = b < r.lo ? r.lo : b < er.m ? b : er.m;
-  r.tiles = static_cast<int>((r.hi - r.lo + tm - 1) / tm);
-  int s = r.tiles;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int t = __shfl_up(s, off, 64);
-    if (lane >= off) s += t;
+  if (covered > 0) {
+    int before = 0;
+    for (int b = 0; b <= c; ++b) {
+      expert_range(er, b, lane, r.lo, r.hi);
+      const int own = cover_tiles(r.hi - r.lo), upto = wave_prefix(own, lane);
+      if (b == c) {
+        const int mine = covered - before - (upto - own);
+        r.lo += static_cast<int64_t>(mine < 0 ? 0 : mine < own ? mine : own) * kCoverRows;
+        r.lo = r.lo < r.hi ? r.lo : r.hi;
+      }
+      before += __builtin_amdgcn_readlane(upto, 63);
+    }
+  } else {
+    expert_range(er, c, lane, r.lo, r.hi);
   }
-  r.upto = s;
+  r.tiles = static_cast<int>((r.hi - r.lo + tm - 1) / tm);
+  r.upto = wave_prefix(r.tiles, lane);
   return r;
 }
 
@@ -43,14 +83,16 @@ __device__ __forceinline__ ExpertLane expert_lane(const ExpertRows& er, int c, i
 // experts are read once.  Every lane of a wave calls these.
 struct ExpertScan {
   ExpertLane first;
-  int tiles;  // all tiles
+  int tiles;    // all tiles
+  int covered;  // tiles that another kernel takes
 };
 
-__device__ __forceinline__ ExpertScan scan_experts(const ExpertRows& er, int tm, int lane) {
+__device__ __forceinline__ ExpertScan scan_experts(const ExpertRows& er, int tm, int lane, int covered = 0) {
   ExpertScan s;
-  s.first = expert_lane(er, 0, tm, lane);
+  s.covered = covered;
+  s.first = expert_lane(er, 0, tm, lane, covered);
   s.tiles = __builtin_amdgcn_readlane(s.first.upto, 63);
-  for (int c = 1; 64 * c < er.experts; ++c) s.tiles += __builtin_amdgcn_readlane(expert_lane(er, c, tm, lane).upto, 63);
+  for (int c = 1; 64 * c < er.experts; ++c) s.tiles += __builtin_amdgcn_readlane(expert_lane(er, c, tm, lane, covered).upto, 63);
   return s;
 }
 
@@ -58,7 +100,7 @@ __device__ __forceinline__ ExpertTile find_expert_tile(const ExpertRows& er, con
   ExpertTile t{-1, 0, 0, 0};
   int before = 0;
   ExpertLane r = s.first;
-  for (int c = 0;; r = expert_lane(er, c, tm, lane)) {
+  for (int c = 0;; r = expert_lane(er, c, tm, lane, s.covered)) {
     const int here = __builtin_amdgcn_readlane(r.upto, 63);
     if (tile < before + here) {
       const int l = __builtin_ctzll(__ballot(before + r.upto > tile));

@@ -4,9 +4,14 @@
 //
 // The tile is the dense input gradient's (gemm_dx_tile.h): (64 MI) rows of one
 // expert x 256 columns, the expert's codes expanded and turned on chip, the
-// weight rounded once to bfloat16 after scaling.  Row counts are device data:
-// the grid covers the most tiles that m rows of that many experts can make,
-// and workgroups past the last tile leave at once.
+// weight rounded once to bfloat16 after scaling.
+//
+// Such a tile keeps a compute unit for long (0.46 ms at 14336 weight rows), so a
+// last round that fills a few of them and the experts' partial tiles would cost
+// as much as full ones.  It is taken for full rounds alone, of tiles that are whole or
+// more than half full; the kernel that turns no weights (k_expert_skinny_dx.hip) does the rest, in
+// tiles of 128 rows.  Row counts are device data: both kernels count the tiles
+// from the offsets, and workgroups past the last tile leave at once.
 #include "expert_tiles.h"
 #include "gemm_dx_tile.h"
 
@@ -19,54 +24,66 @@ struct ExpertDxArgs {
   Codebook cb;
 };
 
-template <int MI, bool kDQ, bool kF8>
+constexpr int kTm = kCoverRows, kMI = kTm / 64;
+
+template <bool kDQ, bool kF8>
 __global__ __launch_bounds__(gt::kDxThreads) void k_expert_gemm_dx(ExpertDxArgs a) {
-  constexpr int kTm = 64 * MI;
   __shared__ __align__(16) char stage0[gt::act_stage_bytes<kTm>()], stage1[gt::act_stage_bytes<kTm>()];
   __shared__ __align__(16) char wts[4][2][gt::kWtBytes];
   __shared__ __align__(16) float scl[8][32];
   __shared__ __align__(16) float2 pairs[256 * gt::kPairCopies];
   const int lane = threadIdx.x & 63;
   const int64_t tiles_k = (a.d.cols + gt::kTk - 1) / gt::kTk;
-  const ExpertScan scan = scan_experts(a.er, kTm, lane);
-  const int64_t tiles = tiles_k * scan.tiles;
-  if (static_cast<int64_t>(blockIdx.x) >= tiles) return;
-  const int64_t id = xcd_run(blockIdx.x, tiles);
-  const ExpertTile t = find_expert_tile(a.er, scan, kTm, static_cast<int>(id / tiles_k), lane);
+  const int64_t units = tiles_k * covered_tiles(a.er, lane);
+  if (static_cast<int64_t>(blockIdx.x) >= units) return;
+  const int64_t id = xcd_run(blockIdx.x, units);
+  // tile id / tiles_k
+  int64_t left = id / tiles_k, lo = 0, hi = 0;
+  int e = 0;
+  for (int c = 0; 64 * c < a.er.experts; ++c) {
+    int64_t elo, ehi;
+    expert_range(a.er, c, lane, elo, ehi);
+    const int own = cover_tiles(ehi - elo), upto = wave_prefix(own, lane), here = __builtin_amdgcn_readlane(upto, 63);
+    if (left < here) {
+      const int l = __builtin_ctzll(__ballot(upto > left));
+      e = 64 * c + l;
+      lo = __builtin_amdgcn_readlane(static_cast<int>(elo), l);
+      hi = __builtin_amdgcn_readlane(static_cast<int>(ehi), l);
+      left -= __builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(own, l);
+      break;
+    }
+    left -= here;
+  }
   gt::DxArgs d = a.d;
-  const int64_t w0 = t.e * d.rows * d.cols;  // the expert's first weight
+  const int64_t w0 = e * d.rows * d.cols;  // the expert's first weight
   d.packed += w0 / 2;
   d.blk0 = w0 / 64;
-  d.dy += t.lo * d.rows;
-  d.dx += t.lo * d.cols;
-  d.m = t.hi - t.lo;
-  gt::dx_tile<MI, kDQ, kF8>(d, a.cb, t.row0 - t.lo, id % tiles_k * gt::kTk, stage0, stage1, wts, scl, pairs);
-}
-
-template <int MI>
-hipError_t launch(const ExpertDxArgs& a, hipStream_t s) {
-  const int64_t most = ((a.er.m + 64 * MI - 1) / (64 * MI) + a.er.experts) * ((a.d.cols + gt::kTk - 1) / gt::kTk);
-  if (most > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const dim3 gd(static_cast<unsigned>(most)), bd(gt::kDxThreads);
-  if (a.d.sc.absmax) hipLaunchKernelGGL((k_expert_gemm_dx<MI, false, false>), gd, bd, 0, s, a);
-  else if (a.d.sc.f8) hipLaunchKernelGGL((k_expert_gemm_dx<MI, true, true>), gd, bd, 0, s, a);
-  else hipLaunchKernelGGL((k_expert_gemm_dx<MI, true, false>), gd, bd, 0, s, a);
-  return hipGetLastError();
+  d.dy += lo * d.rows;
+  d.dx += lo * d.cols;
+  d.m = hi - lo;
+  gt::dx_tile<kMI, kDQ, kF8>(d, a.cb, left * kTm, id % tiles_k * gt::kTk, stage0, stage1, wts, scl, pairs);
 }
 
 }  // namespace
 
 hipError_t launch_expert_gemm_dx(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
                                  const uint16_t* dy, uint16_t* dx, hipStream_t s) {
-  // Fewer rows on the mean than a tile go without turning weights on chip: at 256
-  // rows it takes 161 against 134 us here (64 experts of 1024x2048), and 464
-  // against 468 us (8 experts of 14336x4096).
-  if (er.m < 256 * static_cast<int64_t>(er.experts)) return launch_expert_skinny_dx(packed, rows, cols, sc, er, dy, dx, s);
+  // Fewer rows on the mean than a tile: all of it goes without turning weights.
+  if (er.m < kTm * static_cast<int64_t>(er.experts)) return launch_expert_skinny_dx(packed, rows, cols, sc, er, dy, dx, s);
+  const int64_t tiles_k = (cols + gt::kTk - 1) / gt::kTk, most = (er.m / kTm + er.experts) * tiles_k;
+  if (most > 0x7FFFFFFF) return hipErrorInvalidValue;
   ExpertDxArgs a{};
   a.d.packed = packed; a.d.rows = rows; a.d.cols = cols; a.d.sc = sc; a.d.dy = dy; a.d.m = er.m; a.d.dx = dx;
   a.cb = codebook(sc.fp4);
   a.er = er;
-  return launch<4>(a, s);
+  a.er.cover_slots = device_cus();
+  a.er.cover_units = static_cast<int>(tiles_k);
+  const dim3 gd(static_cast<unsigned>(most)), bd(gt::kDxThreads);
+  if (sc.absmax) hipLaunchKernelGGL((k_expert_gemm_dx<false, false>), gd, bd, 0, s, a);
+  else if (sc.f8) hipLaunchKernelGGL((k_expert_gemm_dx<true, true>), gd, bd, 0, s, a);
+  else hipLaunchKernelGGL((k_expert_gemm_dx<true, false>), gd, bd, 0, s, a);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  return launch_expert_skinny_dx(packed, rows, cols, sc, a.er, dy, dx, s);
 }
 
 }  // namespace nf4i

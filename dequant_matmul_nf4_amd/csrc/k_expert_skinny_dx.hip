@@ -79,7 +79,7 @@ __global__ __launch_bounds__(64 * dx_waves<kRt>(), dx_waves<kRt>() / 4) void k_e
   const char* tabc = reinterpret_cast<const char*>(tab);
   const uint32_t slot = static_cast<uint32_t>(lane & (kCopies - 1)) << 3;
 
-  const ExpertScan scan = scan_experts(a.er, kTm, lane);
+  const ExpertScan scan = scan_experts(a.er, kTm, lane, a.er.cover_slots ? covered_tiles(a.er, lane) : 0);
   const int64_t per_tile = (a.cols + unit_cols - 1) / unit_cols;
   const int64_t units = per_tile * scan.tiles;
   if (static_cast<int64_t>(blockIdx.x) >= units) return;

@@ -203,7 +203,12 @@ struct ExpertRows {        // which rows of the product belong to which expert
   const int32_t* offsets;  // [experts + 1]
   int experts;
   int64_t m;               // rows of the product's buffers: offsets are clamped to them
+  // Where two kernels share a product: a first one takes tiles of kCoverRows
+  // rows in full rounds of `cover_slots` workgroups, cover_units of them per
+  // tile, and the other the rest.  0: not shared.
+  int cover_slots, cover_units;
 };
+constexpr int kCoverRows = 256;
 struct ExpertX {           // where the product's row p finds its activations
   const uint16_t* x;       // [rows][cols]
   int64_t rows;
@@ -220,6 +225,7 @@ hipError_t launch_expert_skinny(const uint8_t* packed, int64_t rows, int64_t col
                                 const ExpertX& ex, uint16_t* y, hipStream_t s);
 hipError_t launch_expert_gemm_dx(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
                                  const uint16_t* dy, uint16_t* dx, hipStream_t s);
+// Its form without turning weights on chip, for what the tall tiles leave or all rows.
 hipError_t launch_expert_skinny_dx(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
                                    const uint16_t* dy, uint16_t* dx, hipStream_t s);
 hipError_t launch_expert_combine(const uint16_t* y, int64_t m, const int32_t* position, int64_t tokens, int slots,

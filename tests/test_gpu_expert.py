@@ -149,21 +149,59 @@ def _expert(W, experts, e):
     return nf4.NF4Weight(W.packed[e * n // 2:(e + 1) * n // 2], rows, W.cols, absmax=W.absmax[e * n // 64:(e + 1) * n // 64])
 
 
-def test_many_rows_equal_the_dense_products():
-    """Experts of many rows: bit for bit nf4_gemm and nf4_gemm_dx on each
-    expert's rows (the same tiles and the same order of the sums)."""
+def test_many_rows_equal_the_dense_product():
+    """Experts of many rows: bit for bit nf4_gemm on each expert's rows (the
+    same tiles and the same order of the sums)."""
     torch = need_gpu()
     experts, rows, cols, m = 3, 512, 768, 1500
     W = _stack(torch, experts, rows, cols, "plain")
     off = np.array([0, 700, 700, 1500])
     offsets = torch.from_numpy(off.astype(np.int32)).cuda()
     x = torch.randn((m, cols), device="cuda").bfloat16()
-    dy = torch.randn((m, rows), device="cuda").bfloat16()
-    y, dx = nf4.nf4_expert_gemm(W, experts, x, offsets), nf4.nf4_expert_gemm_dx(W, experts, dy, offsets)
+    y = nf4.nf4_expert_gemm(W, experts, x, offsets)
     for e in (0, 2):
         at = slice(off[e], off[e + 1])
         assert torch.equal(y[at], nf4.nf4_gemm(_expert(W, experts, e), x[at]))
-        assert torch.equal(dx[at], nf4.nf4_gemm_dx(_expert(W, experts, e), dy[at]))
+
+
+@pytest.mark.parametrize("experts,rows,cols,m", [
+    (3, 64, 4096, 4200),      # a little over one round of whole tiles
+    (3, 72, 4096, 6300),      # one round and a half
+    (2, 40, 4160, 7700),      # a last round nearly full
+    (70, 8, 1024, 18500),     # more experts than lanes of a wave
+    (1, 256, 256, 300),       # whole tiles, but far from a round
+])
+@pytest.mark.parametrize("kind", ["even", "one", "uneven"])
+def test_dx_of_many_rows(experts, rows, cols, m, kind):
+    """Sizes where two kernels share the gradient's rows: every row right, rows
+    of no expert left alone, the same bits again."""
+    torch = need_gpu()
+    say("expert dx of many rows", experts, rows, cols, m, kind)
+    W = _stack(torch, experts, rows, cols, "fp8")
+    off = _counts(kind, experts, m - 2) + 1
+    dy = torch.randn((m, rows), device="cuda").bfloat16()
+    offsets = torch.from_numpy(off.astype(np.int32)).cuda()
+    dx = torch.full((m, cols), 7.0, dtype=torch.bfloat16, device="cuda")
+    nf4.nf4_expert_gemm_dx(W, experts, dy, offsets, dx=dx)
+    assert (dx[0] == 7).all() and (dx[m - 1] == 7).all()
+    ref, mag = _reference(torch, W, experts, dy, off, dx=True)
+    _check(dx[1:m - 1], ref, mag, rows)
+    assert torch.equal(dx[1:m - 1], nf4.nf4_expert_gemm_dx(W, experts, dy, offsets)[1:m - 1])
+
+
+@pytest.mark.parametrize("mean", [10, 41, 113, 230])
+def test_every_tile_height(mean):
+    """The forward's kernels by the mean number of rows, one expert with most of them."""
+    torch = need_gpu()
+    experts, rows, cols = 5, 272, 192
+    m = mean * experts
+    W = _stack(torch, experts, rows, cols, "plain", fp4=True)
+    c = np.array([0, m // 2, 1, 0, m - m // 2 - 1])
+    off = np.concatenate([[0], np.cumsum(c)])
+    x = torch.randn((m, cols), device="cuda").bfloat16()
+    y = nf4.nf4_expert_gemm(W, experts, x, torch.from_numpy(off.astype(np.int32)).cuda())
+    ref, mag = _reference(torch, W, experts, x, off)
+    _check(y, ref, mag, cols)
 
 
 @pytest.mark.parametrize("m", [6, 400])
