@@ -115,6 +115,27 @@ __device__ __forceinline__ ExpertTile find_expert_tile(const ExpertRows& er, con
   }
 }
 
+// Number `tile` of the cover_tiles (there are more than that).
+__device__ __forceinline__ ExpertTile find_cover_tile(const ExpertRows& er, int tile, int lane) {
+  ExpertTile t{0, 0, 0, 0};
+  for (int c = 0; 64 * c < er.experts; ++c) {
+    int64_t lo, hi;
+    expert_range(er, c, lane, lo, hi);
+    const int own = cover_tiles(hi - lo), upto = wave_prefix(own, lane), here = __builtin_amdgcn_readlane(upto, 63);
+    if (tile < here) {
+      const int l = __builtin_ctzll(__ballot(upto > tile));
+      t.e = 64 * c + l;
+      t.lo = __builtin_amdgcn_readlane(static_cast<int>(lo), l);
+      t.hi = __builtin_amdgcn_readlane(static_cast<int>(hi), l);
+      tile -= __builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(own, l);
+      t.row0 = t.lo + static_cast<int64_t>(tile) * kCoverRows;
+      return t;
+    }
+    tile -= here;
+  }
+  return t;
+}
+
 // Unit u of n dealt round-robin over the 8 XCDs (as workgroups are): each XCD
 // gets one contiguous run of the units, so that the units it works on at one
 // time are neighbours.

@@ -10,7 +10,9 @@
 //
 // The row counts are device data, so the grid does not depend on them:
 // persistent workgroups count the tiles from the offsets and take theirs,
-// those of one expert's row band next to each other.  The rows of x are
+// those of one expert's row band next to each other.  Of many rows, full rounds
+// of 256-row tiles (whole, or more than half full) go first and a second launch
+// takes what is left in tiles of 128 rows, so that no round runs nearly empty.  The rows of x are
 // gathered by the loads that bring them into LDS, so no sorted copy of x is
 // made.
 #include "expert_tiles.h"
@@ -43,8 +45,11 @@ __global__ __launch_bounds__(kThreads, MI == 2 ? 2 : 1) void k_expert_gemm(Exper
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t slot = static_cast<uint32_t>(lane & (kCopies - 1)) << 3;
   const int64_t tiles_n = (a.rows + kBN - 1) / kBN;
-  const ExpertScan scan = scan_experts(a.er, kBM, lane);
-  const int64_t units = tiles_n * scan.tiles;
+  // MI = 8: the cover tiles of full rounds; else every tile, or what those leave
+  const int covered = a.er.cover_slots ? covered_tiles(a.er, lane) : 0;
+  ExpertScan scan;
+  if constexpr (MI < 8) scan = scan_experts(a.er, kBM, lane, covered);
+  const int64_t units = tiles_n * (MI == 8 ? covered : scan.tiles);
   if (static_cast<int64_t>(blockIdx.x) >= units) return;
   gt::fill_level_pairs<kCopies>(tab, a.cb);  // ends with a barrier
   const float mean = kDQ ? *a.sc.mean : 0.0f;
@@ -52,7 +57,9 @@ __global__ __launch_bounds__(kThreads, MI == 2 ? 2 : 1) void k_expert_gemm(Exper
 
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t id = xcd_run(u, units);
-    const ExpertTile tile = find_expert_tile(a.er, scan, kBM, static_cast<int>(id / tiles_n), lane);
+    ExpertTile tile;
+    if constexpr (MI == 8) tile = find_cover_tile(a.er, static_cast<int>(id / tiles_n), lane);
+    else tile = find_expert_tile(a.er, scan, kBM, static_cast<int>(id / tiles_n), lane);
     const int64_t n0 = id % tiles_n * kBN;
 
     // the lane's pieces of the x tile: rows past the expert's last repeat it (never stored)
@@ -121,7 +128,12 @@ hipError_t launch_expert_gemm(const uint8_t* packed, int64_t rows, int64_t cols,
   ExpertGemmArgs a{};
   a.packed = packed; a.rows = rows; a.cols = cols; a.sc = sc; a.er = er; a.ex = ex; a.y = y;
   a.cb = codebook(sc.fp4);
-  return er.m <= 112 * experts ? launch<2>(a, s) : er.m <= 224 * experts ? launch<4>(a, s) : launch<8>(a, s);
+  if (er.m <= 112 * experts) return launch<2>(a, s);
+  if (er.m <= 224 * experts) return launch<4>(a, s);
+  a.er.cover_slots = device_cus();
+  a.er.cover_units = static_cast<int>((rows + gt::kTileN - 1) / gt::kTileN);
+  if (hipError_t e = launch<8>(a, s); e != hipSuccess) return e;
+  return launch<4>(a, s);
 }
 
 }  // namespace nf4i

@@ -37,31 +37,15 @@ __global__ __launch_bounds__(gt::kDxThreads) void k_expert_gemm_dx(ExpertDxArgs 
   const int64_t units = tiles_k * covered_tiles(a.er, lane);
   if (static_cast<int64_t>(blockIdx.x) >= units) return;
   const int64_t id = xcd_run(blockIdx.x, units);
-  // tile id / tiles_k
-  int64_t left = id / tiles_k, lo = 0, hi = 0;
-  int e = 0;
-  for (int c = 0; 64 * c < a.er.experts; ++c) {
-    int64_t elo, ehi;
-    expert_range(a.er, c, lane, elo, ehi);
-    const int own = cover_tiles(ehi - elo), upto = wave_prefix(own, lane), here = __builtin_amdgcn_readlane(upto, 63);
-    if (left < here) {
-      const int l = __builtin_ctzll(__ballot(upto > left));
-      e = 64 * c + l;
-      lo = __builtin_amdgcn_readlane(static_cast<int>(elo), l);
-      hi = __builtin_amdgcn_readlane(static_cast<int>(ehi), l);
-      left -= __builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(own, l);
-      break;
-    }
-    left -= here;
-  }
+  const ExpertTile t = find_cover_tile(a.er, static_cast<int>(id / tiles_k), lane);
   gt::DxArgs d = a.d;
-  const int64_t w0 = e * d.rows * d.cols;  // the expert's first weight
+  const int64_t w0 = t.e * d.rows * d.cols;  // the expert's first weight
   d.packed += w0 / 2;
   d.blk0 = w0 / 64;
-  d.dy += lo * d.rows;
-  d.dx += lo * d.cols;
-  d.m = hi - lo;
-  gt::dx_tile<kMI, kDQ, kF8>(d, a.cb, left * kTm, id % tiles_k * gt::kTk, stage0, stage1, wts, scl, pairs);
+  d.dy += t.lo * d.rows;
+  d.dx += t.lo * d.cols;
+  d.m = t.hi - t.lo;
+  gt::dx_tile<kMI, kDQ, kF8>(d, a.cb, t.row0 - t.lo, id % tiles_k * gt::kTk, stage0, stage1, wts, scl, pairs);
 }
 
 }  // namespace

@@ -189,6 +189,29 @@ def test_dx_of_many_rows(experts, rows, cols, m, kind):
     assert torch.equal(dx[1:m - 1], nf4.nf4_expert_gemm_dx(W, experts, dy, offsets)[1:m - 1])
 
 
+@pytest.mark.parametrize("experts,rows,cols,m", [
+    (3, 4096, 64, 4200),      # a little over one round of 256-row tiles
+    (2, 4090, 128, 7700),     # a last round nearly full
+    (70, 1000, 64, 18500),    # more experts than lanes of a wave
+    (1, 17, 64, 300),         # far from a round
+])
+@pytest.mark.parametrize("kind", ["even", "one", "uneven"])
+def test_gemm_of_many_rows(experts, rows, cols, m, kind):
+    """Sizes where two launches share the product's rows."""
+    torch = need_gpu()
+    say("expert gemm of many rows", experts, rows, cols, m, kind)
+    W = _stack(torch, experts, rows, cols, "fp8")
+    off = _counts(kind, experts, m - 2) + 1
+    x = torch.randn((200, cols), device="cuda").bfloat16()
+    index = torch.randint(0, 400, (m,), device="cuda", dtype=torch.int32)
+    offsets = torch.from_numpy(off.astype(np.int32)).cuda()
+    y = torch.full((m, rows), 7.0, dtype=torch.bfloat16, device="cuda")
+    nf4.nf4_expert_gemm(W, experts, x, offsets, index=index, slots=2, y=y)
+    assert (y[0] == 7).all() and (y[m - 1] == 7).all()
+    ref, mag = _reference(torch, W, experts, x[(index // 2).long()], off)
+    _check(y[1:m - 1], ref, mag, cols)
+
+
 @pytest.mark.parametrize("mean", [10, 41, 113, 230])
 def test_every_tile_height(mean):
     """The forward's kernels by the mean number of rows, one expert with most of them."""
