@@ -754,6 +754,8 @@ def nf4_expert_gemm(w: NF4Weight, experts: int, x, offsets, index=None, slots: i
     dev = w.device
     if not 1 <= experts <= MAX_EXPERTS or w.rows % experts:
         raise ValueError(f"a weight of {w.rows} rows does not stack {experts} experts")
+    if not 1 <= slots < 2 ** 31:
+        raise ValueError(f"slots = {slots}: at least 1")
     m = x2.shape[0] if index is None else index.numel()
     rows = w.rows // experts
     _need("x", x2, torch.bfloat16, x2.numel(), dev)
@@ -815,7 +817,7 @@ def nf4_expert_combine_backward(dout, y, position, slots: int, weights=None, dy=
                                 stream=None):
     """The gradients of nf4_expert_combine: (dy [m, cols] bf16, dweights
     [tokens, slots] float32); one not in `want` (and not given) is None.  Rows
-    of dy that no position names are not written."""
+    of dy that no position names are not written; no row is named twice."""
     torch = _torch()
     dev = dout.device
     if y.dim() != 2 or slots < 1 or position.numel() % slots:

@@ -37,7 +37,7 @@ __device__ __forceinline__ int cover_tiles(int64_t rows) { return static_cast<in
 
 // How many of these the first of two kernels takes: full rounds of its
 // workgroups, and a last round that fills most of them.
-__device__ __forceinline__ int covered_tiles(const ExpertRows& er, int lane) {
+__device__ __forceinline__ int64_t covered_tiles(const ExpertRows& er, int lane) {
   int64_t all = 0;
   for (int c = 0; 64 * c < er.experts; ++c) {
     int64_t lo, hi;
@@ -45,7 +45,7 @@ __device__ __forceinline__ int covered_tiles(const ExpertRows& er, int lane) {
     all += __builtin_amdgcn_readlane(wave_prefix(cover_tiles(hi - lo), lane), 63);
   }
   const int64_t units = all * er.cover_units, full = units / er.cover_slots * er.cover_slots;
-  return static_cast<int>(3 * (units - full) > 2 * er.cover_slots ? all : full / er.cover_units);
+  return 3 * (units - full) > 2 * er.cover_slots ? all : full / er.cover_units;
 }
 
 // Tiles of the experts 64 c .. 64 c + 63, one expert per lane.
@@ -57,16 +57,16 @@ struct ExpertLane {
 
 // covered: of the cover_tiles, counted expert by expert, the first ones that
 // another kernel takes; the expert's rows begin behind them.
-__device__ __forceinline__ ExpertLane expert_lane(const ExpertRows& er, int c, int tm, int lane, int covered = 0) {
+__device__ __forceinline__ ExpertLane expert_lane(const ExpertRows& er, int c, int tm, int lane, int64_t covered = 0) {
   ExpertLane r;
   if (covered > 0) {
-    int before = 0;
+    int64_t before = 0;
     for (int b = 0; b <= c; ++b) {
       expert_range(er, b, lane, r.lo, r.hi);
       const int own = cover_tiles(r.hi - r.lo), upto = wave_prefix(own, lane);
       if (b == c) {
-        const int mine = covered - before - (upto - own);
-        r.lo += static_cast<int64_t>(mine < 0 ? 0 : mine < own ? mine : own) * kCoverRows;
+        const int64_t mine = covered - before - (upto - own);
+        r.lo += (mine < 0 ? 0 : mine < own ? mine : own) * kCoverRows;
         r.lo = r.lo < r.hi ? r.lo : r.hi;
       }
       before += __builtin_amdgcn_readlane(upto, 63);
@@ -80,14 +80,17 @@ __device__ __forceinline__ ExpertLane expert_lane(const ExpertRows& er, int c, i
 }
 
 // The offsets of the first 64 experts stay in the lanes' registers, so that few
-// experts are read once.  Every lane of a wave calls these.
+// experts are read once.  Every lane of a wave calls these.  Offsets
+// that go up and down can give all rows to every other expert: the tiles of 64
+// experts still fit 31 bits (tiles of fewer than 64 rows are for few rows), those
+// of all take 64.
 struct ExpertScan {
   ExpertLane first;
-  int tiles;    // all tiles
-  int covered;  // tiles that another kernel takes
+  int64_t tiles;    // all tiles
+  int64_t covered;  // tiles that another kernel takes
 };
 
-__device__ __forceinline__ ExpertScan scan_experts(const ExpertRows& er, int tm, int lane, int covered = 0) {
+__device__ __forceinline__ ExpertScan scan_experts(const ExpertRows& er, int tm, int lane, int64_t covered = 0) {
   ExpertScan s;
   s.covered = covered;
   s.first = expert_lane(er, 0, tm, lane, covered);
@@ -96,39 +99,38 @@ __device__ __forceinline__ ExpertScan scan_experts(const ExpertRows& er, int tm,
   return s;
 }
 
-__device__ __forceinline__ ExpertTile find_expert_tile(const ExpertRows& er, const ExpertScan& s, int tm, int tile, int lane) {
+__device__ __forceinline__ ExpertTile find_expert_tile(const ExpertRows& er, const ExpertScan& s, int tm, int64_t tile, int lane) {
   ExpertTile t{-1, 0, 0, 0};
-  int before = 0;
   ExpertLane r = s.first;
   for (int c = 0;; r = expert_lane(er, c, tm, lane, s.covered)) {
     const int here = __builtin_amdgcn_readlane(r.upto, 63);
-    if (tile < before + here) {
-      const int l = __builtin_ctzll(__ballot(before + r.upto > tile));
+    if (tile < here) {
+      const int l = __builtin_ctzll(__ballot(r.upto > static_cast<int>(tile)));
       t.e = 64 * c + l;
       t.lo = __builtin_amdgcn_readlane(static_cast<int>(r.lo), l);
       t.hi = __builtin_amdgcn_readlane(static_cast<int>(r.hi), l);
-      t.row0 = t.lo + static_cast<int64_t>(tile - before - (__builtin_amdgcn_readlane(r.upto, l) - __builtin_amdgcn_readlane(r.tiles, l))) * tm;
+      t.row0 = t.lo + (tile - (__builtin_amdgcn_readlane(r.upto, l) - __builtin_amdgcn_readlane(r.tiles, l))) * tm;
       return t;
     }
-    before += here;
+    tile -= here;
     if (64 * ++c >= er.experts) return t;
   }
 }
 
 // Number `tile` of the cover_tiles (there are more than that).
-__device__ __forceinline__ ExpertTile find_cover_tile(const ExpertRows& er, int tile, int lane) {
+__device__ __forceinline__ ExpertTile find_cover_tile(const ExpertRows& er, int64_t tile, int lane) {
   ExpertTile t{0, 0, 0, 0};
   for (int c = 0; 64 * c < er.experts; ++c) {
     int64_t lo, hi;
     expert_range(er, c, lane, lo, hi);
     const int own = cover_tiles(hi - lo), upto = wave_prefix(own, lane), here = __builtin_amdgcn_readlane(upto, 63);
     if (tile < here) {
-      const int l = __builtin_ctzll(__ballot(upto > tile));
+      const int l = __builtin_ctzll(__ballot(upto > static_cast<int>(tile)));
       t.e = 64 * c + l;
       t.lo = __builtin_amdgcn_readlane(static_cast<int>(lo), l);
       t.hi = __builtin_amdgcn_readlane(static_cast<int>(hi), l);
       tile -= __builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(own, l);
-      t.row0 = t.lo + static_cast<int64_t>(tile) * kCoverRows;
+      t.row0 = t.lo + tile * kCoverRows;
       return t;
     }
     tile -= here;

@@ -49,7 +49,7 @@ __global__ __launch_bounds__(kThreads, MI == 2 ? 2 : 1) void k_expert_gemm(Exper
   const uint32_t slot = static_cast<uint32_t>(lane & (kCopies - 1)) << 3;
   const int64_t tiles_n = (a.rows + kBN - 1) / kBN;
   // MI = 8: the cover tiles of full rounds; else every tile, or what those leave
-  const int covered = a.er.cover_slots ? covered_tiles(a.er, lane) : 0;
+  const int64_t covered = a.er.cover_slots ? covered_tiles(a.er, lane) : 0;
   ExpertScan scan;
   if constexpr (MI < 8) scan = scan_experts(a.er, kBM, lane, covered);
   const int64_t units = tiles_n * (MI == 8 ? covered : scan.tiles);
@@ -61,8 +61,8 @@ __global__ __launch_bounds__(kThreads, MI == 2 ? 2 : 1) void k_expert_gemm(Exper
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t id = xcd_run(u, units);
     ExpertTile tile;
-    if constexpr (MI == 8) tile = find_cover_tile(a.er, static_cast<int>(id / tiles_n), lane);
-    else tile = find_expert_tile(a.er, scan, kBM, static_cast<int>(id / tiles_n), lane);
+    if constexpr (MI == 8) tile = find_cover_tile(a.er, id / tiles_n, lane);
+    else tile = find_expert_tile(a.er, scan, kBM, id / tiles_n, lane);
     const int64_t n0 = id % tiles_n * kBN;
 
     // the lane's pieces of the x tile: rows past the expert's last repeat it (never stored)

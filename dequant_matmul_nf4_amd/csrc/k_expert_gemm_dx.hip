@@ -40,7 +40,7 @@ __global__ __launch_bounds__(gt::kDxThreads) void k_expert_gemm_dx(ExpertDxArgs 
   const int64_t units = tiles_k * covered_tiles(a.er, lane);
   if (static_cast<int64_t>(blockIdx.x) >= units) return;
   const int64_t id = xcd_run(blockIdx.x, units);
-  const ExpertTile t = find_cover_tile(a.er, static_cast<int>(id / tiles_k), lane);
+  const ExpertTile t = find_cover_tile(a.er, id / tiles_k, lane);
   gt::DxArgs d = a.d;
   const int64_t w0 = t.e * d.rows * d.cols;  // the expert's first weight
   d.packed += w0 / 2;
@@ -58,7 +58,7 @@ hipError_t launch_expert_gemm_dx(const uint8_t* packed, int64_t rows, int64_t co
   // Fewer rows on the mean than a tile: all of it goes without turning weights.
   if (er.m < kTm * static_cast<int64_t>(er.experts)) return launch_expert_skinny_dx(packed, rows, cols, sc, er, dy, dx, s);
   const int64_t tiles_k = (cols + gt::kTk - 1) / gt::kTk, most = (er.m / kTm + er.experts) * tiles_k;
-  if (most > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (most * gt::kDxThreads > 0xFFFFFFFF) return hipErrorInvalidValue;  // a grid's threads are counted in 32 bits
   ExpertDxArgs a{};
   a.d.packed = packed; a.d.rows = rows; a.d.cols = cols; a.d.sc = sc; a.d.dy = dy; a.d.m = er.m; a.d.dx = dx;
   a.cb = codebook(sc.fp4);

@@ -183,7 +183,7 @@ __global__ __launch_bounds__(256) void k_combine(const uint16_t* __restrict__ y,
                                                  const int32_t* __restrict__ position, int64_t tokens, int slots,
                                                  int64_t cols, const float* __restrict__ weights,
                                                  uint16_t* __restrict__ out, int lanes) {
-  const int64_t token = static_cast<int64_t>(blockIdx.x) * (256 / lanes) + threadIdx.x / lanes;
+  const int64_t token = block_number() * (256 / lanes) + threadIdx.x / lanes;
   if (token >= tokens) return;
   const int32_t* pos = position + token * slots;
   const float* wt = weights ? weights + token * slots : nullptr;
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(256) void k_combine_backward(const uint16_t* __rest
                                                           int64_t cols, const float* __restrict__ weights,
                                                           uint16_t* __restrict__ dy, float* __restrict__ dweights) {
   const int lane = threadIdx.x & 63;
-  const int64_t s = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t s = block_number() * 4 + (threadIdx.x >> 6);
   if (s >= n) return;
   const int64_t p = position[s], token = s / slots;
   const bool live = p >= 0 && p < m;
@@ -275,8 +275,7 @@ hipError_t launch_expert_combine(const uint16_t* y, int64_t m, const int32_t* po
   int lanes = 8;
   while (lanes < 256 && lanes * 8 < cols) lanes <<= 1;
   const int64_t blocks = (tokens + 256 / lanes - 1) / (256 / lanes);
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(k_combine, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, y, m, position, tokens, slots, cols,
+  hipLaunchKernelGGL(k_combine, block_grid(blocks), dim3(256), 0, s, y, m, position, tokens, slots, cols,
                      weights, out, lanes);
   return hipGetLastError();
 }
@@ -286,8 +285,7 @@ hipError_t launch_expert_combine_backward(const uint16_t* dout, const uint16_t* 
                                           float* dweights, hipStream_t s) {
   const int64_t n = tokens * slots;
   const int64_t blocks = (n + 3) / 4;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(k_combine_backward, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, dout, y, m, position, n,
+  hipLaunchKernelGGL(k_combine_backward, block_grid(blocks), dim3(256), 0, s, dout, y, m, position, n,
                      slots, cols, weights, dy, dweights);
   return hipGetLastError();
 }

@@ -125,7 +125,7 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_expert_skinny(SkinnyArgs a)
   // the part of the run that lies in one tile
   for (int64_t next; at < end; at = next) {
     const int64_t tid = at / ngr, j0 = at - tid * ngr;
-    const ExpertTile tile = find_expert_tile(a.er, scan, sk::kRows, static_cast<int>(tid), lane);
+    const ExpertTile tile = find_expert_tile(a.er, scan, sk::kRows, tid, lane);
     next = at + (ngr - j0) < end ? at + (ngr - j0) : end;
     const int ng = static_cast<int>(next - at);
     const int cnt = static_cast<int>(tile.hi - tile.row0 < sk::kRows ? tile.hi - tile.row0 : sk::kRows);  // rows of x

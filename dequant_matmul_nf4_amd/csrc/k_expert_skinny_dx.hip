@@ -116,7 +116,7 @@ __global__ __launch_bounds__(64 * dx_waves<kRt>(), dx_waves<kRt>() / 4) void k_e
   uint32_t cl, cb, dyo[kRt];
   auto take_unit = [&](int64_t u) {
     const int64_t id = xcd_run(u, units);
-    const ExpertTile tile = find_expert_tile(a.er, scan, kTm, static_cast<int>(id / per_tile), lane);
+    const ExpertTile tile = find_expert_tile(a.er, scan, kTm, id / per_tile, lane);
     row0 = tile.row0;
     col0 = id % per_tile * unit_cols;
     w0 = tile.e * a.rows + n_lo;

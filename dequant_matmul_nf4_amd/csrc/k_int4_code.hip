@@ -74,7 +74,7 @@ template <int kType>
 __global__ __launch_bounds__(256) void k_int4_quantize(const void* __restrict__ x, int64_t n, int shift,
                                                        uint8_t* __restrict__ packed, void* __restrict__ scales,
                                                        int scale_type, uint8_t* __restrict__ zeros) {
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 16;
+  const int64_t i = (block_number() * 256 + threadIdx.x) * 16;
   // groups are whole: the lanes of one are all here or all past the end
   if (i >= n) return;
   float v[16];
@@ -137,7 +137,7 @@ constexpr int kUnroll = 4;
 template <int kType>
 __global__ __launch_bounds__(256) void k_int4_dequantize(Int4Weight w, int shift, int64_t n, void* __restrict__ out) {
   constexpr int kPer = kType == 0 ? 4 : 8;
-  const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * (256 * kUnroll) + threadIdx.x) * kPer;
+  const int64_t i0 = (block_number() * (256 * kUnroll) + threadIdx.x) * kPer;
   uint32_t c[kUnroll];
   float s[kUnroll];
   int z[kUnroll];
@@ -185,9 +185,8 @@ static int shift_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
 hipError_t launch_int4_quantize(const void* x, int x_type, int64_t n, int group, uint8_t* packed, void* scales,
                                 int scale_type, uint8_t* zeros, hipStream_t s) {
   const int64_t blocks = (n + 4095) / 4096;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   const int shift = shift_of(group);
-  const dim3 gd(static_cast<unsigned>(blocks)), bd(256);
+  const dim3 gd = block_grid(blocks), bd(256);
   if (x_type == 0) hipLaunchKernelGGL((k_int4_quantize<0>), gd, bd, 0, s, x, n, shift, packed, scales, scale_type, zeros);
   else if (x_type == 1) hipLaunchKernelGGL((k_int4_quantize<1>), gd, bd, 0, s, x, n, shift, packed, scales, scale_type, zeros);
   else hipLaunchKernelGGL((k_int4_quantize<2>), gd, bd, 0, s, x, n, shift, packed, scales, scale_type, zeros);
@@ -198,8 +197,7 @@ hipError_t launch_int4_dequantize(const Int4Weight& w, void* out, int out_type, 
   const int64_t n = w.rows * w.cols;
   const int per = (out_type == 0 ? 1024 : 2048) * kUnroll;
   const int64_t blocks = (n + per - 1) / per;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const dim3 gd(static_cast<unsigned>(blocks)), bd(256);
+  const dim3 gd = block_grid(blocks), bd(256);
   if (out_type == 0) hipLaunchKernelGGL((k_int4_dequantize<0>), gd, bd, 0, s, w, shift_of(w.group), n, out);
   else if (out_type == 1) hipLaunchKernelGGL((k_int4_dequantize<1>), gd, bd, 0, s, w, shift_of(w.group), n, out);
   else hipLaunchKernelGGL((k_int4_dequantize<2>), gd, bd, 0, s, w, shift_of(w.group), n, out);

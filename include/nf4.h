@@ -386,8 +386,10 @@ int nf4_lora_merge(const nf4_weight* w, const void* lora_a, const void* lora_b, 
  * e is rows e * R .. (e + 1) * R - 1 with R = w->rows / experts (quantize the
  * [experts * R][cols] matrix; the second level of the scales is then common).
  * offsets[e] .. offsets[e + 1] - 1 are the product's rows of expert e; offsets
- * outside 0 .. m or descending are clamped.  Rows of the outputs that belong
- * to no expert are left as they were. */
+ * outside 0 .. m are clamped; where they descend, which expert's product a row
+ * gets is not defined, and no access leaves the buffers.  Rows of the outputs
+ * that belong to no expert are left as they were, and such rows of the inputs
+ * are not read. */
 
 #define NF4_MAX_EXPERTS 1024
 

@@ -477,3 +477,92 @@ def test_weight_past_32_bit_offsets():
     dx = nf4.nf4_expert_gemm_dx(W, experts, y, offsets)
     assert (dx[0] == 0).all()
     _check(dx[1:], y[1:].double() @ w, y[1:].double().abs() @ w.abs(), rows)
+
+
+@pytest.mark.parametrize("experts,m", [(6, 12), (6, 300), (4, 2000)])
+def test_offsets_that_descend_stay_inside(experts, m):
+    """All rows given to every other expert: a row gets some expert's product,
+    and nothing around the outputs is touched."""
+    torch = need_gpu()
+    rows, cols, pad = 64, 128, 8
+    W = _stack(torch, experts, rows, cols, "plain")
+    offsets = torch.tensor([0, m] * (experts // 2) + [0], dtype=torch.int32, device="cuda")
+    x = torch.randn((m, cols), device="cuda").bfloat16()
+    dy = torch.randn((m, rows), device="cuda").bfloat16()
+    y = torch.full((m + 2 * pad, rows), 7.0, dtype=torch.bfloat16, device="cuda")
+    dx = torch.full((m + 2 * pad, cols), 7.0, dtype=torch.bfloat16, device="cuda")
+    nf4.nf4_expert_gemm(W, experts, x, offsets, y=y[pad:m + pad])
+    nf4.nf4_expert_gemm_dx(W, experts, dy, offsets, dx=dx[pad:m + pad])
+    for out in (y, dx):
+        assert (out[:pad] == 7).all() and (out[m + pad:] == 7).all()
+    each = [torch.tensor([0] * (e + 1) + [m] * (experts - e), dtype=torch.int32, device="cuda") for e in range(0, experts, 2)]
+    ys = torch.stack([nf4.nf4_expert_gemm(W, experts, x, o) for o in each])
+    assert (y[pad:m + pad] == ys).any(0).all()
+
+
+@pytest.mark.parametrize("m", [16, 300, 1400])
+def test_rows_stay_apart(m):
+    """Infinities and NaN in one row of x or dy, and in rows of no expert, reach
+    no other row."""
+    torch = need_gpu()
+    experts, rows, cols = 4, 256, 640
+    W = _stack(torch, experts, rows, cols)
+    off = np.array([3, 5, m // 2, m // 2, m - 4])
+    offsets = torch.from_numpy(off.astype(np.int32)).cuda()
+    for call, k in ((nf4.nf4_expert_gemm, cols), (nf4.nf4_expert_gemm_dx, rows)):
+        x = torch.randn((m, k), device="cuda").bfloat16()
+        clean = call(W, experts, x, offsets)
+        bad = [5, m - 6]
+        x[bad[0], k // 2] = float("inf")
+        x[bad[1]] = float("nan")
+        x[:3] = float("nan")
+        x[m - 4:] = float("nan")
+        got = call(W, experts, x, offsets)
+        good = torch.ones(m, dtype=torch.bool, device="cuda")
+        good[bad] = False
+        good[:3] = False
+        good[m - 4:] = False
+        assert torch.equal(got[good], clean[good])
+        assert not got[bad].isfinite().any()
+
+
+def test_dropped_slots_hide_what_is_not_finite():
+    """NaN in a dropped slot's weight and in rows that no position names."""
+    torch = need_gpu()
+    tokens, slots, cols, m = 5, 3, 264, 20
+    position = torch.arange(tokens * slots, dtype=torch.int32, device="cuda").view(tokens, slots)
+    y = torch.randn((m, cols), device="cuda").bfloat16()
+    weights = torch.rand((tokens, slots), device="cuda")
+    dout = torch.randn((tokens, cols), device="cuda").bfloat16()
+    position[1, 2], position[3, 0], position[4] = -1, m, -5
+    dropped = (position < 0) | (position >= m)
+    y[15:] = float("nan")
+    y[[5, 9]] = float("nan")
+    weights[dropped] = float("nan")
+    out = nf4.nf4_expert_combine(y, position, slots, weights)
+    dy, dweights = nf4.nf4_expert_combine_backward(dout, y, position, slots, weights, dy=torch.full_like(y, 7.0))
+    assert out.isfinite().all() and (out[4] == 0).all()
+    assert dweights.isfinite().all() and (dweights[dropped] == 0).all()
+    named = torch.zeros(m, dtype=torch.bool, device="cuda")
+    named[position[~dropped].long()] = True
+    assert dy[named].isfinite().all() and (dy[~named] == 7).all()
+
+
+def test_combine_of_more_slots_than_one_grid_dimension_counts():
+    """2^26 slots and a few: one wave each in the backward sum is more than 2^32
+    threads.  A gate's gradient is a float32 sum of 8 products, in any order: 8
+    products and 7 additions, each off by 2^-24."""
+    torch = need_gpu()
+    n, cols, tail = 2 ** 26 + 5, 8, 1000
+    position = torch.arange(n - 1, -1, -1, dtype=torch.int32, device="cuda")
+    y = torch.randn((n, cols), dtype=torch.bfloat16, device="cuda")
+    dout = torch.randn((n, cols), dtype=torch.bfloat16, device="cuda")
+    weights = torch.rand(n, device="cuda")
+    out = nf4.nf4_expert_combine(y, position, 1, weights)
+    dy, dweights = nf4.nf4_expert_combine_backward(dout, y, position, 1, weights)
+    for at in (slice(0, tail), slice(n // 2, n // 2 + tail), slice(n - tail, n)):
+        rows, w = position[at].long(), weights[at, None]
+        assert torch.equal(out[at], (w * y[rows].float()).bfloat16())
+        assert torch.equal(dy[rows], (w * dout[at].float()).bfloat16())
+        p = dout[at].double() * y[rows].double()
+        assert ((dweights[at, 0].double() - p.sum(1)).abs() <= 15 * 2.0 ** -24 * p.abs().sum(1) + 1e-30).all()

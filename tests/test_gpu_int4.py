@@ -224,3 +224,20 @@ def test_int4_graph_and_side_stream():
     side.synchronize()
     del junk
     assert torch.equal(got, y)
+
+
+def test_int4_coding_of_more_blocks_than_one_grid_dimension():
+    """A weight of more than 2^32 values: its first and last rows as if alone."""
+    torch = need_gpu()
+    rows, cols, few = 65600, 65536, 40
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    for at in (slice(0, few), slice(rows - few, rows)):
+        x[at] = torch.randn((few, cols), device="cuda").bfloat16()
+    W = nf4.quantize_int4(x, group=64, symmetric=False)
+    out = nf4.nf4_int4_dequantize(W)
+    for at in (slice(0, few), slice(rows - few, rows)):
+        one = nf4.quantize_int4(x[at], group=64, symmetric=False)
+        assert torch.equal(W.packed.view(rows, -1)[at], one.packed.view(few, -1))
+        assert torch.equal(W.scales[at], one.scales) and torch.equal(W.zeros[at], one.zeros)
+        assert torch.equal(out[at], nf4.nf4_int4_dequantize(one))
+    assert not out[few:rows - few].any()
