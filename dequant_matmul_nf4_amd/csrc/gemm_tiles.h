@@ -138,7 +138,7 @@ __device__ __forceinline__ void zero_acc(floatx16 (&acc)[MI][2]) {
 // element e at output column (e % 4) + 4 (lane / 32) + 8 (e / 4) and output
 // row lane % 32: four consecutive columns per group of four e, written as one
 // 8-byte store when the row holds them all and is 8-byte aligned.
-template <int MI>
+template <int MI, bool kSwap = false>
 __device__ __forceinline__ void store_acc(const floatx16 (&acc)[MI][2], uint16_t* out, int64_t m, int64_t ncols,
                                           int64_t m0, int64_t c0, int wave, int lane) {
   const bool vec = (ncols & 3) == 0;
@@ -152,8 +152,8 @@ __device__ __forceinline__ void store_acc(const floatx16 (&acc)[MI][2], uint16_t
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int64_t col = c0 + wave * 64 + j * 32 + 4 * (lane >> 5) + 8 * g;
-        const uint32_t p0 = bf16_pair(acc[i][j][4 * g], acc[i][j][4 * g + 1]);
-        const uint32_t p1 = bf16_pair(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
+        const uint32_t p0 = bf16_pair(acc[i][j][4 * g + kSwap], acc[i][j][4 * g + 1 - kSwap]);
+        const uint32_t p1 = bf16_pair(acc[i][j][4 * g + 2 + kSwap], acc[i][j][4 * g + 3 - kSwap]);
         if (vec && col + 3 < ncols) {
           *reinterpret_cast<uint2*>(orow + col) = make_uint2(p0, p1);
         } else {

@@ -1,4 +1,4 @@
-// The input gradient grouped by expert for few rows per expert:
+// The input gradient grouped by expert for few tiles:
 //
 //   dx[p] = dy[p] . deq(W_e)     for offsets[e] <= p < offsets[e + 1]
 //
@@ -17,10 +17,10 @@
 // Bound: reading the codes, so waves work on their own (no barrier in the loop)
 // with the next steps' loads on their way; a workgroup's 8 waves are 1 or 2
 // column chunks x 8 or 4 slices of the reduction, whose partial tiles are added
-// in slice order at the end.  16 rows over 8 experts of 14336x4096: 84 us; 4096 rows
-// over 64 experts of 1024x2048: 72 us, where expanding the weights once per tile
-// of 64 rows keeps the VALU busy 45% of the time.  In tall tiles the loads of dy,
-// 16 lines each, add up to as much as the products.
+// in slice order at the end.  16 rows over 8 experts of 14336x4096: 84 us; 512: 210
+// us (253 us with whole reductions on half of the compute units,
+// k_expert_gemm_dx.hip).  In tall tiles the loads of dy, 16 lines each, add up to
+// as much as the products.
 #include "expert_tiles.h"
 #include "skinny_tile.h"
 
@@ -82,7 +82,7 @@ __global__ __launch_bounds__(64 * dx_waves<kRt>(), dx_waves<kRt>() / 4) void k_e
   const char* tabc = reinterpret_cast<const char*>(tab);
   const uint32_t slot = static_cast<uint32_t>(lane & (kCopies - 1)) << 3;
 
-  const ExpertScan scan = scan_experts(a.er, kTm, lane, a.er.cover_slots ? covered_tiles(a.er, lane) : 0);
+  const ExpertScan scan = scan_experts(a.er, kTm, lane);
   const int64_t per_tile = (a.cols + unit_cols - 1) / unit_cols;
   const int64_t units = per_tile * scan.tiles;
   if (static_cast<int64_t>(blockIdx.x) >= units) return;

@@ -225,7 +225,7 @@ hipError_t launch_expert_skinny(const uint8_t* packed, int64_t rows, int64_t col
                                 const ExpertX& ex, uint16_t* y, hipStream_t s);
 hipError_t launch_expert_gemm_dx(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
                                  const uint16_t* dy, uint16_t* dx, hipStream_t s);
-// Its form without turning weights on chip, for what the tall tiles leave or all rows.
+// Its form for few tiles: the reduction split over the waves of a workgroup.
 hipError_t launch_expert_skinny_dx(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
                                    const uint16_t* dy, uint16_t* dx, hipStream_t s);
 hipError_t launch_expert_combine(const uint16_t* y, int64_t m, const int32_t* position, int64_t tokens, int slots,

@@ -566,3 +566,66 @@ def test_combine_of_more_slots_than_one_grid_dimension_counts():
         assert torch.equal(dy[rows], (w * dout[at].float()).bfloat16())
         p = dout[at].double() * y[rows].double()
         assert ((dweights[at, 0].double() - p.sum(1)).abs() <= 15 * 2.0 ** -24 * p.abs().sum(1) + 1e-30).all()
+
+
+@pytest.mark.parametrize("experts,rows,cols,m", [
+    (300, 8, 576, 700), (70, 40, 2112, 900), (16, 200, 4160, 640), (64, 1032, 1088, 3000), (9, 64, 8192, 500),  # 64-row tiles
+    (20, 72, 1600, 3000), (9, 520, 2368, 1500), (4, 1000, 8128, 600),                                        # 128-row tiles
+    (3, 136, 4096, 4200), (1, 56, 16384, 1030),                                                            # 256- and 64-row tiles
+])
+@pytest.mark.parametrize("kind", ["even", "one", "uneven"])
+def test_dx_of_every_tile_height(experts, rows, cols, m, kind):
+    """Reductions that end inside a step, columns that end inside a tile, each
+    form of the scales; rows of no expert left, the same bits again."""
+    torch = need_gpu()
+    say("expert dx by tile height", experts, rows, cols, m, kind)
+    for i, scales in enumerate(("int8", "fp8", "plain")):
+        W = _stack(torch, experts, rows, cols, scales, fp4=(m + i) % 2 == 0)
+        off = _counts(kind, experts, m - 2) + 1
+        dy = torch.randn((m, rows), device="cuda").bfloat16()
+        offsets = torch.from_numpy(off.astype(np.int32)).cuda()
+        dx = torch.full((m, cols), 7.0, dtype=torch.bfloat16, device="cuda")
+        nf4.nf4_expert_gemm_dx(W, experts, dy, offsets, dx=dx)
+        assert (dx[0] == 7).all() and (dx[m - 1] == 7).all()
+        ref, mag = _reference(torch, W, experts, dy, off, dx=True)
+        _check(dx[1:m - 1], ref, mag, rows)
+        assert torch.equal(dx[1:m - 1], nf4.nf4_expert_gemm_dx(W, experts, dy, offsets)[1:m - 1])
+
+
+def test_dx_of_one_hot_rows_is_the_weight():
+    """dy of ones in single places: the rows of the weight, rounded once to
+    bfloat16, in every place of a step and of a tile."""
+    torch = need_gpu()
+    experts, rows, cols = 5, 200, 8256
+    W = _stack(torch, experts, rows, cols, "fp8")
+    m = experts * rows
+    dy = torch.eye(rows, device="cuda").bfloat16().repeat(experts, 1)
+    offsets = torch.arange(experts + 1, dtype=torch.int32, device="cuda") * rows
+    assert torch.equal(nf4.nf4_expert_gemm_dx(W, experts, dy, offsets), nf4.nf4_dequantize(W, out_dtype=torch.float32).bfloat16())
+    # many small experts: 64-row tiles
+    small = 8
+    one = torch.eye(small, device="cuda").bfloat16().repeat(m // small, 1)
+    offsets = torch.arange(m // small + 1, dtype=torch.int32, device="cuda") * small
+    assert torch.equal(nf4.nf4_expert_gemm_dx(W, m // small, one, offsets), nf4.nf4_dequantize(W, out_dtype=torch.float32).bfloat16())
+
+
+def test_dx_of_a_weight_past_32_bit_offsets():
+    """As above for products of whole tiles: the last expert's weights and scales."""
+    torch = need_gpu()
+    experts, rows, cols, m = 33, 16384, 8192, 600
+    n = experts * rows * cols
+    packed = torch.zeros(n // 2, dtype=torch.uint8, device="cuda").fill_(0x77)
+    absmax = torch.ones(n // 64, device="cuda")
+    last = (experts - 1) * rows * cols
+    packed[last // 2:].random_(0, 256)
+    absmax[last // 64:] = torch.rand(rows * cols // 64, device="cuda") + 0.5
+    W = nf4.NF4Weight(packed, experts * rows, cols, absmax=absmax)
+    one = nf4.NF4Weight(packed[last // 2:], rows, cols, absmax=absmax[last // 64:])
+    dy = torch.randn((m, rows), device="cuda").bfloat16()
+    offsets = torch.zeros(experts + 1, dtype=torch.int32, device="cuda")
+    offsets[experts - 1:] = torch.tensor([100, m], dtype=torch.int32)
+    dx = nf4.nf4_expert_gemm_dx(W, experts, dy, offsets)
+    assert (dx[:100] == 0).all()
+    w = nf4.nf4_dequantize(one, out_dtype=torch.float32).double()
+    d = dy[100:].double()
+    _check(dx[100:], d @ w, d.abs() @ w.abs(), rows)
