@@ -14,15 +14,17 @@
 // the sums).  A wave's 64 columns are one block of a weight row, so a step has 64
 // scales, one made by each lane and read back from LDS.
 //
-// The codes come from HBM and are requested three steps ahead, dy one.  As in the
-// forward product, tiles are counted from the offsets, and of many rows full
-// rounds of 256-row tiles go first and 64-row tiles take the rest.
+// A wave is alone on its SIMD (two waves at 64 rows), so what it does besides the
+// products is spelled out between them, one lookup, one read of dy, or one pair
+// expanded at a time; left to the compiler it collects behind them (8192 rows over
+// 8 experts of 14336x4096: 1110 us; in place 962 us).  The codes come from HBM and
+// are requested three steps ahead, dy one to two.  As in the forward product,
+// tiles are counted from the offsets, and of many rows full rounds of 256-row
+// tiles go first and 64-row tiles take the rest.
 //
-// Bound: the matrix cores are busy 47% of the cycles, like the forward product's;
-// a wave's waits for LDS and at barriers are 22%, its own instructions between
-// the products the rest.  8192 rows over 8 experts of 14336x4096: 1140 us, 845
-// TFLOP/s; 4096 over 64 of 1024x2048: 50 us.  Expanding to bfloat16 and turning
-// that in LDS, 8 waves a tile, took 1240 and 85.
+// Bound: the matrix cores.  8192 rows over 8 experts of 14336x4096: 962 us, 1000
+// TFLOP/s; 4096 over 64 of 1024x2048: 46 us.  Expanding to bfloat16 first and
+// turning that in LDS, 8 waves a tile, took 1240 and 85.
 #include "expert_tiles.h"
 #include "gemm_fwd.h"
 #include "skinny_tile.h"
@@ -122,7 +124,9 @@ __global__ __launch_bounds__(gt::kThreads, MI == 2 ? 2 : 1) void k_expert_gemm_d
   const uint32_t ld = static_cast<uint32_t>(a.rows * 2);
   float* scl = &scl_all[wave][0][0];
   const float* raw = &raw_all[wave][0][0][0];
-  const uint32_t raw0 = lds_address(raw);
+  // where the wave's requests go
+  const uint32_t raw0 = lds_address(raw), codes0 = lds_address(cs_all[0]) + 2 * wave * 1024;
+  const uint32_t dst0 = lds_address(xs0) + MI * wave * 1024, dst1 = lds_address(xs1) + MI * wave * 1024;
   const uint32_t sw = ((lane & 31) >> 1) & 7, h4 = (lane >> 5) * 4;
   // where the lane reads the codes it turns: row 32 h + 16 t + lane % 16, 16-byte
   // piece 2 wave + j of the row at slot piece ^ (row % 8)
@@ -141,69 +145,54 @@ __global__ __launch_bounds__(gt::kThreads, MI == 2 ? 2 : 1) void k_expert_gemm_d
     const uint8_t* cop = a.packed + tile.e * a.rows * row_bytes;
     int64_t blk = tile.e * a.rows * nblk + (k0 / 64 + wave < nblk ? k0 / 64 + wave : nblk - 1);
     int dy_left = static_cast<int>(a.rows), co_left = dy_left, sc_left = dy_left;
-    // the lane's piece of a row of codes (pieces past the row's end repeat its
-    // last: such columns are not stored)
+    // Offsets of the lane's requests.  Those past the weight's rows repeat the last
+    // ones (of dy the last 8 of the same row); their scales are 0.  Pieces past the
+    // end of a row of codes repeat its last: such columns are not stored.
     const uint32_t cp = static_cast<uint32_t>(k0 / 32) + ((lane & 7) ^ (lane >> 3));
-    const uint32_t coff = (cp < row_bytes / 16 ? cp : row_bytes / 16 - 1) * 16 + (16 * wave + (lane >> 3)) * row_bytes;
-    uint32_t off[MI];
+    const uint32_t cpiece = (cp < row_bytes / 16 ? cp : row_bytes / 16 - 1) * 16, crow = (16 * wave + (lane >> 3)) * row_bytes;
+    const uint32_t piece[2] = {static_cast<uint32_t>(gt::act_piece(0, lane)) << 4, static_cast<uint32_t>(gt::act_piece(1, lane)) << 4};
+    uint32_t drow[MI];
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       const int r = 8 * (MI * wave + i) + (lane >> 3);
-      off[i] = static_cast<uint32_t>(r < cnt ? r : cnt - 1) * ld + (gt::act_piece(MI * wave + i, lane) << 4);
+      drow[i] = static_cast<uint32_t>(r < cnt ? r : cnt - 1) * ld;
     }
-    // Requests past the weight's rows repeat the last ones (of dy the last 8 of
-    // the same row); their scales are 0.  Past the last step they repeat it.
-    auto dma_dy = [&](char* stage) {
-      const uint32_t to = lds_address(stage) + MI * wave * 1024;
-      if (dy_left >= kStep) {
-#pragma unroll
-        for (int i = 0; i < MI; ++i) dma16(dyp, off[i], to + i * 1024);
-      } else {
-        const int l2 = opaque(lane);
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          const int r = 8 * (MI * wave + i) + (l2 >> 3), piece = gt::act_piece(MI * wave + i, l2), last = dy_left / 8 - 1;
-          dma16(dyp, static_cast<uint32_t>(r < cnt ? r : cnt - 1) * ld + ((piece < last ? piece : last) << 4), to + i * 1024);
-        }
-      }
-      if (dy_left > kStep) {
-        dyp += kStep * 2;
-        dy_left -= kStep;
+    auto least = [](uint32_t x, uint32_t y) { return x < y ? x : y; };
+    // Each of these requests a part of the next step's data, the last one moves on
+    // (past the last step: it stays).
+    uint32_t dy_last = 0, co_last = 0;  // of the step that is requested: the last piece of a row, the last row
+    auto dma_dy = [&](int i, uint32_t stage) {
+      if (i == 0) dy_last = (static_cast<uint32_t>(dy_left < kStep ? dy_left : kStep) - 8) * 2;
+      dma16(dyp, drow[i] + least(piece[i & 1], dy_last), stage + i * 1024);
+      if (i == MI - 1) {
+        const int by = dy_left > kStep ? kStep : 0;
+        dyp += by * 2;
+        dy_left -= by;
       }
     };
-    auto dma_codes = [&](int stage) {
-      const uint32_t to = lds_address(cs_all[0]) + stage * kCodeStage + 2 * wave * 1024;
-      if (co_left >= kStep) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) dma16(cop, coff + i * 8 * row_bytes, to + i * 1024);
-      } else {
-        const int l2 = opaque(lane);
-        const uint32_t at = coff - (16 * wave + (lane >> 3)) * row_bytes;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = 16 * wave + 8 * i + (l2 >> 3);
-          dma16(cop, at + static_cast<uint32_t>(r < co_left ? r : co_left - 1) * row_bytes, to + i * 1024);
-        }
-      }
-      if (co_left > kStep) {
-        cop += kStep * static_cast<int64_t>(row_bytes);
-        co_left -= kStep;
+    auto dma_codes = [&](int i, int stage) {
+      if (i == 0) co_last = static_cast<uint32_t>((co_left < kStep ? co_left : kStep) - 1) * row_bytes;
+      dma16(cop, cpiece + least(crow + i * 8 * row_bytes, co_last), codes0 + stage * kCodeStage + i * 1024);
+      if (i == 1) {
+        const int by = co_left > kStep ? kStep : 0;
+        cop += by * static_cast<int64_t>(row_bytes);
+        co_left -= by;
       }
     };
     // lane n: the scale of the step's weight row n in the wave's block
+    const uint32_t srow = lane * nblk;
     auto dma_scale = [&](int ks) {
       const uint32_t to = raw0 + (ks & 1) * sizeof(raw_all[0][0]);
-      const uint32_t o = static_cast<uint32_t>(lane < sc_left ? lane : sc_left - 1) * nblk;
+      const uint32_t o = least(srow, static_cast<uint32_t>((sc_left < kStep ? sc_left : kStep) - 1) * nblk);
       if constexpr (kDQ) {
         dma1(a.sc.q + blk, o, to);
         dma4(a.sc.absmax2 + (blk >> 8), (static_cast<uint32_t>(blk & 255) + o) >> 8 << 2, to + 4 * kStep);
       } else {
         dma4(a.sc.absmax + blk, o << 2, to);
       }
-      if (sc_left > kStep) {
-        blk += kStep * static_cast<int64_t>(nblk);
-        sc_left -= kStep;
-      }
+      const int by = sc_left > kStep ? kStep : 0;
+      blk += by * static_cast<int64_t>(nblk);
+      sc_left -= by;
     };
     auto put_scale = [&](int ks) {
       const float* r = raw + (ks & 1) * (sizeof(raw_all[0][0]) / 4) + lane;
@@ -221,100 +210,116 @@ __global__ __launch_bounds__(gt::kThreads, MI == 2 ? 2 : 1) void k_expert_gemm_d
       s[0] = *reinterpret_cast<const floatx4*>(p);
       s[1] = *reinterpret_cast<const floatx4*>(p + 4);
     };
-    auto turn_step = [&](u32x4 (&w)[2], const char* stage) {
+    // words 2 t, 2 t + 1 of both columns: reduction steps 2 t, 2 t + 1
+    u32x4 w[2];
+    auto turn_half = [&](int t, const char* stage) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint2 lo = turn_codes(stage + (turn ^ (16 * j))), hi = turn_codes(stage + (turn ^ (16 * j)) + 16 * kCodeRow);
-        w[j] = u32x4{lo.x, lo.y, hi.x, hi.y};
+        const uint2 v = turn_codes(stage + (turn ^ (16 * j)) + 16 * kCodeRow * t);
+        w[j][2 * t] = v.x;
+        w[j][2 * t + 1] = v.y;
       }
     };
 
     floatx16 acc[MI][2];
     gt::zero_acc(acc);
-    constexpr int kV = 24 / MI, kL = MI == 8 ? 2 : 8 / MI + 1;
-    // As the forward product's loop, and the codes come three steps ahead: while
-    // step k is multiplied, those of k + 1 are turned, those of k + 2 and k + 3 and
-    // dy of k + 1 are on their way.  The wait at its end leaves the youngest.
-    constexpr int kYoungest = 2 + (kDQ ? 2 : 1);
-    u32x4 wc[2], wn[2];
-    dma_dy(xs0);
-    dma_codes(0);
-    dma_codes(1);
+    // While the products of 16 reduction indices (s) run, the wave expands the
+    // weights of s + 1 (looked up one s earlier) and reads dy of s + 1 and the
+    // lookups of s + 2.  The barrier is between s = 2 and 3: by then all of this
+    // step's dy and the next step's codes have been read, so that their stages are
+    // requested again, and s = 3 runs while the next dy is read.
+    floatx4 sb[2][2];
+    bf16x8 bf[2][2], af[2][MI];
+    gt::Lookups lk[2];
+    // The products of s with the rest between them.  stage, at: where dy of s + 1
+    // is read; word: the codes of s + 2; more(q): what else goes behind product q.
+    auto phase = [&](int s, const char* stage, int at, int word, auto more) {
+      const int cur = s & 1, nxt = cur ^ 1;
+      u32x4 v[2];
+#pragma unroll
+      for (int q = 0; q < 2 * MI; ++q) {
+        acc[q >> 1][q & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[cur][q & 1], af[cur][q >> 1], acc[q >> 1][q & 1], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        more(q);
+#pragma unroll
+        for (int e = 8 * q / (2 * MI); e < 8 * (q + 1) / (2 * MI); ++e) {
+          const int j = e >> 2, t = e & 3;
+          // (opaque: here, not where the operand is used)
+          v[j][t] = opaque(gt::bf16_pair(lk[nxt].l[j][t].x * sb[nxt][t >> 1][2 * (t & 1)], lk[nxt].l[j][t].y * sb[nxt][t >> 1][2 * (t & 1) + 1]));
+        }
+#pragma unroll
+        for (int e = (8 * q + 2 * MI - 1) / (2 * MI); e < (8 * (q + 1) + 2 * MI - 1) / (2 * MI); ++e) {
+          const int j = e >> 2, t = e & 3;
+          const uint32_t addr = __builtin_amdgcn_perm(w[j][word], slot, 0x0C0C0000u | ((4u + t) << 8)) >> (kC == 32 ? 0 : 1);
+          lk[cur].l[j][t] = *reinterpret_cast<const float2*>(tabc + addr);
+        }
+#pragma unroll
+        for (int i = (q + 1) / 2; i < (q + 2) / 2; ++i)
+          af[nxt][i] = gt::lds_frag(stage + (((h4 + at) ^ sw) << 4) + i * 32 * gt::kActRowBytes);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      bf[nxt][0] = __builtin_bit_cast(bf16x8, v[0]);
+      bf[nxt][1] = __builtin_bit_cast(bf16x8, v[1]);
+    };
+#pragma unroll
+    for (int i = 0; i < MI; ++i) dma_dy(i, dst0);
     dma_scale(0);
     dma_scale(1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dma_codes(i & 1, i >> 1);
     wait_loads<0>();
     sk::wave_lds_order();
     put_scale(0);
-    sk::wave_lds_order();
-    dma_codes(2);
-    dma_scale(2);
-    floatx4 sb[2][2];
-    bf16x8 bf[2][2];
-    gt::Lookups lk[3];
-    bf16x8 af[3][MI];
     sk::lds_barrier();
-    turn_step(wc, cs_all[0]);
+    turn_half(0, cs_all[0]);
+    turn_half(1, cs_all[0]);
+    sk::lds_barrier();  // before the first codes are overwritten
+#pragma unroll
+    for (int i = 0; i < MI; ++i) dma_dy(i, dst1);
+    dma_scale(2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dma_codes(i & 1, i < 2 ? 2 : 0);
+    const char* xa = xs0 + (lane & 31) * gt::kActRowBytes;
+    gt::read_act(xa, 0, sw, h4, af[0]);
     read_scales(sb[0], 0, 0);
     read_scales(sb[1], 0, 1);
-    gt::lookup_step<kC>(lk[0], wc, 0, tabc, slot);
+    gt::lookup_step<kC>(lk[0], w, 0, tabc, slot);
+    gt::lookup_step<kC>(lk[1], w, 1, tabc, slot);
     bf[0][0] = expand_rows(lk[0].l[0], sb[0]);
     bf[0][1] = expand_rows(lk[0].l[1], sb[0]);
-    sk::lds_barrier();  // before the first codes are overwritten
-    int free = 0;   // the codes' stage of step ks, ks % 3
+    int next = 1;  // the stage of the next step's codes
     for (int ks = 0; ks < nk; ++ks) {
-      dma_dy((ks & 1) ? xs0 : xs1);
-      dma_codes(free);
-      free = free == 2 ? 0 : free + 1;
-      __builtin_amdgcn_sched_barrier(0);
-      const char* xa = ((ks & 1) ? xs1 : xs0) + (lane & 31) * gt::kActRowBytes;
-      gt::read_act(xa, 0, sw, h4, af[0]);
-      gt::read_act(xa, 1, sw, h4, af[1]);
-      gt::lookup_step<kC>(lk[1], wc, 1, tabc, slot);
-      __builtin_amdgcn_sched_barrier(0);
-      // s = 0
-      gt::mfma16(af[0], bf[0], acc);
-      bf[1][0] = expand_rows(lk[1].l[0], sb[1]);
-      bf[1][1] = expand_rows(lk[1].l[1], sb[1]);
-      gt::read_act(xa, 2, sw, h4, af[2]);
-      gt::lookup_step<kC>(lk[2], wc, 2, tabc, slot);
-      read_scales(sb[0], ks, 2);
-      gt::mfma_interleave<2 * MI, kV, kL>();
-      __builtin_amdgcn_sched_barrier(0);
+      phase(0, xa, 1, 2, [&](int q) {
+        if (q == 0) read_scales(sb[0], ks, 2);
+      });
+      phase(1, xa, 2, 3, [&](int q) {
+        if (q == 0) read_scales(sb[1], ks, 3);
+        if (q == 1) turn_half(0, cs_all[next]);
+        if (q == 2) put_scale(ks + 1);
+      });
       sk::wave_lds_order();
-      put_scale(ks + 1);
-      sk::wave_lds_order();
-      dma_scale(ks + 3);
-      // s = 1
-      gt::mfma16(af[1], bf[1], acc);
-      bf[0][0] = expand_rows(lk[2].l[0], sb[0]);
-      bf[0][1] = expand_rows(lk[2].l[1], sb[0]);
-      gt::read_act(xa, 3, sw, h4, af[0]);
-      gt::lookup_step<kC>(lk[0], wc, 3, tabc, slot);
-      read_scales(sb[1], ks, 3);
-      gt::mfma_interleave<2 * MI, kV, kL>();
-      __builtin_amdgcn_sched_barrier(0);
-      // s = 2, with the next step's codes
-      gt::mfma16(af[2], bf[0], acc);
-      bf[1][0] = expand_rows(lk[0].l[0], sb[1]);
-      bf[1][1] = expand_rows(lk[0].l[1], sb[1]);
-      turn_step(wn, cs_all[free]);
-      read_scales(sb[0], ks + 1, 0);
-      gt::mfma_interleave<2 * MI, kV, kL>();
-      __builtin_amdgcn_sched_barrier(0);
-      // s = 3, with the next step's s = 0 expansion
-      gt::mfma16(af[0], bf[1], acc);
-      gt::lookup_step<kC>(lk[1], wn, 0, tabc, slot);
-      bf[0][0] = expand_rows(lk[1].l[0], sb[0]);
-      bf[0][1] = expand_rows(lk[1].l[1], sb[0]);
-      read_scales(sb[1], ks + 1, 1);
-      gt::mfma_interleave<2 * MI, kV, kL>();
-      __builtin_amdgcn_sched_barrier(0);
-      wait_loads<kYoungest>();
+      phase(2, xa, 3, 0, [&](int q) {
+        if (q == 0) read_scales(sb[0], ks + 1, 0);
+        if (q == 1) turn_half(1, cs_all[next]);
+      });
+      // the next step's dy is here, and the codes of the one after
+      wait_loads<2>();
       sk::lds_barrier();
-      wc[0] = wn[0];
-      wc[1] = wn[1];
+      const uint32_t freed = (ks & 1) ? dst1 : dst0;
+      xa = ((ks & 1) ? xs0 : xs1) + (lane & 31) * gt::kActRowBytes;
+      phase(3, xa, 0, 1, [&](int q) {
+        if (q == 0) read_scales(sb[1], ks + 1, 1);
+        if (q < MI) dma_dy(q, freed);
+        if (q == MI) dma_scale(ks + 3);
+        if (q == MI + 1) {
+          dma_codes(0, next);
+          dma_codes(1, next);
+        }
+      });
+      next = next == 2 ? 0 : next + 1;
     }
     wait_loads<0>();
+    sk::lds_barrier();  // the last reads of dy, before the next tile's is requested
     gt::store_acc<MI, true>(acc, a.dx, tile.hi, a.cols, tile.row0, k0, wave, lane);
   }
 }
@@ -335,25 +340,26 @@ hipError_t launch(const ExpertDxArgs& a, hipStream_t s) {
 hipError_t launch_expert_gemm_dx(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
                                  const uint16_t* dy, uint16_t* dx, hipStream_t s) {
   // By the mean number of rows of an expert (the only one known here) and whether
-  // about this many tiles of 64 rows give every compute unit one; where the
-  // reduction is long, an emptier last round costs more than what the kernel that
-  // splits it (k_expert_skinny_dx.hip) loses.  Measured in us: that kernel, then
-  // tiles of 64 and of 128 rows, and full rounds of 256 rows here:
-  //   64 experts of 1024x2048,  mean  12:   48   33   52   35
-  //                                   48:   61   50   79   53
-  //                                  160:  126   98  107  102
-  //                                  300:  188  160  159  146
-  //   16 of 4096x4096,          mean  24:   93   97   90  100
-  //                                  160:  193  197  176  200
-  //                                  300:  282  301  265  241
-  //   4 of 2048x8192,           mean  24:   28   43   49   46
-  //                                   96:   63   43   51   46
-  //   8 of 14336x4096,          mean  64:  210  253  289  257
-  //                                  256:  470  536  571  540
-  //                                 1024: 1437 1541 1454 1138
+  // about this many tiles of 64 rows occupy most compute units; if not, the kernel
+  // that splits the reduction.  Measured in us: that kernel
+  // (k_expert_skinny_dx.hip), then tiles of 64 and of 128 rows, and full rounds of
+  // 256 rows here:
+  //   64 experts of 1024x2048,  mean  12:   48   31   42   34
+  //                                   48:   61   44   66   47
+  //                                  160:  126   89   90   93
+  //                                  300:  188  148  134  136
+  //   16 of 4096x4096,          mean   4:   57   65   67   68
+  //                                   24:   93   83   74   87
+  //                                  160:  193  179  144  182
+  //                                  300:  282  277  225  219
+  //   4 of 2048x8192,           mean  24:   28   37   38   40
+  //                                   48:   44   36   40   40
+  //   8 of 14336x4096,          mean  32:  186  208  209  212
+  //                                  150:  307  281  218  285
+  //                                  512:  874  704  678  589
   const int64_t experts = er.experts, tiles_k = (cols + gt::kTileN - 1) / gt::kTileN;
   const int64_t about = ((er.m < experts ? er.m : experts) / 2 + er.m / 64) * tiles_k;
-  if (about < device_cus() * (rows > 8192 ? 3 : 1)) return launch_expert_skinny_dx(packed, rows, cols, sc, er, dy, dx, s);
+  if (8 * about < 5 * device_cus()) return launch_expert_skinny_dx(packed, rows, cols, sc, er, dy, dx, s);
   ExpertDxArgs a{};
   a.packed = packed; a.rows = rows; a.cols = cols; a.sc = sc; a.er = er; a.dy = dy; a.dx = dx;
   a.cb = codebook(sc.fp4);
