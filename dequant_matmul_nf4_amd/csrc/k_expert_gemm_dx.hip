@@ -15,9 +15,9 @@
 // scales, one made by each lane and read back from LDS.
 //
 // A wave is alone on its SIMD (two waves at 64 rows), so what it does besides the
-// products is spelled out between them, one lookup, one read of dy, or one pair
-// expanded at a time; left to the compiler it collects behind them (8192 rows over
-// 8 experts of 14336x4096: 1110 us; in place 962 us).  The codes come from HBM and
+// products is spelled out between them (expert_phases.h); left to the compiler it
+// collects behind them (8192 rows over 8 experts of 14336x4096: 1110 us; in place
+// 962 us).  The codes come from HBM and
 // are requested three steps ahead, dy one to two.  As in the forward product,
 // tiles are counted from the offsets, and of many rows full rounds of 256-row
 // tiles go first and 64-row tiles take the rest.
@@ -25,9 +25,8 @@
 // Bound: the matrix cores.  8192 rows over 8 experts of 14336x4096: 962 us, 1000
 // TFLOP/s; 4096 over 64 of 1024x2048: 46 us.  Expanding to bfloat16 first and
 // turning that in LDS, 8 waves a tile, took 1240 and 85.
+#include "expert_phases.h"
 #include "expert_tiles.h"
-#include "gemm_fwd.h"
-#include "skinny_tile.h"
 
 namespace nf4i {
 namespace {
@@ -60,34 +59,6 @@ constexpr int pair_copies() { return MI == 2 ? 16 : 32; }
 __device__ __forceinline__ uint2 turn_codes(const char* p) {
   const intx2 v = __builtin_amdgcn_ds_read_tr4_b64_v2i32((__attribute__((address_space(3))) intx2*)(char*)p);
   return make_uint2(static_cast<uint32_t>(v[0]), static_cast<uint32_t>(v[1]));
-}
-
-// Direct global-to-LDS loads of a wave: lane l's 16 (4, 1) bytes at base + off
-// to lds + 16 l (4 l, 4 l).  Inline assembly, since the compiler lets every
-// turn_codes wait for all loads to LDS that it knows of; the waits are counted
-// by hand (wait_loads).
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)(const char*)p));
-}
-__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
-}
-__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
-}
-__device__ __forceinline__ void dma1(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
-}
-// Until at most N of the wave's loads are on their way.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ bf16x8 expand_rows(const float2 (&l)[4], const floatx4 (&s)[2]) {
-  const u32x4 v = {gt::bf16_pair(l[0].x * s[0][0], l[0].y * s[0][1]), gt::bf16_pair(l[1].x * s[0][2], l[1].y * s[0][3]),
-                   gt::bf16_pair(l[2].x * s[1][0], l[2].y * s[1][1]), gt::bf16_pair(l[3].x * s[1][2], l[3].y * s[1][3])};
-  return __builtin_bit_cast(bf16x8, v);
 }
 
 template <int MI, bool kDQ, bool kF8>
@@ -125,8 +96,8 @@ __global__ __launch_bounds__(gt::kThreads, MI == 2 ? 2 : 1) void k_expert_gemm_d
   float* scl = &scl_all[wave][0][0];
   const float* raw = &raw_all[wave][0][0][0];
   // where the wave's requests go
-  const uint32_t raw0 = lds_address(raw), codes0 = lds_address(cs_all[0]) + 2 * wave * 1024;
-  const uint32_t dst0 = lds_address(xs0) + MI * wave * 1024, dst1 = lds_address(xs1) + MI * wave * 1024;
+  const uint32_t raw0 = gt::lds_address(raw), codes0 = gt::lds_address(cs_all[0]) + 2 * wave * 1024;
+  const uint32_t dst0 = gt::lds_address(xs0) + MI * wave * 1024, dst1 = gt::lds_address(xs1) + MI * wave * 1024;
   const uint32_t sw = ((lane & 31) >> 1) & 7, h4 = (lane >> 5) * 4;
   // where the lane reads the codes it turns: row 32 h + 16 t + lane % 16, 16-byte
   // piece 2 wave + j of the row at slot piece ^ (row % 8)
@@ -163,7 +134,7 @@ __global__ __launch_bounds__(gt::kThreads, MI == 2 ? 2 : 1) void k_expert_gemm_d
     uint32_t dy_last = 0, co_last = 0;  // of the step that is requested: the last piece of a row, the last row
     auto dma_dy = [&](int i, uint32_t stage) {
       if (i == 0) dy_last = (static_cast<uint32_t>(dy_left < kStep ? dy_left : kStep) - 8) * 2;
-      dma16(dyp, drow[i] + least(piece[i & 1], dy_last), stage + i * 1024);
+      gt::request16(dyp, drow[i] + least(piece[i & 1], dy_last), stage + i * 1024);
       if (i == MI - 1) {
         const int by = dy_left > kStep ? kStep : 0;
         dyp += by * 2;
@@ -172,7 +143,7 @@ __global__ __launch_bounds__(gt::kThreads, MI == 2 ? 2 : 1) void k_expert_gemm_d
     };
     auto dma_codes = [&](int i, int stage) {
       if (i == 0) co_last = static_cast<uint32_t>((co_left < kStep ? co_left : kStep) - 1) * row_bytes;
-      dma16(cop, cpiece + least(crow + i * 8 * row_bytes, co_last), codes0 + stage * kCodeStage + i * 1024);
+      gt::request16(cop, cpiece + least(crow + i * 8 * row_bytes, co_last), codes0 + stage * kCodeStage + i * 1024);
       if (i == 1) {
         const int by = co_left > kStep ? kStep : 0;
         cop += by * static_cast<int64_t>(row_bytes);
@@ -185,10 +156,10 @@ __global__ __launch_bounds__(gt::kThreads, MI == 2 ? 2 : 1) void k_expert_gemm_d
       const uint32_t to = raw0 + (ks & 1) * sizeof(raw_all[0][0]);
       const uint32_t o = least(srow, static_cast<uint32_t>((sc_left < kStep ? sc_left : kStep) - 1) * nblk);
       if constexpr (kDQ) {
-        dma1(a.sc.q + blk, o, to);
-        dma4(a.sc.absmax2 + (blk >> 8), (static_cast<uint32_t>(blk & 255) + o) >> 8 << 2, to + 4 * kStep);
+        gt::request1(a.sc.q + blk, o, to);
+        gt::request4(a.sc.absmax2 + (blk >> 8), (static_cast<uint32_t>(blk & 255) + o) >> 8 << 2, to + 4 * kStep);
       } else {
-        dma4(a.sc.absmax + blk, o << 2, to);
+        gt::request4(a.sc.absmax + blk, o << 2, to);
       }
       const int by = sc_left > kStep ? kStep : 0;
       blk += by * static_cast<int64_t>(nblk);
@@ -223,51 +194,22 @@ __global__ __launch_bounds__(gt::kThreads, MI == 2 ? 2 : 1) void k_expert_gemm_d
 
     floatx16 acc[MI][2];
     gt::zero_acc(acc);
-    // While the products of 16 reduction indices (s) run, the wave expands the
-    // weights of s + 1 (looked up one s earlier) and reads dy of s + 1 and the
-    // lookups of s + 2.  The barrier is between s = 2 and 3: by then all of this
-    // step's dy and the next step's codes have been read, so that their stages are
-    // requested again, and s = 3 runs while the next dy is read.
-    floatx4 sb[2][2];
-    bf16x8 bf[2][2], af[2][MI];
-    gt::Lookups lk[2];
-    // The products of s with the rest between them.  stage, at: where dy of s + 1
-    // is read; word: the codes of s + 2; more(q): what else goes behind product q.
-    auto phase = [&](int s, const char* stage, int at, int word, auto more) {
-      const int cur = s & 1, nxt = cur ^ 1;
-      u32x4 v[2];
-#pragma unroll
-      for (int q = 0; q < 2 * MI; ++q) {
-        acc[q >> 1][q & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[cur][q & 1], af[cur][q >> 1], acc[q >> 1][q & 1], 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        more(q);
-#pragma unroll
-        for (int e = 8 * q / (2 * MI); e < 8 * (q + 1) / (2 * MI); ++e) {
-          const int j = e >> 2, t = e & 3;
-          // (opaque: here, not where the operand is used)
-          v[j][t] = opaque(gt::bf16_pair(lk[nxt].l[j][t].x * sb[nxt][t >> 1][2 * (t & 1)], lk[nxt].l[j][t].y * sb[nxt][t >> 1][2 * (t & 1) + 1]));
-        }
-#pragma unroll
-        for (int e = (8 * q + 2 * MI - 1) / (2 * MI); e < (8 * (q + 1) + 2 * MI - 1) / (2 * MI); ++e) {
-          const int j = e >> 2, t = e & 3;
-          const uint32_t addr = __builtin_amdgcn_perm(w[j][word], slot, 0x0C0C0000u | ((4u + t) << 8)) >> (kC == 32 ? 0 : 1);
-          lk[cur].l[j][t] = *reinterpret_cast<const float2*>(tabc + addr);
-        }
-#pragma unroll
-        for (int i = (q + 1) / 2; i < (q + 2) / 2; ++i)
-          af[nxt][i] = gt::lds_frag(stage + (((h4 + at) ^ sw) << 4) + i * 32 * gt::kActRowBytes);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      bf[nxt][0] = __builtin_bit_cast(bf16x8, v[0]);
-      bf[nxt][1] = __builtin_bit_cast(bf16x8, v[1]);
+    // A step's four phases as in the forward product, the barrier between s = 2 and
+    // 3: by then all of this step's dy and the next step's codes have been read.
+    floatx4 sb[2][2];  // the scales of s in sb[s % 2]
+    gt::Operands<MI> o;
+    const auto expand = [&](const floatx4 (&f)[2], int t, const float2& l) {
+      return gt::bf16_pair(l.x * f[t >> 1][2 * (t & 1)], l.y * f[t >> 1][2 * (t & 1) + 1]);
     };
+    const auto even = [&](int, int t, const float2& l) { return expand(sb[0], t, l); };
+    const auto odd = [&](int, int t, const float2& l) { return expand(sb[1], t, l); };
 #pragma unroll
     for (int i = 0; i < MI; ++i) dma_dy(i, dst0);
     dma_scale(0);
     dma_scale(1);
 #pragma unroll
     for (int i = 0; i < 4; ++i) dma_codes(i & 1, i >> 1);
-    wait_loads<0>();
+    gt::wait_requests<0>();
     sk::wave_lds_order();
     put_scale(0);
     sk::lds_barrier();
@@ -280,34 +222,30 @@ __global__ __launch_bounds__(gt::kThreads, MI == 2 ? 2 : 1) void k_expert_gemm_d
 #pragma unroll
     for (int i = 0; i < 4; ++i) dma_codes(i & 1, i < 2 ? 2 : 0);
     const char* xa = xs0 + (lane & 31) * gt::kActRowBytes;
-    gt::read_act(xa, 0, sw, h4, af[0]);
     read_scales(sb[0], 0, 0);
     read_scales(sb[1], 0, 1);
-    gt::lookup_step<kC>(lk[0], w, 0, tabc, slot);
-    gt::lookup_step<kC>(lk[1], w, 1, tabc, slot);
-    bf[0][0] = expand_rows(lk[0].l[0], sb[0]);
-    bf[0][1] = expand_rows(lk[0].l[1], sb[0]);
+    gt::first_operands<MI, kC>(o, w, xa, sw, h4, tabc, slot, even);
     int next = 1;  // the stage of the next step's codes
     for (int ks = 0; ks < nk; ++ks) {
-      phase(0, xa, 1, 2, [&](int q) {
+      gt::mfma_phase<MI, kC>(0, o, acc, w, 2, xa, 1, sw, h4, tabc, slot, odd, [&](int q) {
         if (q == 0) read_scales(sb[0], ks, 2);
       });
-      phase(1, xa, 2, 3, [&](int q) {
+      gt::mfma_phase<MI, kC>(1, o, acc, w, 3, xa, 2, sw, h4, tabc, slot, even, [&](int q) {
         if (q == 0) read_scales(sb[1], ks, 3);
         if (q == 1) turn_half(0, cs_all[next]);
         if (q == 2) put_scale(ks + 1);
       });
       sk::wave_lds_order();
-      phase(2, xa, 3, 0, [&](int q) {
+      gt::mfma_phase<MI, kC>(2, o, acc, w, 0, xa, 3, sw, h4, tabc, slot, odd, [&](int q) {
         if (q == 0) read_scales(sb[0], ks + 1, 0);
         if (q == 1) turn_half(1, cs_all[next]);
       });
       // the next step's dy is here, and the codes of the one after
-      wait_loads<2>();
+      gt::wait_requests<2>();
       sk::lds_barrier();
       const uint32_t freed = (ks & 1) ? dst1 : dst0;
       xa = ((ks & 1) ? xs0 : xs1) + (lane & 31) * gt::kActRowBytes;
-      phase(3, xa, 0, 1, [&](int q) {
+      gt::mfma_phase<MI, kC>(3, o, acc, w, 1, xa, 0, sw, h4, tabc, slot, even, [&](int q) {
         if (q == 0) read_scales(sb[1], ks + 1, 1);
         if (q < MI) dma_dy(q, freed);
         if (q == MI) dma_scale(ks + 3);
@@ -318,7 +256,7 @@ __global__ __launch_bounds__(gt::kThreads, MI == 2 ? 2 : 1) void k_expert_gemm_d
       });
       next = next == 2 ? 0 : next + 1;
     }
-    wait_loads<0>();
+    gt::wait_requests<0>();
     sk::lds_barrier();  // the last reads of dy, before the next tile's is requested
     gt::store_acc<MI, true>(acc, a.dx, tile.hi, a.cols, tile.row0, k0, wave, lane);
   }
