@@ -1,6 +1,7 @@
 // The K loop of the forward products y = x . deq(W)^T on the matrix cores,
 // shared by the GEMM (k_gemm.hip, where its schedule and operands are
-// described) and the product grouped by expert (k_expert_gemm.hip): a workgroup
+// described) and the 64-row tiles of the product grouped by expert
+// (k_expert_gemm.hip): a workgroup
 // of 4 waves accumulates a (32 MI) x 256 tile, x through two LDS stages that
 // the caller's `dma` fills, the weights' codes straight into operands.
 #pragma once

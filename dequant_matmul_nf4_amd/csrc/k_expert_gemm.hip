@@ -284,16 +284,19 @@ hipError_t launch(const ExpertGemmArgs& a, hipStream_t s) {
 hipError_t launch_expert_gemm(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
                               const ExpertX& ex, uint16_t* y, hipStream_t s) {
   // By the mean number of rows of an expert (the only one known here).  Measured in
-  // us: streaming tiles of 16 rows, then tiles of 64, 128 and 256 rows here:
-  //   8 experts of 14336x4096, mean  10:   67  106  169  223
-  //                                  32:  136  181  175  227
-  //                                  64:  241  189  250  236
-  //                                 150:  507  316  260  351
-  //                                 256:  854  441  424  371
-  //   64 experts of 1024x2048, mean  32:   49   55   53   67
-  //                                  64:   81   55   93   71
-  //                                 128:  138   96   95  128
-  //                                 256:  258  149  137  135
+  // us: streaming tiles of 16 rows, then tiles of 64, of 128, and of 256 rows with
+  // 64-row tiles for the rest:
+  //   8 experts of 14336x4096, mean  10:   68  106  146  108
+  //                                  40:  153  173  152  176
+  //                                  64:  239  179  218  183
+  //                                 112:  386  219  225  219
+  //                                 150:  508  291  242  296
+  //                                 224:  735  403  380  338
+  //                                 512: 1624  788  659  589
+  //   64 experts of 1024x2048, mean  32:   50   55   48   58
+  //                                  64:   80   55   82   58
+  //                                 128:  143   92   86   94
+  //                                 256:  265  137  128  124
   const int64_t experts = er.experts;
   if (er.m <= 40 * experts) return launch_expert_skinny(packed, rows, cols, sc, er, ex, y, s);
   ExpertGemmArgs a{};
