@@ -76,7 +76,7 @@ def sources_digest(names) -> str:
 
 
 GEMM_TRAFFIC_FILE = os.path.join(ROOT, "profiles", "k_gemm_qlora_forward_traffic.json")
-GEMM_SOURCES = ["k_gemm.hip", "gemm_tiles.h", "nf4_device.h", "nf4_internal.h"]
+GEMM_SOURCES = ["k_gemm.hip", "gemm_fwd.h", "gemm_tiles.h", "nf4_device.h", "nf4_internal.h"]
 
 
 def measured_traffic(path=TRAFFIC_FILE, sources=GEMV_SOURCES):

@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "nf4.h"
+#include "expert_int4.h"
 #include "nf4_internal.h"
 
 namespace {

@@ -4,6 +4,7 @@
 // and to ascend, so that no offset makes a kernel leave its buffers.
 #pragma once
 
+#include "expert_int4.h"
 #include "nf4_device.h"
 
 namespace nf4i {

@@ -11,6 +11,7 @@
 // launches and latency (64 slots: one launch, 3.1 us; 131072 slots over 128 experts:
 // two, 2.5 + 7.0 us).  The sums are bound by HBM: 32768 rows of 4096 columns into
 // 16384 tokens 78 us (5.2 TB/s), backward 134 us (4.8 TB/s).
+#include "expert_int4.h"
 #include "nf4_device.h"
 
 namespace nf4i {

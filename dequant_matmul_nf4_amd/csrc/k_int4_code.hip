@@ -16,6 +16,7 @@
 // flattened weight (cols is a multiple of the group), so a lane takes 16
 // consecutive values, a group is 2, 4 or 8 lanes, and its extremes are found
 // with that many lanes' permutes.
+#include "expert_int4.h"
 #include "nf4_device.h"
 
 namespace nf4i {

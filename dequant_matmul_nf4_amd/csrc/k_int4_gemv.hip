@@ -17,6 +17,7 @@
 // points (3.5 TB/s; 25 us at the rate of a large copy); groups of 32 47 to 52 us:
 // each scale costs 8 multiply-adds of a lane.  4096x4096 takes 7 us: launch, x, one
 // step and the join follow each other.
+#include "expert_int4.h"
 #include "skinny_tile.h"
 
 namespace nf4i {

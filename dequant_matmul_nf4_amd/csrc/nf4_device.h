@@ -76,16 +76,6 @@ __device__ __forceinline__ int batch_item_of(const int (&first)[N + 1], int coun
   return j;
 }
 
-// Workgroups numbered over a grid of two dimensions: the threads of one are
-// counted in 32 bits.  Kernels leave where the number is past their last.
-inline dim3 block_grid(int64_t blocks) {
-  const int64_t gy = (blocks + (1 << 20) - 1) >> 20;
-  return dim3(static_cast<unsigned>((blocks + gy - 1) / gy), static_cast<unsigned>(gy));
-}
-__device__ __forceinline__ int64_t block_number() {
-  return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
-}
-
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, kWave);
