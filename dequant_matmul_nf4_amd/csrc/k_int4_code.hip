@@ -104,7 +104,9 @@ __global__ __launch_bounds__(256) void k_int4_quantize(const void* __restrict__ 
   // rint(x / s): with r = fl32(1 / s), q0 = fl32(x r) and the exact remainder
   // x - q0 s, fl32(q0 + (x - q0 s) r) is the IEEE quotient (Markstein) while
   // nothing under- or overflows on the way; smaller quotients round to 0 both ways.
-  const bool fast = s >= 0x1p-80f && s <= 0x1p100f;
+  // (Under a float16 scale, which saturates, a value can be infinite and s not:
+  // its remainder would be a NaN, where the quotient is infinite.)
+  const bool fast = s >= 0x1p-80f && s <= 0x1p100f && fmaxf(fabsf(lo), fabsf(hi)) <= 0x1.fffffep127f;
   const float r = 1.0f / s;
 #pragma unroll
   for (int k = 0; k < 16; ++k) {

@@ -485,7 +485,9 @@ typedef struct nf4_int4_weight {
  *               z = clamp(rint(-lo / s), 0, 15), q = clamp(rint(x / s) + z, 0, 15)
  * with rnd() the rounding to scale_dtype (to nearest even; a float16 scale
  * saturates at 65504), IEEE divisions and rint() to even.  A group whose s is
- * 0 gets q = z (z = 0 where asymmetric). */
+ * 0 gets q = z (z = 0 where asymmetric).  With a float16 scale the formulas hold
+ * for infinite x too: its q is the end of the range on its side.  In the other
+ * types such a group's scale is infinite and the group is lost. */
 int nf4_int4_quantize(const void* x, int x_dtype, const nf4_int4_weight* w, void* stream);
 
 /* out[r][c] = (q - z) . s: the product in float32, rounded once to out_dtype
