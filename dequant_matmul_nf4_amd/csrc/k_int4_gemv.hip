@@ -9,7 +9,8 @@
 // group (one product of x with ones per step, kept while x is),
 //   sum (q - z) x = 16 (d - (1 + z / 16) X),
 // so a group costs two fused multiply-adds per output and nothing is rounded
-// below float32.  (An offset of 1 on q / 16 in [0, 1) costs the sum about two
+// below float32.  The 16 goes to the finished sums: 16 s would overflow for the
+// largest float32 scales.  (An offset of 1 on q / 16 in [0, 1) costs the sum about two
 // bits; 128 + q, whose offset needs no shift, would cost five.)
 //
 // Bound: reading the codes; skinny_tile.h has the walk.  28672x8192 takes 29 us at
@@ -229,7 +230,7 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_int4_gemv(Int4Args a) {
 #pragma unroll
           for (int j = 0; j < kPer; ++j)
             scl[ln * kNs + g * kPer + j] =
-                make_float2(16.0f * scale_value<kWide>(st.s[j], a.scale_type), a.zeros ? -1.0f - static_cast<float>(st.z[j]) * 0.0625f : -1.5f);
+                make_float2(scale_value<kWide>(st.s[j], a.scale_type), a.zeros ? -1.0f - static_cast<float>(st.z[j]) * 0.0625f : -1.5f);
         }
         load_at(st, base, gi + 2 < kG ? seg : seg + 1, (gi + 2) % kG);
         if (!here) continue;
@@ -276,7 +277,7 @@ __global__ __launch_bounds__(sk::kThreads, 2) void k_int4_gemv(Int4Args a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int xm = 4 * (l >> 4) + i;
-        if (xm < a.m) store_y(a.y, a.y_type, xm * a.rows + row, v[i]);
+        if (xm < a.m) store_y(a.y, a.y_type, xm * a.rows + row, 16.0f * v[i]);
       }
     }
     sk::lds_barrier();

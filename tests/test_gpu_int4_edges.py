@@ -45,3 +45,25 @@ def test_infinite_values_under_a_saturated_scale(kind, group, asym):
         codes = q[[0, 1, 2, 2, 3], [3, 5, 0, group - 1, cols - 1]]
         assert codes.tolist() == [15, 0, 15, 0, 15]
     assert np.array_equal(W.packed.cpu().numpy(), _pack(q))
+
+
+@pytest.mark.parametrize("m", [1, 5])
+@pytest.mark.parametrize("asym", [False, True])
+def test_product_under_the_largest_scales(m, asym):
+    """float32 scales up to 3e38 with x small enough for a finite result: within
+    the products' bound (test_gpu_int4.py), as for any other scale."""
+    torch = need_gpu()
+    rows, cols, group = 40, 640, 64
+    g = torch.Generator(device="cuda").manual_seed(4)
+    packed = torch.randint(0, 256, (rows * cols // 2,), generator=g, device="cuda", dtype=torch.uint8)
+    scales = 3e37 * (1 + 9 * torch.rand((rows, cols // group), generator=g, device="cuda"))
+    zeros = torch.randint(0, 16, scales.shape, generator=g, device="cuda", dtype=torch.uint8) if asym else None
+    x = (torch.randn((m, cols), generator=g, device="cuda") * 2.0 ** -20).bfloat16()
+    W = nf4.Int4Weight(packed, rows, cols, group, scales, zeros)
+    q = torch.stack((packed >> 4, packed & 15), 1).reshape(rows, -1, group).double()
+    w = ((q - (zeros.double()[..., None] if asym else 8.0)) * scales.double()[..., None]).reshape(rows, cols)
+    ref, size = x.double() @ w.t(), x.double().abs() @ scales.double().repeat_interleave(group, 1).t()
+    for kind in (torch.float32, torch.bfloat16):
+        y = nf4.nf4_int4_gemv(W, x, y_dtype=kind)
+        bound = torch.finfo(kind).eps / 2 * ref.abs() + (group + cols / group + 24) * 2.0 ** -24 * 64 * size
+        assert ((y.double() - ref).abs() <= bound).all()
