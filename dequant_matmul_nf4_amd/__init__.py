@@ -817,14 +817,26 @@ def nf4_expert_combine_backward(dout, y, position, slots: int, weights=None, dy=
                                 stream=None):
     """The gradients of nf4_expert_combine: (dy [m, cols] bf16, dweights
     [tokens, slots] float32); one not in `want` (and not given) is None.  Rows
-    of dy that no position names are not written; no row is named twice."""
+    of dy that no position names are not written; no row is named twice.  y may
+    be None where dweights is not wanted: m is then dy's rows, or without dy
+    the number of slots."""
     torch = _torch()
     dev = dout.device
-    if y.dim() != 2 or slots < 1 or position.numel() % slots:
-        raise ValueError("y must be [m, cols], and position hold `slots` entries per token")
-    (m, cols), n = y.shape, position.numel()
+    if slots < 1 or position.numel() % slots:
+        raise ValueError("position must hold `slots` entries per token")
+    n = position.numel()
+    if y is not None:
+        if y.dim() != 2:
+            raise ValueError("y must be [m, cols]")
+        m, cols = y.shape
+        _need("y", y, torch.bfloat16, m * cols, dev)
+    else:
+        if dweights is not None or "dweights" in want:
+            raise ValueError("dweights needs y")
+        if dy is not None and dy.dim() != 2:
+            raise ValueError("dy must be [m, cols]")
+        m, cols = dy.shape if dy is not None else (n, dout.numel() // max(n // slots, 1))
     _need("dout", dout, torch.bfloat16, n // slots * cols, dev)
-    _need("y", y, torch.bfloat16, m * cols, dev)
     _need("position", position, torch.int32, n, dev)
     if weights is not None:
         _need("weights", weights, torch.float32, n, dev)
@@ -836,7 +848,7 @@ def nf4_expert_combine_backward(dout, y, position, slots: int, weights=None, dy=
         _need("dy", dy, torch.bfloat16, m * cols, dev)
     if dweights is not None:
         _need("dweights", dweights, torch.float32, n, dev)
-    _call(dev, stream, lib().nf4_expert_combine_backward, dout.data_ptr(), y.data_ptr(), m, position.data_ptr(),
+    _call(dev, stream, lib().nf4_expert_combine_backward, dout.data_ptr(), _ptr(y), m, position.data_ptr(),
           n // slots, slots, cols, _ptr(weights), _ptr(dy), _ptr(dweights))
     return dy, dweights
 
