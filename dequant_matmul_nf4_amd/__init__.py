@@ -712,11 +712,27 @@ def _need(name, t, dtype, numel, dev):
     raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
+def _zero(t, stream) -> None:
+    """Zeros into a small result that no kernel is launched for."""
+    torch = _torch()
+    if stream is None:
+        t.zero_()
+        return
+    if stream.device != t.device:
+        raise ValueError(f"stream of {stream.device}, tensors on {t.device}")
+    with torch.cuda.stream(stream):
+        t.zero_()
+
+
+# Batches without a token (a rank that none was sent to) are answered here: the
+# C calls take at least one row.
+
 def nf4_expert_plan(ids, experts: int, order=None, position=None, offsets=None, workspace=None, stream=None):
     """The slots' expert ids (int32, any shape: n of them) sorted by expert:
     returns (order [n], position [n], offsets [experts + 1]), int32.  order[p]
     is the slot at sorted row p (-1 past the last), position[s] the row of slot
-    s (-1 where its id is outside 0 .. experts - 1: a dropped slot)."""
+    s (-1 where its id is outside 0 .. experts - 1: a dropped slot).  There may
+    be no slots, and so no rows in the calls that follow."""
     torch = _torch()
     dev, n = ids.device, ids.numel()
     _need("ids", ids, torch.int32, n, dev)
@@ -730,6 +746,9 @@ def nf4_expert_plan(ids, experts: int, order=None, position=None, offsets=None, 
         return t
 
     order, position, offsets = out("order", order, n), out("position", position, n), out("offsets", offsets, experts + 1)
+    if n == 0:
+        _zero(offsets, stream)
+        return order, position, offsets
     if workspace is None:
         wsn = nf4_expert_plan_workspace(n, experts)
         if wsn:
@@ -766,6 +785,8 @@ def nf4_expert_gemm(w: NF4Weight, experts: int, x, offsets, index=None, slots: i
         y = _alloc_on(stream, (m, rows), torch.bfloat16, dev)
     else:
         _need("y", y, torch.bfloat16, m * rows, dev)
+    if m == 0:
+        return y
     _call(dev, stream, lib().nf4_expert_gemm, ctypes.byref(cs), experts, x2.data_ptr(), x2.shape[0], _ptr(index), slots,
           offsets.data_ptr(), m, y.data_ptr())
     return y
@@ -786,6 +807,8 @@ def nf4_expert_gemm_dx(w: NF4Weight, experts: int, dy, offsets, dx=None, stream=
         dx = _alloc_on(stream, (m, w.cols), torch.bfloat16, dev)
     else:
         _need("dx", dx, torch.bfloat16, m * w.cols, dev)
+    if m == 0:
+        return dx
     _call(dev, stream, lib().nf4_expert_gemm_dx, ctypes.byref(cs), experts, dy2.data_ptr(), offsets.data_ptr(), m,
           dx.data_ptr())
     return dx
@@ -808,6 +831,9 @@ def nf4_expert_combine(y, position, slots: int, weights=None, out=None, stream=N
         out = _alloc_on(stream, (n // slots, cols), torch.bfloat16, dev)
     else:
         _need("out", out, torch.bfloat16, n // slots * cols, dev)
+    if m == 0 or n == 0:
+        _zero(out, stream)
+        return out
     _call(dev, stream, lib().nf4_expert_combine, y.data_ptr(), m, position.data_ptr(), n // slots, slots, cols,
           _ptr(weights), out.data_ptr())
     return out
@@ -835,7 +861,7 @@ def nf4_expert_combine_backward(dout, y, position, slots: int, weights=None, dy=
             raise ValueError("dweights needs y")
         if dy is not None and dy.dim() != 2:
             raise ValueError("dy must be [m, cols]")
-        m, cols = dy.shape if dy is not None else (n, dout.numel() // max(n // slots, 1))
+        m, cols = dy.shape if dy is not None else (n, dout.shape[-1])
     _need("dout", dout, torch.bfloat16, n // slots * cols, dev)
     _need("position", position, torch.int32, n, dev)
     if weights is not None:
@@ -848,6 +874,10 @@ def nf4_expert_combine_backward(dout, y, position, slots: int, weights=None, dy=
         _need("dy", dy, torch.bfloat16, m * cols, dev)
     if dweights is not None:
         _need("dweights", dweights, torch.float32, n, dev)
+    if m == 0 or n == 0:
+        if dweights is not None:
+            _zero(dweights, stream)
+        return dy, dweights
     _call(dev, stream, lib().nf4_expert_combine_backward, dout.data_ptr(), _ptr(y), m, position.data_ptr(),
           n // slots, slots, cols, _ptr(weights), _ptr(dy), _ptr(dweights))
     return dy, dweights
