@@ -9,13 +9,15 @@
 // device data, so a workgroup finds its run from the offsets).
 //
 // A byte of codes indexes a table of level pairs in LDS, rounded to float16 (11
-// significant bits: off by at most 2^-12 of a level), and the sums of a
+// significant bits: off by less than 2^-11 of a level), and the sums of a
 // 64-block are scaled in float32, so no scaled weight is rounded to 16 bits.
 // x becomes float16 exactly: a wave scales its columns of a row by the power
 // of two that brings their largest value to [2^14, 2^15) and scales the sums
-// back (values 2^-29 of the largest and below lose bits).  Two bfloat16 parts
-// per level instead were exact to 2^-17 but moved two registers per lookup to
-// line up the operands: 66 against 57 us (16 rows over 8 experts of 14336x4096).
+// back (values 2^-29 of the largest and below lose bits; a block scale of 2^104
+// could overflow the sum of a segment, 8 blocks of 64 products below 2^15).  Two
+// bfloat16 parts per level instead were exact to 2^-17 but moved two registers per
+// lookup to line up the operands: 66 against 57 us (16 rows over 8 experts of
+// 14336x4096).
 //
 // That product takes 49 us now (4.5 TB/s; its codes and scales take 43 us at the
 // rate of a large copy).  One row alone takes 16 us, where launch, offsets, index

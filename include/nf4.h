@@ -425,7 +425,8 @@ int nf4_expert_plan(const int32_t* ids, int64_t n, int32_t experts, int32_t* ord
  * nf4_gemm; for few, the level is rounded to fp16 (11 significant bits), x is
  * taken exactly (as fp16, scaled by a power of two per row and up to 512
  * columns: values 2^-29 of the largest there and below lose bits) and the
- * scale is applied in float32. */
+ * scale is applied in float32, before that power of two is taken back: for few
+ * rows block scales are below 2^104. */
 int nf4_expert_gemm(const nf4_weight* w, int32_t experts, const void* x, int64_t x_rows, const int32_t* index,
                     int32_t slots, const int32_t* offsets, int64_t m, void* y, void* stream);
 
@@ -499,7 +500,9 @@ int nf4_int4_dequantize(const nf4_int4_weight* w, void* out, int out_dtype, void
  *   y : [m][rows] of y_dtype (NF4_F32, NF4_BF16 or NF4_F16), 16-byte aligned,
  *       not overlapping any input.
  * The codes enter the products exactly; scales and zero points are applied to
- * the groups' sums in float32; y is rounded once. */
+ * the groups' sums in float32; y is rounded once.  A row of x that is not finite
+ * gives NaN in its row of y (also where the definition has an infinity: the zero
+ * point is applied as a difference of sums) and reaches no other row. */
 int nf4_int4_gemv(const nf4_int4_weight* w, const void* x, int x_dtype, int64_t m, void* y, int y_dtype, void* stream);
 
 #ifdef __cplusplus

@@ -67,3 +67,23 @@ def test_product_under_the_largest_scales(m, asym):
         y = nf4.nf4_int4_gemv(W, x, y_dtype=kind)
         bound = torch.finfo(kind).eps / 2 * ref.abs() + (group + cols / group + 24) * 2.0 ** -24 * 64 * size
         assert ((y.double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("m", [2, 5, 16])
+@pytest.mark.parametrize("rows,cols,group", [(40, 96, 32), (83, 640, 64), (300, 3584, 128), (70, 8256, 64)])
+def test_rows_of_x_stay_apart(m, rows, cols, group):
+    """Infinities and NaN in one row of x: NaN in its row of y, every
+    other row as without them, bit for bit."""
+    torch = need_gpu()
+    for asym in (False, True):
+        w = torch.randn((rows, cols), device="cuda")
+        W = nf4.quantize_int4(w, group=group, symmetric=not asym)
+        x = torch.randn((m, cols), device="cuda").bfloat16()
+        clean = nf4.nf4_int4_gemv(W, x, y_dtype=torch.float32)
+        for row, at, value in ((m - 1, cols - 1, "inf"), (0, cols // 2, "-inf"), (m // 2, 0, "nan")):
+            bad = x.clone()
+            bad[row, at] = float(value)
+            got = nf4.nf4_int4_gemv(W, bad, y_dtype=torch.float32)
+            others = torch.arange(m, device="cuda") != row
+            assert torch.equal(got[others], clean[others])
+            assert got[row].isnan().all()
