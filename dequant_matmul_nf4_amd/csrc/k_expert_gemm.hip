@@ -284,8 +284,8 @@ hipError_t launch(const ExpertGemmArgs& a, hipStream_t s) {
 hipError_t launch_expert_gemm(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const ExpertRows& er,
                               const ExpertX& ex, uint16_t* y, hipStream_t s) {
   // By the mean number of rows of an expert (the only one known here).  Measured in
-  // us: streaming tiles of 16 rows, then tiles of 64, of 128, and of 256 rows with
-  // 64-row tiles for the rest:
+  // us, rows unevenly spread, stacks changing from call to call: streaming tiles of
+  // 16 rows, then tiles of 64, of 128, and of 256 rows with 64-row tiles for the rest:
   //   8 experts of 14336x4096, mean  10:   68  106  146  108
   //                                  40:  153  173  152  176
   //                                  64:  239  179  218  183
@@ -297,6 +297,10 @@ hipError_t launch_expert_gemm(const uint8_t* packed, int64_t rows, int64_t cols,
   //                                  64:   80   55   82   58
   //                                 128:  143   92   86   94
   //                                 256:  265  137  128  124
+  // The last bound lies between the two shapes' crossings, of which the first is
+  // below 224 and the second above 128: at 224 it costs the first 12%.  What the
+  // spread does to full rounds is not known here either: 8 of 14336x4096 at a mean
+  // of 64 take 117 us where the rows are evenly spread.
   const int64_t experts = er.experts;
   if (er.m <= 40 * experts) return launch_expert_skinny(packed, rows, cols, sc, er, ex, y, s);
   ExpertGemmArgs a{};

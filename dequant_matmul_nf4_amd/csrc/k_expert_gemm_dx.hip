@@ -279,9 +279,9 @@ hipError_t launch_expert_gemm_dx(const uint8_t* packed, int64_t rows, int64_t co
                                  const uint16_t* dy, uint16_t* dx, hipStream_t s) {
   // By the mean number of rows of an expert (the only one known here) and whether
   // about this many tiles of 64 rows occupy most compute units; if not, the kernel
-  // that splits the reduction.  Measured in us: that kernel
-  // (k_expert_skinny_dx.hip), then tiles of 64 and of 128 rows, and full rounds of
-  // 256 rows here:
+  // that splits the reduction.  Measured in us, rows unevenly spread, stacks changing
+  // from call to call: that kernel (k_expert_skinny_dx.hip), then tiles of 64 and of
+  // 128 rows, and full rounds of 256 rows here:
   //   64 experts of 1024x2048,  mean  12:   48   31   42   34
   //                                   48:   61   44   66   47
   //                                  160:  126   89   90   93
@@ -295,6 +295,8 @@ hipError_t launch_expert_gemm_dx(const uint8_t* packed, int64_t rows, int64_t co
   //   8 of 14336x4096,          mean  32:  186  208  209  212
   //                                  150:  307  281  218  285
   //                                  512:  874  704  678  589
+  // (Where 64-row tiles fill one round and a little of the next, 128-row tiles are
+  // faster from a lower mean on: 16 of 4096x4096 at 24, 12%.)
   const int64_t experts = er.experts, tiles_k = (cols + gt::kTileN - 1) / gt::kTileN;
   const int64_t about = ((er.m < experts ? er.m : experts) / 2 + er.m / 64) * tiles_k;
   if (8 * about < 5 * device_cus()) return launch_expert_skinny_dx(packed, rows, cols, sc, er, dy, dx, s);

@@ -19,12 +19,13 @@
 // lookup to line up the operands: 66 against 57 us (16 rows over 8 experts of
 // 14336x4096).
 //
-// That product takes 49 us now (4.5 TB/s; its codes and scales take 43 us at the
-// rate of a large copy).  One row alone takes 16 us, where launch, offsets, index
-// and x follow each other.  Measured without gain: 16 waves with steps of 256
-// columns, three or four steps on their way, codes kept in the caches, groups
-// taken in rotated order.  Rows of more than 4096 columns re-read x for every
-// batch of groups (14336 columns, 16 rows: 82 us).
+// That product takes 49 us now where 7 of the 8 experts have rows (4.4 TB/s; the
+// codes and scales of 7 take 42 us at the rate of a large copy), 56 us where all
+// have (47 us).  One row alone takes 15 us (6 us), where launch, offsets, index and
+// x follow each other.  Measured without gain: 16 waves with steps of 256 columns,
+// three or four steps on their way, codes kept in the caches, groups taken in
+// rotated order.  Rows of more than 4096 columns re-read x for every batch of groups
+// (8 experts of 4096x14336, 16 rows: 72 us).
 #include "expert_tiles.h"
 #include "skinny_tile.h"
 

@@ -17,10 +17,10 @@
 // Bound: reading the codes, so waves work on their own (no barrier in the loop)
 // with the next steps' loads on their way; a workgroup's 8 waves are 1 or 2
 // column chunks x 8 or 4 slices of the reduction, whose partial tiles are added
-// in slice order at the end.  16 rows over 8 experts of 14336x4096: 84 us; 512: 210
-// us (253 us with whole reductions on half of the compute units,
-// k_expert_gemm_dx.hip).  In tall tiles the loads of dy, 16 lines each, add up to
-// as much as the products.
+// in slice order at the end.  16 rows over 8 experts of 14336x4096: 84 us (47 us
+// at the rate of a large copy); 256 rows, evenly spread: 108 us.  A lane's 4-byte
+// loads cost 723 load instructions a wave where the forward product has 260.  In
+// tall tiles the loads of dy, 16 lines each, add up to as much as the products.
 #include "expert_tiles.h"
 #include "skinny_tile.h"
 
@@ -292,11 +292,21 @@ hipError_t launch_expert_skinny_dx(const uint8_t* packed, int64_t rows, int64_t 
   a.packed = packed; a.rows = rows; a.cols = cols; a.sc = sc; a.er = er; a.dy = dy; a.dx = dx;
   a.cb = codebook(sc.fp4);
   // Taller tiles expand the weights for more rows, but an expert's last tile is
-  // emptier.  While reading the codes is what takes the time, 32 rows cost what 16
-  // do, and an expert of more rows than the mean needs no second tile.  64 rows
-  // against 128 at a mean of 64 rows: 211 against 280 us (8 experts of
-  // 14336x4096), 73 against 94 us (64 of 1024x2048); at 128: 324 against 303 us,
-  // 110 against 100 us.
+  // emptier and a step takes longer.  Measured in us, rows evenly spread, stacks
+  // changing from call to call: tiles of 32, 64 and 128 rows.
+  //   8 experts of 14336x4096, mean   2:   89   97  148
+  //                                  32:  105  109  141
+  //   4 of 2048x8192,          mean   4:   22   22   29
+  //                                  32:   27   26   30
+  //   2 of 14336x4096,         mean  64:   88  118  137
+  //                                 256:  155  112  162
+  //   2 of 4096x2048,          mean 450:   50   37   51
+  //   1 of 14336x8192,         mean 280:  226  193  142
+  //   1 of 16384x4096,         mean 600:  237  201  164
+  // While one round of the compute units takes all tiles, lower ones are as fast
+  // or faster; where they need another round, taller ones are.  The mean is a
+  // rough sign of that: it errs where few experts have their rows in one round
+  // (2 of 14336x4096 at 256: 128-row tiles, 162 us).
   const int64_t mean = er.m / er.experts;
   if (mean < 16) launch<2>(a, s);
   else if (mean < 96) launch<4>(a, s);

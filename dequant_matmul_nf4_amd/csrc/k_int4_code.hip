@@ -11,7 +11,7 @@
 // rint() is to even.  A group whose s is 0 gets q = z (asymmetric: 0).
 //
 // Both are bound by HBM: a value is touched once (28672x8192 bf16: quantizer
-// 113 us, 5.2 TB/s; expanded to float32 143 us, written non-temporally at 6.6
+// 117 us, 5.1 TB/s; expanded to float32 143 us, written non-temporally at 6.6
 // TB/s, 274 us with plain stores).  The groups tile the
 // flattened weight (cols is a multiple of the group), so a lane takes 16
 // consecutive values, a group is 2, 4 or 8 lanes, and its extremes are found

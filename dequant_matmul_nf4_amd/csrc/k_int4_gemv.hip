@@ -13,11 +13,12 @@
 // largest float32 scales.  (An offset of 1 on q / 16 in [0, 1) costs the sum about two
 // bits; 128 + q, whose offset needs no shift, would cost five.)
 //
-// Bound: reading the codes; skinny_tile.h has the walk.  28672x8192 takes 29 us at
-// m = 1 with groups of 128 (4.2 TB/s), 37 us at m = 16 with groups of 64 and zero
-// points (3.5 TB/s; 25 us at the rate of a large copy); groups of 32 47 to 52 us:
-// each scale costs 8 multiply-adds of a lane.  4096x4096 takes 7 us: launch, x, one
-// step and the join follow each other.
+// Bound: reading the codes; skinny_tile.h has the walk.  With weights that change
+// from call to call 28672x8192 takes 29 us at m = 1 with groups of 128 (4.2 TB/s),
+// 39 us at m = 16 with groups of 64 and zero points (3.3 TB/s; 25 us at the rate of
+// a large copy; the VALU is busy 39% of the time, a step of 4 KiB takes 359 of its
+// instructions); groups of 32 53 us: each scale costs 8 multiply-adds of a lane.
+// 4096x4096 takes 7 us: launch, x, one step and the join follow each other.
 #include "expert_int4.h"
 #include "skinny_tile.h"
 
@@ -288,8 +289,9 @@ template <bool kF16, int kGrp, bool kWide>
 void launch(const Int4Args& a, dim3 gd, hipStream_t s) {
   // A wave's columns in one segment: x is read once and the batch only decides
   // how often partial tiles are added up.  Otherwise x is read once a batch:
-  // as many groups as a wave has, up to 8 (28672x8192 at m = 16, 7 groups a
-  // wave: 36 us with 8, 44 with 4; 8192x28672, 2 groups: 60 us with 4, 65 with 8).
+  // about as many groups as a wave has, 2 or 8 (groups of 64 at m = 16, 2, 4 and
+  // 8 a batch: 28672x8192, 7 groups a wave, 63, 46 and 38 us; 16384x8192, 4
+  // groups, 36, 26 and 29 us; 8192x28672, 2 groups, 56, 62 and 69 us).
   const int64_t groups = (a.rows + 15) / 16, each = groups / (static_cast<int64_t>(gd.x) * a.pl.rs);
   const dim3 bd(sk::kThreads);
   if (a.pl.per <= kSeg) hipLaunchKernelGGL((k_int4_gemv<kF16, kGrp, kWide, 4, true>), gd, bd, 0, s, a);

@@ -2,9 +2,10 @@
 promise, against float64.
 
 Precision of a product of few rows per expert (at most 40 on the mean): levels
-rounded to float16 (off by at most 2^-11 of their value), x taken exactly, the
-block scale and the sums in float32, one rounding to bfloat16.  Per output, with
-S = sum |x| |w| over K columns: 2^-8 of the value, and (2^-11 + (K + 8) 2^-24) S
+rounded to float16 (off by at most 2^-11 of their value; not the two bfloat16
+parts of an earlier kernel that test_gpu_expert.py's introduction has), x taken
+exactly, the block scale and the sums in float32, one rounding to bfloat16.  Per
+output, with S = sum |x| |w| over K columns: 2^-8 of the value, and (2^-11 + (K + 8) 2^-24) S
 (K additions; the scale's, the power of two's and the reference weight's
 roundings).  In the mean square the roundings are independent: the error's
 square is that of rounding the reference once, plus the level's,
