@@ -9,6 +9,7 @@ kernels; there is no fallback.  torch supplies device memory and streams.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from dataclasses import dataclass
@@ -26,6 +27,7 @@ NF4_DQ_INT8, NF4_DQ_FP8 = 0, 1
 NF4_QT_NF4, NF4_QT_FP4 = 0, 1
 BLOCKSIZE, BLOCKSIZE2 = 64, 256
 MAX_EXPERTS = 1024
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # enum nf4_act
 
 EXPORTS = (
     "nf4_last_error", "nf4_codebook", "nf4_codebook_fp4", "nf4_quantize", "nf4_quantize_fp4", "nf4_double_quant_workspace",
@@ -34,6 +36,8 @@ EXPORTS = (
     "nf4_gemv_batched", "nf4_double_quant_batched_workspace", "nf4_double_quant_batched", "nf4_quantize_batched",
     "nf4_expert_plan_workspace", "nf4_expert_plan", "nf4_expert_gemm", "nf4_expert_gemm_dx", "nf4_expert_combine",
     "nf4_expert_combine_backward", "nf4_int4_quantize", "nf4_int4_dequantize", "nf4_int4_gemv",
+    "nf4_linear_workspace", "nf4_linear", "nf4_act_backward_workspace", "nf4_act_backward", "nf4_expert_balance_workspace",
+    "nf4_expert_balance", "nf4_expert_balance_backward", "nf4_grad_workspace", "nf4_grad_norm", "nf4_grad_clip",
 )
 
 
@@ -71,6 +75,22 @@ class nf4_int4_weight(ctypes.Structure):
     _fields_ = [
         ("packed", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("group", ctypes.c_int32),
         ("scale_dtype", ctypes.c_int32), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+    ]
+
+
+class nf4_epilogue(ctypes.Structure):
+    """Mirror of `struct nf4_epilogue` in include/nf4.h."""
+    _fields_ = [
+        ("bias", ctypes.c_void_p), ("bias_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+        ("residual", ctypes.c_void_p), ("pre", ctypes.c_void_p),
+    ]
+
+
+class nf4_grad(ctypes.Structure):
+    """Mirror of `struct nf4_grad` in include/nf4.h."""
+    _fields_ = [
+        ("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
     ]
 
 
@@ -121,6 +141,16 @@ def lib() -> ctypes.CDLL:
         "nf4_int4_quantize": (ctypes.c_int, [vp, ctypes.c_int, i4p, vp]),
         "nf4_int4_dequantize": (ctypes.c_int, [i4p, vp, ctypes.c_int, vp]),
         "nf4_int4_gemv": (ctypes.c_int, [i4p, vp, ctypes.c_int, i64, vp, ctypes.c_int, vp]),
+        "nf4_linear_workspace": (sz, [i64, i64, i64, i32]),
+        "nf4_linear": (ctypes.c_int, [wp, vp, i64, vp, ctypes.POINTER(nf4_epilogue), vp, vp, i32, ctypes.c_float, vp, sz, vp]),
+        "nf4_act_backward_workspace": (sz, [i64, i64]),
+        "nf4_act_backward": (ctypes.c_int, [vp, vp, i64, i64, i32, vp, vp, vp, sz, vp]),
+        "nf4_expert_balance_workspace": (sz, [i64, i32]),
+        "nf4_expert_balance": (ctypes.c_int, [vp, ctypes.c_int, vp, vp, i64, i32, i32, ctypes.c_float, vp, vp, vp, vp, sz, vp]),
+        "nf4_expert_balance_backward": (ctypes.c_int, [vp, ctypes.c_int, vp, vp, i64, i32, i32, ctypes.c_float, vp, vp, vp]),
+        "nf4_grad_workspace": (sz, [i32]),
+        "nf4_grad_norm": (ctypes.c_int, [vp, i32, vp, vp, sz, vp]),
+        "nf4_grad_clip": (ctypes.c_int, [vp, i32, ctypes.c_float, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -173,6 +203,22 @@ def nf4_gemm_dx_workspace(m: int, rows: int, r: int) -> int:
 
 def nf4_expert_plan_workspace(n: int, experts: int) -> int:
     return int(lib().nf4_expert_plan_workspace(n, experts))
+
+
+def nf4_linear_workspace(m: int, rows: int, cols: int, r: int = 0) -> int:
+    return int(lib().nf4_linear_workspace(m, rows, cols, r))
+
+
+def nf4_act_backward_workspace(m: int, rows: int) -> int:
+    return int(lib().nf4_act_backward_workspace(m, rows))
+
+
+def nf4_expert_balance_workspace(tokens: int, experts: int) -> int:
+    return int(lib().nf4_expert_balance_workspace(tokens, experts))
+
+
+def nf4_grad_workspace(count: int) -> int:
+    return int(lib().nf4_grad_workspace(count))
 
 
 def nf4_lora_grads_workspace(m: int, rows: int, cols: int, r: int) -> int:
@@ -969,3 +1015,262 @@ def nf4_int4_gemv(w: Int4Weight, x, y=None, y_dtype=None, stream=None):
         _need("y", y, y.dtype, m * w.rows, dev)
     _call(dev, stream, lib().nf4_int4_gemv, ctypes.byref(cs), x2.data_ptr(), _dtype_code(x2), m, y.data_ptr(), _dtype_code(y))
     return y
+
+
+# ------------------------------------------ around the products in a layer
+
+def _act(name) -> int:
+    if name not in ACTS:
+        raise ValueError(f"act {name!r}: one of {', '.join(ACTS)}")
+    return ACTS[name]
+
+
+def _work(workspace, need: int, stream, dev):
+    """The caller's workspace, or one of `need` bytes; and its size."""
+    if workspace is None:
+        return (_alloc_on(stream, (need,), _torch().uint8, dev), need) if need else (None, 0)
+    _need_cuda(workspace)
+    _same_device(dev, workspace)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def nf4_linear(w: NF4Weight, x, bias=None, act: str = "none", residual=None, lora_a=None, lora_b=None,
+               lora_scale: float = 0.0, y=None, pre=None, save_pre: bool = False, workspace=None, stream=None):
+    """y = act(z) + residual with z = x . deq(W)^T + lora_scale . (x . A^T) . B^T
+    + bias, for any number of rows of x; bf16 in and out, bias bf16 or float32
+    [rows], act one of ACTS, residual [m, rows] (may be y itself: added in
+    place).  save_pre (or a buffer as pre): returns (y, pre) with pre = z in
+    bf16, which nf4_act_backward takes."""
+    torch = _torch()
+    x2 = _as_rows(x, w.cols, stream)
+    cs = w.c_struct()
+    dev, m, rows = w.device, x2.shape[0], w.rows
+    bf16 = torch.bfloat16
+    _need("x", x2, bf16, m * w.cols, dev)
+    ep = nf4_epilogue(act=_act(act))
+    if bias is not None:
+        if bias.dtype not in (torch.float32, bf16):
+            raise TypeError(f"bias has dtype {bias.dtype}: float32 or bf16")
+        _need("bias", bias, bias.dtype, rows, dev)
+        ep.bias, ep.bias_dtype = bias.data_ptr(), NF4_F32 if bias.dtype == torch.float32 else NF4_BF16
+    if residual is not None:
+        _need("residual", residual, bf16, m * rows, dev)
+        ep.residual = residual.data_ptr()
+    if (lora_a is None) != (lora_b is None):
+        raise ValueError("lora_a and lora_b come together")
+    r = 0
+    if lora_a is not None:
+        r = lora_a.shape[0]
+        if tuple(lora_a.shape) != (r, w.cols) or tuple(lora_b.shape) != (rows, r):
+            raise ValueError("LoRA shapes must be A [r, cols] and B [rows, r]")
+        _need("lora_a", lora_a, bf16, r * w.cols, dev)
+        _need("lora_b", lora_b, bf16, rows * r, dev)
+    if y is None:
+        y = _alloc_on(stream, (m, rows), bf16, dev)
+    else:
+        _need("y", y, bf16, m * rows, dev)
+    if pre is None and save_pre:
+        pre = _alloc_on(stream, (m, rows), bf16, dev)
+    if pre is not None:
+        _need("pre", pre, bf16, m * rows, dev)
+        ep.pre = pre.data_ptr()
+    if m:
+        workspace, wsn = _work(workspace, lib().nf4_linear_workspace(m, rows, w.cols, r), stream, dev)
+        _call(dev, stream, lib().nf4_linear, ctypes.byref(cs), x2.data_ptr(), m, y.data_ptr(), ctypes.byref(ep), _ptr(lora_a),
+              _ptr(lora_b), r, float(lora_scale), _ptr(workspace), wsn)
+    return y if pre is None else (y, pre)
+
+
+def nf4_act_backward(dy, pre, act: str, dz=None, dbias=None, want=("dz", "dbias"), workspace=None, stream=None):
+    """The backward pass of nf4_linear's epilogue: (dz [m, rows] bf16, dbias
+    [rows] float32) with dz = dy . act'(pre) and dbias the sum of its rows
+    before their rounding; one not in `want` (and not given) is None.  dz goes
+    to nf4_gemm_dx and nf4_lora_grads as their dy, and may be dy itself; pre may
+    be None for act "none"."""
+    torch = _torch()
+    code = _act(act)
+    if dy.dim() < 1:
+        raise ValueError("dy must be [m, rows]")
+    rows = dy.shape[-1]
+    dy2 = _as_rows(dy, rows, stream) if rows else dy
+    dev, n = dy.device, dy.numel()
+    m = n // rows if rows else 0
+    _need("dy", dy2, torch.bfloat16, n, dev)
+    if rows < 1:
+        raise ValueError("dy must have at least one column")
+    pre2 = None
+    if pre is not None:
+        pre2 = _as_rows(pre, rows, stream)
+        _need("pre", pre2, torch.bfloat16, n, dev)
+    elif act != "none":
+        raise ValueError(f"act {act!r} needs pre")
+    if dz is None and "dz" in want:
+        dz = _alloc_on(stream, (m, rows), torch.bfloat16, dev)
+    if dbias is None and "dbias" in want:
+        dbias = _alloc_on(stream, (rows,), torch.float32, dev)
+    if dz is not None:
+        _need("dz", dz, torch.bfloat16, n, dev)
+    if dbias is not None:
+        _need("dbias", dbias, torch.float32, rows, dev)
+    if m == 0:
+        if dbias is not None:
+            _zero(dbias, stream)
+        return dz, dbias
+    need = lib().nf4_act_backward_workspace(m, rows) if dbias is not None else 0
+    workspace, wsn = _work(workspace, need, stream, dev)
+    _call(dev, stream, lib().nf4_act_backward, dy2.data_ptr(), _ptr(pre2), m, rows, code, _ptr(dz), _ptr(dbias), _ptr(workspace), wsn)
+    return dz, dbias
+
+
+def _router(logits, slots: int, mask):
+    """(tokens, experts, mask as bytes) of a router's logits."""
+    torch = _torch()
+    if logits.dim() != 2 or not 1 <= logits.shape[1] <= MAX_EXPERTS:
+        raise ValueError(f"logits must be [tokens, experts] with 1 to {MAX_EXPERTS} experts")
+    if not 1 <= slots < 2 ** 31:
+        raise ValueError(f"slots = {slots}: at least 1")
+    _dtype_code(logits)
+    tokens, experts = logits.shape
+    _need("logits", logits, logits.dtype, tokens * experts, logits.device)
+    if mask is not None:
+        if mask.dtype == torch.bool:
+            mask = mask.view(torch.uint8)
+        _need("mask", mask, torch.uint8, tokens, logits.device)
+    return tokens, experts, mask
+
+
+def nf4_expert_balance(logits, ids, slots: int, coef: float, mask=None, loss=None, counts=None, mean_probs=None,
+                       workspace=None, stream=None):
+    """The routers' balance loss for logits [tokens, experts] (float32, bf16 or
+    fp16) and the chosen experts' ids (int32, `slots` per token; a number outside
+    0 .. experts - 1 is not counted): returns (loss [1], counts [experts + 1],
+    mean_probs [experts]).  counts[:experts] are the slots by expert, the last
+    entry the number of tokens kept by mask (bool or uint8 [tokens]; 0: left
+    out).  loss = coef . experts . sum_e counts[e] / (kept . slots) . mean_probs[e]."""
+    torch = _torch()
+    tokens, experts, mask = _router(logits, slots, mask)
+    dev = logits.device
+    _need("ids", ids, torch.int32, tokens * slots, dev)
+
+    def out(name, t, count, dtype):
+        if t is None:
+            return _alloc_on(stream, (count,), dtype, dev)
+        _need(name, t, dtype, count, dev)
+        return t
+
+    loss = out("loss", loss, 1, torch.float32)
+    counts = out("counts", counts, experts + 1, torch.int32)
+    mean_probs = out("mean_probs", mean_probs, experts, torch.float32)
+    if tokens == 0:
+        for t in (loss, counts, mean_probs):
+            _zero(t, stream)
+        return loss, counts, mean_probs
+    workspace, wsn = _work(workspace, lib().nf4_expert_balance_workspace(tokens, experts), stream, dev)
+    _call(dev, stream, lib().nf4_expert_balance, logits.data_ptr(), _dtype_code(logits), ids.data_ptr(), _ptr(mask), tokens,
+          experts, slots, float(coef), loss.data_ptr(), counts.data_ptr(), mean_probs.data_ptr(), _ptr(workspace), wsn)
+    return loss, counts, mean_probs
+
+
+def nf4_expert_balance_backward(logits, counts, slots: int, coef: float, mask=None, dloss=None, dlogits=None, stream=None):
+    """The gradient of nf4_expert_balance's loss for the logits, in their dtype;
+    counts as it returned them, dloss float32 [1] (None: 1).  dlogits may be
+    logits itself."""
+    torch = _torch()
+    tokens, experts, mask = _router(logits, slots, mask)
+    dev = logits.device
+    _need("counts", counts, torch.int32, experts + 1, dev)
+    if dloss is not None:
+        _need("dloss", dloss, torch.float32, 1, dev)
+    if dlogits is None:
+        dlogits = _alloc_on(stream, (tokens, experts), logits.dtype, dev)
+    else:
+        _need("dlogits", dlogits, logits.dtype, tokens * experts, dev)
+    if tokens:
+        _call(dev, stream, lib().nf4_expert_balance_backward, logits.data_ptr(), _dtype_code(logits), counts.data_ptr(),
+              _ptr(mask), tokens, experts, slots, float(coef), _ptr(dloss), dlogits.data_ptr())
+    return dlogits
+
+
+def _grad_list(grads, out=None):
+    """(array of nf4_grad, device) of gradients that are scaled in place, or into
+    the flat tensor out, one after another."""
+    torch = _torch()
+    codes = {torch.float32: NF4_F32, torch.bfloat16: NF4_BF16, torch.float16: NF4_F16}
+    kinds = {(t.dtype, t.device, t.is_contiguous()) for t in grads}
+    dev = grads[0].device
+    for dtype, d, whole in kinds:
+        if dtype not in codes:
+            raise TypeError(f"unsupported dtype {dtype}")
+        if d.type != "cuda" or not whole:
+            raise ValueError("gradients must be contiguous device tensors")
+        if d != dev:
+            raise ValueError(f"gradient on {d}, expected {dev}")
+    words = array.array("q")
+    if out is None:
+        for t in grads:
+            p, c = t.data_ptr(), codes[t.dtype]
+            words.extend((p, p, t.numel(), c | c << 32))
+        return words, dev
+    if out.dtype not in codes:
+        raise TypeError(f"unsupported dtype {out.dtype}")
+    _need("out", out, out.dtype, sum(t.numel() for t in grads), dev)
+    at, size, code = out.data_ptr(), out.element_size(), codes[out.dtype]
+    lo, hi = at, at + out.numel() * size
+    for t in grads:
+        p, n, c = t.data_ptr(), t.numel(), codes[t.dtype]
+        if p < hi and p + n * (4 if c == NF4_F32 else 2) > lo and n and (p != at or c != code):
+            raise ValueError("out shares memory with a gradient that does not lie exactly in its place")
+        words.extend((p, at, n, c | code << 32))
+        at += n * size
+    return words, dev
+
+
+def _apart(words) -> None:
+    """Gradients that are scaled in place must not share memory."""
+    size = (4, 2, 2)
+    spans = sorted((p, p + n * size[c & 3]) for p, n, c in zip(words[0::4], words[2::4], words[3::4]) if n)
+    for (_, end), (begin, _) in zip(spans, spans[1:]):
+        if begin < end:
+            raise ValueError("two of the gradients share memory: scaled in place, each may be given once")
+
+
+def nf4_grad_norm(grads, norm=None, workspace=None, stream=None):
+    """The norm over many gradients (float32, bf16 or fp16 of any shapes, at
+    least one tensor): float32 [1], summed in float64."""
+    torch = _torch()
+    grads = list(grads)
+    if not grads:
+        raise ValueError("at least one gradient")
+    words, dev = _grad_list(grads)
+    if norm is None:
+        norm = _alloc_on(stream, (1,), torch.float32, dev)
+    else:
+        _need("norm", norm, torch.float32, 1, dev)
+    workspace, wsn = _work(workspace, lib().nf4_grad_workspace(len(grads)), stream, dev)
+    _call(dev, stream, lib().nf4_grad_norm, words.buffer_info()[0], len(grads), norm.data_ptr(), workspace.data_ptr(), wsn)
+    return norm
+
+
+def nf4_grad_clip(grads, max_norm: float, total_norm=None, out=None, norm=None, workspace=None, stream=None):
+    """Scales gradients by min(1, max_norm / (norm + 1e-6)), where norm is that
+    of nf4_grad_norm over them, or total_norm (float32 [1]: one over more than
+    these, as where they are sharded).  In place, or with out, a flat tensor of
+    their number of values and any of the dtypes, into that, one after another.
+    Returns the norm float32 [1], and with out (norm, out)."""
+    torch = _torch()
+    grads = list(grads)
+    if not grads:
+        raise ValueError("at least one gradient")
+    words, dev = _grad_list(grads, out)
+    if out is None:
+        _apart(words)
+    if total_norm is not None:
+        _need("total_norm", total_norm, torch.float32, 1, dev)
+    if norm is None:
+        norm = _alloc_on(stream, (1,), torch.float32, dev)
+    else:
+        _need("norm", norm, torch.float32, 1, dev)
+    workspace, wsn = _work(workspace, lib().nf4_grad_workspace(len(grads)), stream, dev)
+    _call(dev, stream, lib().nf4_grad_clip, words.buffer_info()[0], len(grads), float(max_norm), _ptr(total_norm),
+          norm.data_ptr(), workspace.data_ptr(), wsn)
+    return norm if out is None else (norm, out)

@@ -11,6 +11,7 @@
 
 #include "nf4.h"
 #include "expert_int4.h"
+#include "layer_ops.h"
 #include "nf4_internal.h"
 
 namespace {
@@ -664,6 +665,188 @@ int nf4_int4_gemv(const nf4_int4_weight* w, const void* x, int x_dtype, int64_t 
   return launched(nf4i::launch_int4_gemv(iw, static_cast<const uint16_t*>(x), x_dtype == NF4_F16, m, y, y_dtype,
                                          as_stream(stream)),
                   who);
+}
+
+// ---- around the products in a layer
+
+size_t nf4_linear_workspace(int64_t m, int64_t rows, int64_t cols, int32_t r) {
+  if (m < 1 || m > kMaxRows || rows < 1 || rows > kMaxN || cols < 1 || cols >= (int64_t(1) << 23) || r < 0 || r > 64) return 0;
+  return (nf4i::linear_workspace(m, rows, cols, r) + 255) & ~size_t(255);
+}
+
+int nf4_linear(const nf4_weight* w, const void* x, int64_t m, void* y, const nf4_epilogue* ep, const void* lora_a,
+               const void* lora_b, int32_t r, float lora_scale, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "nf4_linear";
+  nf4i::Scales sc{};
+  int64_t n = 0;
+  if (int rc = check_weight(w, &sc, &n, who)) return rc;
+  if (!x || !y) return fail(NF4_ERR_NULL, "%s: x and y are required", who);
+  if (w->cols % 64) return fail(NF4_ERR_SIZE, "%s: cols = %lld is not a multiple of 64", who, (long long)w->cols);
+  if (w->cols >= (int64_t(1) << 23)) return fail(NF4_ERR_SIZE, "%s: cols = %lld out of range", who, (long long)w->cols);
+  if (m < 1 || m > kMaxRows) return fail(NF4_ERR_SIZE, "%s: m = %lld out of range", who, (long long)m);
+  nf4i::Epilogue e{};
+  if (ep) {
+    if (ep->act < NF4_ACT_NONE || ep->act > NF4_ACT_GELU_TANH) return fail(NF4_ERR_DTYPE, "%s: act %d unknown", who, (int)ep->act);
+    if (ep->bias && ep->bias_dtype != NF4_F32 && ep->bias_dtype != NF4_BF16)
+      return fail(NF4_ERR_DTYPE, "%s: bias_dtype %d is not NF4_F32 or NF4_BF16", who, (int)ep->bias_dtype);
+    if (!aligned(ep->bias, ep->bias_dtype == NF4_F32 ? 4 : 2)) return fail(NF4_ERR_ALIGN, "%s: bias must be aligned to its type", who);
+    if (!aligned(ep->residual, 16) || !aligned(ep->pre, 16))
+      return fail(NF4_ERR_ALIGN, "%s: residual and pre must be 16-byte aligned", who);
+    if (ep->pre && (ep->pre == y || ep->pre == ep->residual || ep->pre == x))
+      return fail(NF4_ERR_ALIGN, "%s: pre must be a buffer of its own", who);
+    e = nf4i::Epilogue{ep->bias, ep->bias_dtype == NF4_F32, ep->act, static_cast<const uint16_t*>(ep->residual),
+                       static_cast<uint16_t*>(ep->pre)};
+  }
+  if (x == y) return fail(NF4_ERR_ALIGN, "%s: y must not be x", who);
+  if ((lora_a == nullptr) != (lora_b == nullptr))
+    return fail(NF4_ERR_NULL, "%s: lora_a and lora_b must both be NULL or both be set", who);
+  if (lora_a) {
+    if (r < 1 || r > 64) return fail(NF4_ERR_SIZE, "%s: LoRA rank r = %d out of range 1..64", who, (int)r);
+    if (!std::isfinite(lora_scale)) return fail(NF4_ERR_SIZE, "%s: lora_scale is not finite", who);
+    if (!aligned(lora_a, 16) || !aligned(lora_b, 16))
+      return fail(NF4_ERR_ALIGN, "%s: lora_a and lora_b must be 16-byte aligned", who);
+  } else if (r != 0) {
+    return fail(NF4_ERR_SIZE, "%s: r must be 0 without LoRA matrices", who);
+  }
+  const size_t need = nf4_linear_workspace(m, w->rows, w->cols, r);
+  if (need && (!workspace || workspace_bytes < need)) return fail(NF4_ERR_WORKSPACE, "%s: workspace needs %zu bytes", who, need);
+  if (need && !aligned(workspace, 256)) return fail(NF4_ERR_ALIGN, "%s: workspace must be 256-byte aligned", who);
+  if (!aligned(x, 16) || !aligned(y, 16)) return fail(NF4_ERR_ALIGN, "%s: x and y must be 16-byte aligned", who);
+  if (int rc = check_device()) return rc;
+  return launched(nf4i::launch_linear(w->packed, w->rows, w->cols, sc, static_cast<const uint16_t*>(x), m,
+                                      static_cast<uint16_t*>(y), e, static_cast<const uint16_t*>(lora_a),
+                                      static_cast<const uint16_t*>(lora_b), r, lora_scale, workspace, as_stream(stream)),
+                  who);
+}
+
+static bool act_backward_size(int64_t m, int64_t rows) {
+  return m >= 1 && m <= kMaxRows && rows >= 1 && rows < kMaxRows && m <= kMaxN / rows;
+}
+
+size_t nf4_act_backward_workspace(int64_t m, int64_t rows) {
+  return act_backward_size(m, rows) ? nf4i::act_backward_workspace(m, rows) : 0;
+}
+
+int nf4_act_backward(const void* dy, const void* pre, int64_t m, int64_t rows, int32_t act, void* dz, float* dbias,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "nf4_act_backward";
+  if (!dy) return fail(NF4_ERR_NULL, "%s: dy is required", who);
+  if (act < NF4_ACT_NONE || act > NF4_ACT_GELU_TANH) return fail(NF4_ERR_DTYPE, "%s: act %d unknown", who, (int)act);
+  if (!pre && act != NF4_ACT_NONE) return fail(NF4_ERR_NULL, "%s: pre is required", who);
+  if (!dz && !dbias) return fail(NF4_ERR_NULL, "%s: at least one of dz and dbias is required", who);
+  if (!act_backward_size(m, rows))
+    return fail(NF4_ERR_SIZE, "%s: m = %lld, rows = %lld out of range", who, (long long)m, (long long)rows);
+  if (!aligned(dy, 16) || !aligned(pre, 16) || !aligned(dz, 16))
+    return fail(NF4_ERR_ALIGN, "%s: dy, pre and dz must be 16-byte aligned", who);
+  if (!aligned(dbias, 4)) return fail(NF4_ERR_ALIGN, "%s: dbias must be 4-byte aligned", who);
+  if (dz && dz == pre) return fail(NF4_ERR_ALIGN, "%s: dz must not be pre", who);
+  const size_t need = dbias ? nf4_act_backward_workspace(m, rows) : 0;
+  if (need && (!workspace || workspace_bytes < need)) return fail(NF4_ERR_WORKSPACE, "%s: workspace needs %zu bytes", who, need);
+  if (need && !aligned(workspace, 4)) return fail(NF4_ERR_ALIGN, "%s: workspace must be 4-byte aligned", who);
+  if (int rc = check_device()) return rc;
+  return launched(nf4i::launch_act_backward(static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(pre), m, rows, act,
+                                            static_cast<uint16_t*>(dz), dbias, static_cast<float*>(workspace),
+                                            as_stream(stream)),
+                  who);
+}
+
+static bool balance_size(int64_t tokens, int32_t experts, int32_t slots) {
+  return tokens >= 1 && tokens < kMaxRows && experts >= 1 && experts <= NF4_MAX_EXPERTS && slots >= 1 && tokens * slots < kMaxRows;
+}
+
+size_t nf4_expert_balance_workspace(int64_t tokens, int32_t experts) {
+  return balance_size(tokens, experts, 1) ? nf4i::expert_balance_workspace(tokens, experts) : 0;
+}
+
+static int check_balance(const void* logits, int dtype, int64_t tokens, int32_t experts, int32_t slots, float coef,
+                         const char* who) {
+  if (!known_dtype(dtype)) return fail(NF4_ERR_DTYPE, "%s: dtype %d unknown", who, dtype);
+  if (int rc = check_experts(experts, who)) return rc;
+  if (!balance_size(tokens, experts, slots))
+    return fail(NF4_ERR_SIZE, "%s: tokens = %lld, slots = %d out of range", who, (long long)tokens, (int)slots);
+  if (!std::isfinite(coef)) return fail(NF4_ERR_SIZE, "%s: coef is not finite", who);
+  if (!aligned(logits, dtype == NF4_F32 ? 4 : 2)) return fail(NF4_ERR_ALIGN, "%s: logits must be aligned to their type", who);
+  return NF4_OK;
+}
+
+int nf4_expert_balance(const void* logits, int dtype, const int32_t* ids, const uint8_t* mask, int64_t tokens,
+                       int32_t experts, int32_t slots, float coef, float* loss, int32_t* counts, float* mean_probs,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "nf4_expert_balance";
+  if (!logits || !ids || !loss || !counts || !mean_probs)
+    return fail(NF4_ERR_NULL, "%s: logits, ids, loss, counts and mean_probs are required", who);
+  if (int rc = check_balance(logits, dtype, tokens, experts, slots, coef, who)) return rc;
+  if (!aligned(ids, 4) || !aligned(loss, 4) || !aligned(counts, 4) || !aligned(mean_probs, 4))
+    return fail(NF4_ERR_ALIGN, "%s: ids, loss, counts and mean_probs must be 4-byte aligned", who);
+  const size_t need = nf4_expert_balance_workspace(tokens, experts);
+  if (!workspace || workspace_bytes < need) return fail(NF4_ERR_WORKSPACE, "%s: workspace needs %zu bytes", who, need);
+  if (!aligned(workspace, 8)) return fail(NF4_ERR_ALIGN, "%s: workspace must be 8-byte aligned", who);
+  if (int rc = check_device()) return rc;
+  return launched(nf4i::launch_expert_balance(logits, dtype, ids, mask, tokens, experts, slots, coef, loss, counts, mean_probs,
+                                              workspace, as_stream(stream)),
+                  who);
+}
+
+int nf4_expert_balance_backward(const void* logits, int dtype, const int32_t* counts, const uint8_t* mask, int64_t tokens,
+                                int32_t experts, int32_t slots, float coef, const float* dloss, void* dlogits,
+                                void* stream) {
+  const char* who = "nf4_expert_balance_backward";
+  if (!logits || !counts || !dlogits) return fail(NF4_ERR_NULL, "%s: logits, counts and dlogits are required", who);
+  if (int rc = check_balance(logits, dtype, tokens, experts, slots, coef, who)) return rc;
+  if (!aligned(dlogits, dtype == NF4_F32 ? 4 : 2)) return fail(NF4_ERR_ALIGN, "%s: dlogits must be aligned to their type", who);
+  if (!aligned(counts, 4) || !aligned(dloss, 4)) return fail(NF4_ERR_ALIGN, "%s: counts and dloss must be 4-byte aligned", who);
+  if (int rc = check_device()) return rc;
+  return launched(nf4i::launch_expert_balance_backward(logits, dtype, counts, mask, tokens, experts, slots, coef, dloss, dlogits,
+                                                       as_stream(stream)),
+                  who);
+}
+
+static constexpr int32_t kMaxGrads = 1 << 20;
+
+size_t nf4_grad_workspace(int32_t count) {
+  return count >= 0 && count <= kMaxGrads ? nf4i::grad_workspace(count) : 0;
+}
+
+static int check_grads(const nf4_grad* grads, int32_t count, bool outs, void* workspace, size_t workspace_bytes, const char* who) {
+  if (count < 0 || count > kMaxGrads) return fail(NF4_ERR_SIZE, "%s: count = %d out of range 0..%d", who, (int)count, (int)kMaxGrads);
+  if (count && !grads) return fail(NF4_ERR_NULL, "%s: grads is NULL", who);
+  for (int32_t i = 0; i < count; ++i) {
+    const nf4_grad& g = grads[i];
+    if (g.n < 0 || g.n >= kMaxN) return fail(NF4_ERR_SIZE, "%s: gradient %d: n = %lld out of range", who, (int)i, (long long)g.n);
+    if (!known_dtype(g.dtype) || (outs && !known_dtype(g.out_dtype)))
+      return fail(NF4_ERR_DTYPE, "%s: gradient %d: dtype %d or out_dtype %d unknown", who, (int)i, (int)g.dtype, (int)g.out_dtype);
+    if (g.n && (!g.grad || (outs && !g.out)))
+      return fail(NF4_ERR_NULL, "%s: gradient %d: grad and, to clip, out are required", who, (int)i);
+    if (!aligned(g.grad, g.dtype == NF4_F32 ? 4 : 2) || (outs && !aligned(g.out, g.out_dtype == NF4_F32 ? 4 : 2)))
+      return fail(NF4_ERR_ALIGN, "%s: gradient %d: grad and out must be aligned to their types", who, (int)i);
+    if (outs && g.n && g.out == g.grad && g.dtype != g.out_dtype)
+      return fail(NF4_ERR_DTYPE, "%s: gradient %d: scaled in place, it keeps its dtype", who, (int)i);
+  }
+  const size_t need = nf4_grad_workspace(count);
+  if (!workspace || workspace_bytes < need) return fail(NF4_ERR_WORKSPACE, "%s: workspace needs %zu bytes", who, need);
+  if (!aligned(workspace, 8)) return fail(NF4_ERR_ALIGN, "%s: workspace must be 8-byte aligned", who);
+  return NF4_OK;
+}
+
+int nf4_grad_norm(const nf4_grad* grads, int32_t count, float* norm, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  const char* who = "nf4_grad_norm";
+  if (!norm) return fail(NF4_ERR_NULL, "%s: norm is required", who);
+  if (!aligned(norm, 4)) return fail(NF4_ERR_ALIGN, "%s: norm must be 4-byte aligned", who);
+  if (int rc = check_grads(grads, count, false, workspace, workspace_bytes, who)) return rc;
+  if (int rc = check_device()) return rc;
+  return launched(nf4i::launch_grads(grads, count, false, 0.0f, nullptr, norm, workspace, as_stream(stream)), who);
+}
+
+int nf4_grad_clip(const nf4_grad* grads, int32_t count, float max_norm, const float* total_norm, float* norm,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "nf4_grad_clip";
+  if (!std::isfinite(max_norm) || max_norm < 0) return fail(NF4_ERR_SIZE, "%s: max_norm must be finite and not negative", who);
+  if (!aligned(norm, 4) || !aligned(total_norm, 4))
+    return fail(NF4_ERR_ALIGN, "%s: norm and total_norm must be 4-byte aligned", who);
+  if (int rc = check_grads(grads, count, true, workspace, workspace_bytes, who)) return rc;
+  if (int rc = check_device()) return rc;
+  return launched(nf4i::launch_grads(grads, count, true, max_norm, total_norm, norm, workspace, as_stream(stream)), who);
 }
 
 }  // extern "C"

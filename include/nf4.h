@@ -505,6 +505,137 @@ int nf4_int4_dequantize(const nf4_int4_weight* w, void* out, int out_dtype, void
  * point is applied as a difference of sums) and reaches no other row. */
 int nf4_int4_gemv(const nf4_int4_weight* w, const void* x, int x_dtype, int64_t m, void* y, int y_dtype, void* stream);
 
+/* ------------------------------------------ around the products in a layer
+ *
+ * What a layer adds to its product, the backward pass of that, the routers'
+ * balance loss, and the norm and clipping of a training step's gradients. */
+
+/* Activations of nf4_linear. */
+typedef enum nf4_act {
+  NF4_ACT_NONE = 0,
+  NF4_ACT_RELU = 1,      /* max(z, 0)                                                */
+  NF4_ACT_SILU = 2,      /* z / (1 + exp(-z))                                        */
+  NF4_ACT_GELU = 3,      /* z Phi(z), Phi the normal distribution's integral          */
+  NF4_ACT_GELU_TANH = 4  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2         */
+} nf4_act;
+
+/* [host] What nf4_linear does to its product: a struct of device pointers.
+ * A zero-initialised one does nothing. */
+typedef struct nf4_epilogue {
+  const void* bias;      /* [rows] values of bias_dtype, aligned to it, or NULL           */
+  int32_t bias_dtype;    /* NF4_F32 or NF4_BF16 (read only with a bias)                   */
+  int32_t act;           /* nf4_act                                                       */
+  const void* residual;  /* bf16 [m][rows], 16-byte aligned, or NULL; may be y itself     */
+  void* pre;             /* out: bf16 [m][rows], 16-byte aligned, or NULL                 */
+} nf4_epilogue;
+
+/* Bytes of device workspace nf4_linear needs (0 where it needs none, and for
+ * sizes out of range). */
+size_t nf4_linear_workspace(int64_t m, int64_t rows, int64_t cols, int32_t r);
+
+/* A layer's product, for any number of rows of x from one token to a prompt:
+ *   z   = x . deq(W)^T + lora_scale . (x . A^T) . B^T + bias
+ *   pre = z, rounded once to bf16 (what nf4_act_backward takes)
+ *   y   = act(z) + residual, formed in float32 and rounded once to bf16
+ *   x, y, lora_a, lora_b, r, lora_scale: as nf4_gemm (1 <= m <= 2^31, cols % 64
+ *            == 0, cols < 2^23); y overlaps no input but, where it is the same
+ *            pointer, residual.
+ *   ep     : the epilogue, or NULL for none.  pre overlaps nothing else.
+ *   workspace: at least nf4_linear_workspace(m, rows, cols, r) bytes, 256-byte
+ *            aligned (may be NULL when that is 0); overwritten.
+ * Sums are float32.  The weight enters the products rounded once to bf16 after
+ * scaling, as in nf4_gemm, or as nf4_gemv's streaming form takes it (levels
+ * rounded to fp16, scales in float32), which is closer to it. */
+int nf4_linear(const nf4_weight* w, const void* x, int64_t m, void* y, const nf4_epilogue* ep, const void* lora_a,
+               const void* lora_b, int32_t r, float lora_scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace nf4_act_backward needs for a dbias (0 where it
+ * needs none, and for sizes out of range). */
+size_t nf4_act_backward_workspace(int64_t m, int64_t rows);
+
+/* The backward pass of nf4_linear's epilogue: for dy, the gradient of y,
+ *   dz[t][n] = dy[t][n] . act'(pre[t][n])          rounded once to bf16
+ *   dbias[n] = sum_t dy[t][n] . act'(pre[t][n])    float32, of the unrounded terms
+ * dz is what nf4_gemm_dx and nf4_lora_grads take as their dy; the gradient of
+ * the residual is dy itself.
+ *   dy   : bf16 [m][rows], 1 <= m <= 2^31, 1 <= rows < 2^31, m * rows < 2^40.
+ *   pre  : bf16 [m][rows]; may be NULL for NF4_ACT_NONE (not read).
+ *   dz   : bf16 [m][rows], or NULL to skip it; may be dy itself.
+ *   dbias: float32 [rows], or NULL to skip it; not both NULL.
+ *   workspace: at least nf4_act_backward_workspace(m, rows) bytes, 4-byte
+ *          aligned, where dbias is given (may be NULL when that is 0); overwritten.
+ * bf16 arrays 16-byte aligned.  Sums have a fixed order. */
+int nf4_act_backward(const void* dy, const void* pre, int64_t m, int64_t rows, int32_t act, void* dz, float* dbias,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace nf4_expert_balance needs (0 for sizes out of range). */
+size_t nf4_expert_balance_workspace(int64_t tokens, int32_t experts);
+
+/* The routers' balance loss: with p[t] = softmax(logits[t]) (zeros where all
+ * of a row's logits are -infinity) and T the number of tokens that mask keeps,
+ *   counts[e]     = number of slots of kept tokens with ids == e;  counts[experts] = T
+ *   mean_probs[e] = sum of p[t][e] over the kept tokens / T
+ *   loss          = coef . experts . sum_e counts[e] / (T . slots) . mean_probs[e]
+ * all 0 where T is 0.
+ *   logits    : [tokens][experts] of dtype (NF4_F32, NF4_BF16 or NF4_F16), aligned
+ *               to it; 1 <= experts <= NF4_MAX_EXPERTS.
+ *   ids       : int32 [tokens][slots], 1 <= tokens * slots < 2^31; a number outside
+ *               0 .. experts - 1 is not counted (a dropped slot).
+ *   mask      : uint8 [tokens], 0 for tokens to leave out (padding), or NULL.
+ *   loss      : out, one float32;  counts: out, experts + 1 int32;
+ *   mean_probs: out, experts float32.
+ *   workspace : at least nf4_expert_balance_workspace(tokens, experts) bytes,
+ *               8-byte aligned; its contents on entry do not matter.
+ * Logits of tokens left out may be anything.  Results do not depend on timing. */
+int nf4_expert_balance(const void* logits, int dtype, const int32_t* ids, const uint8_t* mask, int64_t tokens,
+                       int32_t experts, int32_t slots, float coef, float* loss, int32_t* counts, float* mean_probs,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradient of that loss for the logits (counts are constants of it):
+ *   dlogits[t][e] = dloss . coef . experts / (T^2 . slots) . p[t][e] . (counts[e] - sum_j counts[j] . p[t][j])
+ * and 0 for tokens left out.
+ *   counts : as nf4_expert_balance left them.
+ *   dloss  : one float32 on the device, or NULL for 1.
+ *   dlogits: out, [tokens][experts] of dtype; may be logits itself. */
+int nf4_expert_balance_backward(const void* logits, int dtype, const int32_t* counts, const uint8_t* mask, int64_t tokens,
+                                int32_t experts, int32_t slots, float coef, const float* dloss, void* dlogits,
+                                void* stream);
+
+/* One gradient of a training step (device pointers). */
+typedef struct nf4_grad {
+  const void* grad;   /* n values of dtype, aligned to it                                     */
+  void* out;          /* nf4_grad_clip: n values of out_dtype, aligned to it; may be grad itself
+                         (of the same dtype).  Not read by nf4_grad_norm                      */
+  int64_t n;          /* 0 <= n < 2^40                                                        */
+  int32_t dtype;      /* NF4_F32, NF4_BF16 or NF4_F16                                         */
+  int32_t out_dtype;
+} nf4_grad;
+
+/* Bytes of device workspace the calls below need for `count` gradients (0 for
+ * counts out of range). */
+size_t nf4_grad_workspace(int32_t count);
+
+/* norm = sqrt(sum of g^2 over all gradients), summed in float64 in a fixed order.
+ *   grads: [host] array of count structs, 0 <= count <= 2^20 (NULL for none).
+ *   norm : out, one float32.
+ *   workspace: at least nf4_grad_workspace(count) bytes, 8-byte aligned; its
+ *          contents on entry do not matter. */
+int nf4_grad_norm(const nf4_grad* grads, int32_t count, float* norm, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/* Clips gradients to a largest norm over all of them:
+ *   out = g . min(1, max_norm / (norm + 1e-6)), in float32, rounded once to out_dtype
+ * with norm that of nf4_grad_norm, or the float32 at total_norm (on the device)
+ * where that is not NULL: a norm over more than these gradients, as where they
+ * are sharded.  A norm that is NaN gives NaN, an infinite one zeros (and NaN for
+ * infinite gradients).
+ *   max_norm: finite, >= 0.
+ *   norm    : out, one float32, or NULL.  May be total_norm itself.
+ *   workspace: as nf4_grad_norm.
+ * An out overlaps no other out and no gradient but its own, exactly. */
+int nf4_grad_clip(const nf4_grad* grads, int32_t count, float max_norm, const float* total_norm, float* norm,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
