@@ -2,10 +2,20 @@
 //
 //   z = x . deq(W)^T + s (x . A^T) . B^T + bias;   y = act(z) + residual
 //
-// The K loop is the forward GEMM's (gemm_fwd.h; its schedule, operands and work
-// units are described in k_gemm.hip), the weight rounded once to bf16 after
-// scaling.  The adapters are extra K columns, as there; B is read from its own
-// rows, which only this kernel's last step or two need.
+// Operands are float16: a weight is the product of its level, rounded to
+// float16, and its block scale times a power of two of its row's own, rounded to
+// float16 -- one packed multiplication for two weights, whose three roundings (at
+// most 3 2^-11) are well below the one to bf16 of the dense GEMM (2^-8 at most),
+// whose expansion costs twice the instructions.  x becomes float16 exactly in a
+// small kernel before this one, scaled by a power of two per row.  Both powers
+// are taken back on the finished sums.  Blocks whose scale is 2^-24 of the
+// row's largest and below lose bits, and so do values of x 2^-29 of their row's
+// largest and below.
+//
+// The K loop's schedule, work units and stages are those of the forward GEMM
+// (k_gemm.hip).  The adapters are extra K columns in bf16 (s T in two parts), as
+// there; their operands come straight from memory, B from its own rows, and are
+// brought to the sums' powers of two.
 //
 // The epilogue: the matrix cores leave a lane with 4 consecutive columns of 32
 // rows, 8 bytes of bf16 each, which as they are would touch a line of memory per
@@ -14,15 +24,15 @@
 // takes them back as 8 columns of 8 rows, so that residual, pre and y move in
 // whole lines and the lane's bias stays in registers.  16-byte piece p of row r
 // sits at slot p ^ (r % 16): no two rows of a store meet in a bank.
-#include "gemm_fwd.h"
+#include "gemm_tiles.h"
 #include "linear_epilogue.h"
+#include "linear_f16.h"
 
 namespace nf4i {
 namespace {
 
 using gt::bf16x8;
 using gt::floatx16;
-using gt::kCopies;
 using gt::kThreads;
 
 constexpr int kBN = gt::kTileN, kBK = gt::kStep;
@@ -36,47 +46,97 @@ struct LinearArgs {
   const uint8_t* packed;
   int64_t rows, cols;
   Scales sc;
-  const uint16_t* x;
+  const uint16_t* x;   // the bf16 x as float16 [m][cols], row t scaled by 2^-xe[t]
+  const int32_t* xe;
   int64_t m;
   uint16_t* y;
   Epilogue ep;
-  const uint16_t* u;   // adapter columns of x: [m][kl] (s T hi | s T lo | 0), or null
+  const uint16_t* u;   // adapter columns of x: [m][kl] (s T hi | s T lo | 0)
   const uint16_t* lb;  // B [rows][r]
-  int r, r_pad, kl;
+  int r, r_pad, kl;    // 0 without adapters
   int64_t whole, units;  // as in the forward GEMM
   Codebook cb;
 };
 
-// Eight adapter columns c .. c + 7 of weight row n: (B | B | 0).
-__device__ __forceinline__ bf16x8 adapter_frag(const LinearArgs& a, int64_t n, int c) {
+// Eight adapter columns c .. c + 7 of weight row n: (B | B | 0), times `by`, a power of two.
+__device__ __forceinline__ bf16x8 adapter_w(const LinearArgs& a, int64_t n, int c, float by) {
+  typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
   const int j0 = c < a.r_pad ? c : c - a.r_pad;
-  const uint16_t* b = a.lb + n * a.r;
-  uint32_t w[4];
+  const uint16_t* b = a.lb + n * a.r + j0;
+  gt::u32x4 v = {0, 0, 0, 0};
+  if (j0 + 8 <= a.r) {
+    v = *reinterpret_cast<const u32x4_any*>(b);
+  } else {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t h[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = j0 + 2 * k + i;
-      h[i] = j < a.r ? b[j] : 0u;  // c past 2 r_pad: j >= r there too
-    }
-    w[k] = h[0] | (h[1] << 16);
+    for (int i = 0; i < 8; ++i)
+      if (j0 + i < a.r) v[i >> 1] |= static_cast<uint32_t>(b[i]) << (16 * (i & 1));
   }
-  const gt::u32x4 v = {w[0], w[1], w[2], w[3]};
-  return __builtin_bit_cast(bf16x8, v);
+  gt::u32x4 o;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o[k] = lin::bf16_pair(bf16_to_f32(v[k] & 0xFFFFu) * by, __uint_as_float(v[k] & 0xFFFF0000u) * by);
+  return __builtin_bit_cast(bf16x8, o);
+}
+
+// The adapters' share of the sums, brought to their powers of two.  Lane half h
+// takes columns c + 8 h .. + 7 of each 16.
+template <int MI>
+__device__ __forceinline__ void adapters(floatx16 (&acc)[MI][2], const LinearArgs& a, int64_t m0, const int64_t (&nrow)[2],
+                                         const int (&we)[2], int lane) {
+  if (a.r == 0) return;
+  int64_t tc[MI];
+  float by[MI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int64_t t = m0 + 32 * i + (lane & 31);
+    tc[i] = t < a.m ? t : a.m - 1;
+    by[i] = f16::power(-a.xe[tc[i]]);
+  }
+  for (int c = 0; c < 2 * a.r_pad; c += 16) {
+    const int ch = c + 8 * (lane >> 5);
+    gt::u32x4 v[MI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) v[i] = *reinterpret_cast<const gt::u32x4*>(a.u + tc[i] * a.kl + ch);
+    bf16x8 bl[2], uf[MI];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) bl[j] = adapter_w(a, nrow[j], ch, f16::power(-we[j]));
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      gt::u32x4 o;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        o[k] = lin::bf16_pair(bf16_to_f32(v[i][k] & 0xFFFFu) * by[i], __uint_as_float(v[i][k] & 0xFFFF0000u) * by[i]);
+      uf[i] = __builtin_bit_cast(bf16x8, o);
+    }
+    gt::mfma16(uf, bl, acc);
+  }
 }
 
 template <int MI>
-__device__ __forceinline__ void epilogue(const floatx16 (&acc)[MI][2], const LinearArgs& a, int64_t m0, int64_t n0, char* turn,
-                                         int wave, int lane) {
+__device__ __forceinline__ void epilogue(const floatx16 (&acc)[MI][2], const LinearArgs& a, int64_t m0, int64_t n0,
+                                         const int (&we)[2], char* turn, int wave, int lane) {
   const int64_t col = n0 + wave * 64 + 8 * (lane & 7);
   const bool vec = (a.rows & 7) == 0;  // every row of the outputs 16-byte aligned
   const int left = static_cast<int>(a.rows - col < 8 ? a.rows - col : 8);
   float bias[8];
+  lin::load_bias(bias, a.ep, col, left);
+  // exponents of the weight rows that a lane's sums belong to: 4 consecutive ones per group
 #pragma unroll
-  for (int c = 0; c < 8; ++c) bias[c] = c < left ? lin::bias_at(a.ep, col + c) : 0.0f;
+  for (int j = 0; j < 2; ++j) reinterpret_cast<int*>(turn)[32 * j + (lane & 31)] = we[j];
+  f16::wave_lds_order();
+  int4 wex[2][4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) wex[j][g] = *reinterpret_cast<const int4*>(turn + 4 * (32 * j + 8 * g + 4 * (lane >> 5)));
+  f16::wave_lds_order();
 #pragma unroll
   for (int rd = 0; rd < MI / 2; ++rd) {
+    int xe[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t t = m0 + 64 * rd + 32 * i + (lane & 31);
+      xe[i] = a.xe[t < a.m ? t : a.m - 1];
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -84,37 +144,169 @@ __device__ __forceinline__ void epilogue(const floatx16 (&acc)[MI][2], const Lin
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int row = 32 * i + (lane & 31), p = 8 * j + 2 * g + (lane >> 5);
-          const floatx16& t = acc[2 * rd + i][j];
+          const floatx16& s = acc[2 * rd + i][j];
+          // the powers of two taken back
           *reinterpret_cast<float4*>(turn + row * 256 + ((p ^ (row & 15)) << 4)) =
-              make_float4(t[4 * g], t[4 * g + 1], t[4 * g + 2], t[4 * g + 3]);
+              make_float4(__builtin_amdgcn_ldexpf(s[4 * g], xe[i] + wex[j][g].x), __builtin_amdgcn_ldexpf(s[4 * g + 1], xe[i] + wex[j][g].y),
+                          __builtin_amdgcn_ldexpf(s[4 * g + 2], xe[i] + wex[j][g].z), __builtin_amdgcn_ldexpf(s[4 * g + 3], xe[i] + wex[j][g].w));
         }
-    // the wave's own LDS accesses are served in order; this keeps the compiler to it
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    lin::with_act(a.ep.act, [&](auto act) {
-#pragma unroll 2
-      for (int it = 0; it < 8; ++it) {
-        const int row = 8 * it + (lane >> 3), p = 2 * (lane & 7);
-        const int64_t t = m0 + 64 * rd + row;
-        const float4 lo = *reinterpret_cast<const float4*>(turn + row * 256 + ((p ^ (row & 15)) << 4));
-        const float4 hi = *reinterpret_cast<const float4*>(turn + row * 256 + (((p + 1) ^ (row & 15)) << 4));
-        if (t >= a.m || left <= 0) continue;
-        const float z[8] = {lo.x + bias[0], lo.y + bias[1], lo.z + bias[2], lo.w + bias[3],
-                            hi.x + bias[4], hi.y + bias[5], hi.z + bias[6], hi.w + bias[7]};
-        const int64_t at = t * a.rows + col;
-        if (vec) {
-          lin::finish8<decltype(act)::value>(a.ep, a.y, at, z);
-        } else {
+    f16::wave_lds_order();
+#pragma unroll 1
+    for (int it = 0; it < 8; ++it) {
+      const int row = 8 * it + (lane >> 3), p = 2 * (lane & 7);
+      const int64_t t = m0 + 64 * rd + row;
+      const float4 lo = *reinterpret_cast<const float4*>(turn + row * 256 + ((p ^ (row & 15)) << 4));
+      const float4 hi = *reinterpret_cast<const float4*>(turn + row * 256 + (((p + 1) ^ (row & 15)) << 4));
+      if (t >= a.m || left <= 0) continue;
+      float v[8] = {lo.x + bias[0], lo.y + bias[1], lo.z + bias[2], lo.w + bias[3],
+                    hi.x + bias[4], hi.y + bias[5], hi.z + bias[6], hi.w + bias[7]};
+      lin::finish8(a.ep, a.y, t * a.rows + col, v, left, vec && left == 8);
+    }
+    f16::wave_lds_order();
+  }
+}
+
+// The codes a lane expands in one K step: for its two weight rows (j = 0, 1) the
+// 16 bytes of columns 32 h .. 32 h + 31, and the rows' block scale inputs.
+struct WRegs {
+  gt::u32x4 w[2];
+  float am[2];
+  int q[2];
+  float s2[2];
+};
+
+struct WPtrs {
+  const uint8_t* c[2];
+  int64_t blk[2];
+};
+
+template <bool kDQ>
+__device__ __forceinline__ void load_w(WRegs& r, const WPtrs& p, const Scales& sc, int64_t ks) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            if (c < left) lin::finish1<decltype(act)::value>(a.ep, a.y, at + c, z[c]);
-        }
-      }
-    });
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  for (int j = 0; j < 2; ++j) {
+    r.w[j] = *reinterpret_cast<const gt::u32x4*>(p.c[j] + ks * (kBK / 2));
+    const int64_t blk = p.blk[j] + ks;
+    if constexpr (kDQ) {
+      r.q[j] = sc.q[blk];
+      r.s2[j] = sc.absmax2[blk >> 8];
+    } else {
+      r.am[j] = sc.absmax[blk];
+    }
+  }
+}
+
+// The float16 scales of the lane's two blocks, twice each.
+template <bool kDQ, bool kF8>
+__device__ __forceinline__ void block_scales(const WRegs& r, float mean, const float (&up)[2], f16::half2 (&sa)[2]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float s;
+    if constexpr (kDQ) s = (code_ratio(r.q[j], kF8 ? 1 : 0) * r.s2[j]) + mean;  // a_hat, three roundings
+    else s = r.am[j];
+    sa[j] = f16::twice(s * up[j]);
+  }
+}
+
+// Level pairs of code bytes 4 s .. 4 s + 3 of the lane's 16 bytes of both rows.
+struct Lookups {
+  uint32_t l[2][4];
+};
+__device__ __forceinline__ void lookup_step(Lookups& lk, const gt::u32x4 (&w)[2], int s, const char* tab, uint32_t slot) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) lk.l[j][b] = f16::look_up(w[j][s], b, tab, slot);
+}
+
+template <int MI>
+__device__ __forceinline__ void mfma16(const f16::halfx8 (&af)[MI], const f16::halfx8 (&bf)[2], floatx16 (&acc)[MI][2]) {
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bf[0], af[i], acc[i][0], 0, 0, 0);
+    acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bf[1], af[i], acc[i][1], 0, 0, 0);
+  }
+}
+
+template <int MI>
+__device__ __forceinline__ void read_act(const char* xa, int s, uint32_t sw, uint32_t h4, f16::halfx8 (&f)[MI]) {
+  const char* p = xa + (((h4 + s) ^ sw) << 4);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) f[i] = *reinterpret_cast<const f16::halfx8*>(p + i * 32 * gt::kActRowBytes);
+}
+
+// Per MFMA of a 16-wide k step: V VALU operations and L LDS reads of the next.
+template <int N, int V, int L>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
+    __builtin_amdgcn_sched_group_barrier(0x080, L, 0);
+  }
+}
+
+// acc += x16 . w16^T over nk steps, two LDS stages, software-pipelined as in the
+// forward GEMM: while the products of 16-wide step s run, the weights of s + 1
+// are multiplied out and those of s + 2 looked up.
+template <int MI, bool kDQ, bool kF8>
+__device__ __forceinline__ void steps(const LinearArgs& a, const gt::ActPtrs<MI>& xp, const WPtrs& wp, const float (&up)[2], char* xs0,
+                                      char* xs1, const char* tabc, uint32_t slot, float mean, int wave, int lane,
+                                      floatx16 (&acc)[MI][2]) {
+  constexpr int kV = 16 / MI > 1 ? 16 / MI : 1, kL = 8 / MI;
+  const int64_t nk = a.cols / kBK;
+  WRegs wc, wnx;
+  gt::dma_act(xp, 0, xs0, wave);
+  load_w<kDQ>(wc, wp, a.sc, 0);
+  f16::half2 sa[2];
+  f16::halfx8 bf[2][2];
+  Lookups lk[3];
+  f16::halfx8 af[3][MI];
+  const uint32_t sw = ((lane & 31) >> 1) & 7, h4 = (lane >> 5) * 4;
+  block_scales<kDQ, kF8>(wc, mean, up, sa);
+  lookup_step(lk[0], wc.w, 0, tabc, slot);
+  bf[0][0] = f16::expand(lk[0].l[0], sa[0]);
+  bf[0][1] = f16::expand(lk[0].l[1], sa[1]);
+  gt::wait_vmem();
+  __syncthreads();
+  for (int64_t ks = 0; ks < nk; ++ks) {
+    const int64_t kn = ks + 1 < nk ? ks + 1 : ks;
+    gt::dma_act(xp, kn, (ks & 1) ? xs0 : xs1, wave);  // the other stage was last read before the previous barrier
+    load_w<kDQ>(wnx, wp, a.sc, kn);
+    __builtin_amdgcn_sched_barrier(0);
+    const char* xa = ((ks & 1) ? xs1 : xs0) + (lane & 31) * gt::kActRowBytes;
+    read_act(xa, 0, sw, h4, af[0]);
+    read_act(xa, 1, sw, h4, af[1]);
+    lookup_step(lk[1], wc.w, 1, tabc, slot);
+    __builtin_amdgcn_sched_barrier(0);
+    mfma16(af[0], bf[0], acc);
+    bf[1][0] = f16::expand(lk[1].l[0], sa[0]);
+    bf[1][1] = f16::expand(lk[1].l[1], sa[1]);
+    read_act(xa, 2, sw, h4, af[2]);
+    lookup_step(lk[2], wc.w, 2, tabc, slot);
+    interleave<2 * MI, kV, kL>();
+    __builtin_amdgcn_sched_barrier(0);
+    mfma16(af[1], bf[1], acc);
+    bf[0][0] = f16::expand(lk[2].l[0], sa[0]);
+    bf[0][1] = f16::expand(lk[2].l[1], sa[1]);
+    read_act(xa, 3, sw, h4, af[0]);
+    lookup_step(lk[0], wc.w, 3, tabc, slot);
+    interleave<2 * MI, kV, kL>();
+    __builtin_amdgcn_sched_barrier(0);
+    mfma16(af[2], bf[0], acc);
+    bf[1][0] = f16::expand(lk[0].l[0], sa[0]);
+    bf[1][1] = f16::expand(lk[0].l[1], sa[1]);
+    interleave<2 * MI, kV, kL>();
+    __builtin_amdgcn_sched_barrier(0);
+    mfma16(af[0], bf[1], acc);
+    block_scales<kDQ, kF8>(wnx, mean, up, sa);
+    lookup_step(lk[1], wnx.w, 0, tabc, slot);
+    bf[0][0] = f16::expand(lk[1].l[0], sa[0]);
+    bf[0][1] = f16::expand(lk[1].l[1], sa[1]);
+    interleave<2 * MI, kV, kL>();
+    __builtin_amdgcn_sched_barrier(0);
+    gt::wait_vmem();
+    __syncthreads();
+    wc = wnx;
   }
 }
 
@@ -123,57 +315,41 @@ template <int MI, bool kDQ, bool kF8>
 __device__ __forceinline__ void linear_unit(const LinearArgs& a, int64_t m0, int64_t n0, char* xs, const char* tabc,
                                             uint32_t slot, float mean, int wave, int lane) {
   char *xs0 = xs, *xs1 = xs + kStageBytes;
+  char* turn = xs + wave * (2 * kStageBytes / 4);  // the wave's own quarter, once the steps are through
   const gt::ActPtrs<MI> xp = gt::make_act_ptrs<MI, 32 * MI>(a.x, a.cols, a.m, m0, wave, lane);
-  gt::WPtrs wp;
+  WPtrs wp;
   int64_t nrow[2];
+  int we[2];
+  float up[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int64_t n = n0 + wave * 64 + j * 32 + (lane & 31);
     nrow[j] = n < a.rows ? n : a.rows - 1;  // rows past the end: never stored
     wp.c[j] = a.packed + nrow[j] * (a.cols / 2) + (lane >> 5) * 16;
     wp.blk[j] = nrow[j] * (a.cols / 64);
+    we[j] = f16::row_exponent<kDQ>(a.sc, wp.blk[j], a.cols / 64, mean, lane);
+    up[j] = f16::power(-we[j]);
   }
   floatx16 acc[MI][2];
   gt::zero_acc(acc);
-  gt::fwd_steps<MI, kDQ, kF8>(
-      a.sc, a.cols / kBK, [&](int64_t ks, char* stage) { gt::dma_act(xp, ks, stage, wave); }, wp, xs0, xs1, tabc, slot, mean,
-      lane, acc);
-  if (a.kl > 0) {
-    const gt::ActPtrs<MI> up = gt::make_act_ptrs<MI, 32 * MI>(a.u, a.kl, a.m, m0, wave, lane);
-    const uint32_t sw = ((lane & 31) >> 1) & 7, h4 = (lane >> 5) * 4;
-    for (int k0 = 0; k0 < a.kl; k0 += kBK) {
-      gt::dma_act(up, k0 / kBK, xs0, wave);  // xs0 was last read before the previous barrier
-      bf16x8 bl[4][2];
-#pragma unroll
-      for (int s4 = 0; s4 < 4; ++s4)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) bl[s4][j] = adapter_frag(a, nrow[j], k0 + 8 * static_cast<int>(h4) + 8 * s4);
-      gt::wait_vmem();
-      __syncthreads();
-      const char* xa = xs0 + (lane & 31) * gt::kActRowBytes;
-#pragma unroll
-      for (int s4 = 0; s4 < 4; ++s4) {
-        bf16x8 af[MI];
-        gt::read_act(xa, s4, sw, h4, af);
-        gt::mfma16(af, bl[s4], acc);
-      }
-      __syncthreads();
-    }
-  }
-  epilogue<MI>(acc, a, m0, n0, xs + wave * (2 * kStageBytes / 4), wave, lane);
+  steps<MI, kDQ, kF8>(a, xp, wp, up, xs0, xs1, tabc, slot, mean, wave, lane, acc);
+  adapters<MI>(acc, a, m0, nrow, we, lane);
+  epilogue<MI>(acc, a, m0, n0, we, turn, wave, lane);
   __syncthreads();  // the next unit's first stage may lie in another wave's quarter
 }
 
 template <bool kDQ, bool kF8>
 __global__ __launch_bounds__(kThreads, 1) void k_linear(LinearArgs a) {
-  __shared__ __align__(16) char xs[2 * kStageBytes];
-  __shared__ __align__(16) float2 tab[256 * kCopies];
-  const char* tabc = reinterpret_cast<const char*>(tab);
+  // the table at LDS address 0: a lookup's address is then its one permute
+  __shared__ __align__(16) char lds[4 * f16::kTabWords + 2 * kStageBytes];
+  uint32_t* tab = reinterpret_cast<uint32_t*>(lds);
+  char* xs = lds + 4 * f16::kTabWords;
+  const char* tabc = lds;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  static_assert(kCopies == 32, "a copy's slot");
-  const uint32_t slot = static_cast<uint32_t>(lane & (kCopies - 1)) << 3;
-  gt::fill_level_pairs<kCopies>(tab, a.cb);  // ends with a barrier
+  const uint32_t slot = f16::table_slot(lane);
+  f16::fill_table<kThreads>(tab, a.cb);
+  __syncthreads();
   const float mean = kDQ ? *a.sc.mean : 0.0f;
   const int64_t tiles_n = (a.rows + kBN - 1) / kBN;
   const int64_t tiles = tiles_n * ((a.m + kBM - 1) / kBM);
@@ -193,27 +369,44 @@ __global__ __launch_bounds__(kThreads, 1) void k_linear(LinearArgs a) {
   }
 }
 
+// x in float16, its rows' exponents, the adapter columns: each at a multiple of 256 bytes.
+struct Workspace {
+  size_t xe, u, bytes;
+};
+Workspace workspace_of(int64_t m, int64_t cols, int r) {
+  const auto round = [](size_t n) { return (n + 255) & ~size_t(255); };
+  Workspace w{};
+  w.xe = round(static_cast<size_t>(m) * static_cast<size_t>(cols) * sizeof(uint16_t));
+  w.u = w.xe + round(static_cast<size_t>(m) * sizeof(int32_t));
+  w.bytes = w.u + (r > 0 ? round(static_cast<size_t>(m) * gemm_lora_cols(r) * sizeof(uint16_t)) : 0);
+  return w;
+}
+
 }  // namespace
 
 size_t linear_workspace(int64_t m, int64_t rows, int64_t cols, int r) {
   (void)rows;
-  (void)cols;
-  return r > 0 ? static_cast<size_t>(m) * gemm_lora_cols(r) * sizeof(uint16_t) : 0;
+  return workspace_of(m, cols, r).bytes;
 }
 
 hipError_t launch_linear(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x, int64_t m,
                          uint16_t* y, const Epilogue& ep, const uint16_t* lora_a, const uint16_t* lora_b, int r,
                          float lora_scale, void* ws, hipStream_t s) {
   LinearArgs a{};
-  a.packed = packed; a.rows = rows; a.cols = cols; a.sc = sc; a.x = x; a.m = m; a.y = y; a.ep = ep;
+  const Workspace at = workspace_of(m, cols, r);
+  char* const w8 = static_cast<char*>(ws);
+  a.packed = packed; a.rows = rows; a.cols = cols; a.sc = sc; a.m = m; a.y = y; a.ep = ep;
+  a.x = reinterpret_cast<const uint16_t*>(w8);
+  a.xe = reinterpret_cast<const int32_t*>(w8 + at.xe);
+  if (hipError_t e = launch_x16(x, m, cols, reinterpret_cast<uint16_t*>(w8), reinterpret_cast<int32_t*>(w8 + at.xe), s)) return e;
   a.cb = codebook(sc.fp4);
   if (r > 0) {
-    a.u = static_cast<const uint16_t*>(ws);
+    a.u = reinterpret_cast<const uint16_t*>(w8 + at.u);
     a.lb = lora_b;
     a.r = r;
     a.r_pad = (r + 15) / 16 * 16;
     a.kl = static_cast<int>(gemm_lora_cols(r));
-    if (hipError_t e = launch_lora_u(x, lora_a, m, cols, r, lora_scale, static_cast<uint16_t*>(ws), s)) return e;
+    if (hipError_t e = launch_lora_u(x, lora_a, m, cols, r, lora_scale, reinterpret_cast<uint16_t*>(w8 + at.u), s)) return e;
   }
   const int64_t tiles = ((rows + kBN - 1) / kBN) * ((m + kBM - 1) / kBM);
   const int64_t slots = device_cus();

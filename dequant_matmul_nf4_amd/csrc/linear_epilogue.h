@@ -3,8 +3,6 @@
 // z reaches the activation in float32; y and pre are rounded once each.
 #pragma once
 
-#include <type_traits>
-
 #include "epilogue.h"
 #include "layer_ops.h"
 
@@ -19,47 +17,88 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, p);
 }
 
-__device__ __forceinline__ float bias_at(const Epilogue& ep, int64_t col) {
-  if (!ep.bias) return 0.0f;
-  return ep.bias_f32 ? static_cast<const float*>(ep.bias)[col] : bf16_to_f32(static_cast<const uint16_t*>(ep.bias)[col]);
+// N bias values of columns col .., `left` of which exist (zeros past them and without a bias).
+template <int N>
+__device__ __forceinline__ void load_bias(float (&b)[N], const Epilogue& ep, int64_t col, int left) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) b[c] = 0.0f;
+  if (!ep.bias) return;
+  if (ep.bias_f32) {
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      if (c < left) b[c] = static_cast<const float*>(ep.bias)[col + c];
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      if (c < left) b[c] = bf16_to_f32(static_cast<const uint16_t*>(ep.bias)[col + c]);
+  }
 }
 
-// f(integral constant of the activation): one branch around code made for each.
-template <class F>
-__device__ __forceinline__ void with_act(int act, const F& f) {
+// act(z) of N values: one branch around code made for each activation.
+template <int N>
+__device__ __forceinline__ void apply_act(int act, float (&z)[N]) {
   switch (act) {
-    case kActNone: f(std::integral_constant<int, kActNone>{}); break;
-    case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
-    case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
-    case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
-    default: f(std::integral_constant<int, kActGeluTanh>{});
+    case kActNone: break;
+    case kActRelu:
+#pragma unroll
+      for (int c = 0; c < N; ++c) z[c] = act_value<kActRelu>(z[c]);
+      break;
+    case kActSilu:
+#pragma unroll
+      for (int c = 0; c < N; ++c) z[c] = act_value<kActSilu>(z[c]);
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int c = 0; c < N; ++c) z[c] = act_value<kActGelu>(z[c]);
+      break;
+    default:
+#pragma unroll
+      for (int c = 0; c < N; ++c) z[c] = act_value<kActGeluTanh>(z[c]);
   }
 }
 
 // One value at `at` of the outputs.
-template <int A>
 __device__ __forceinline__ void finish1(const Epilogue& ep, uint16_t* y, int64_t at, float z) {
   if (ep.pre) ep.pre[at] = static_cast<uint16_t>(bf16_pair(z, 0.0f));
-  float v = act_value<A>(z);
-  if (ep.residual) v += bf16_to_f32(ep.residual[at]);
-  y[at] = static_cast<uint16_t>(bf16_pair(v, 0.0f));
+  float v[1] = {z};
+  apply_act(ep.act, v);
+  if (ep.residual) v[0] += bf16_to_f32(ep.residual[at]);
+  y[at] = static_cast<uint16_t>(bf16_pair(v[0], 0.0f));
 }
 
-// Eight consecutive values of a row, `at` a multiple of 8 and the buffers 16-byte aligned.
-template <int A>
-__device__ __forceinline__ void finish8(const Epilogue& ep, uint16_t* y, int64_t at, const float (&z)[8]) {
+// Eight consecutive values of a row, the first `left` of which exist; `whole`:
+// all do, and 16-byte accesses are aligned.
+__device__ __forceinline__ void finish8(const Epilogue& ep, uint16_t* y, int64_t at, float (&z)[8], int left, bool whole) {
   u32x4 res{};
-  if (ep.residual) res = *reinterpret_cast<const u32x4*>(ep.residual + at);
-  if (ep.pre) {
-    const u32x4 p = {bf16_pair(z[0], z[1]), bf16_pair(z[2], z[3]), bf16_pair(z[4], z[5]), bf16_pair(z[6], z[7])};
-    *reinterpret_cast<u32x4*>(ep.pre + at) = p;
-  }
-  u32x4 o;
+  if (ep.residual) {
+    if (whole) {
+      res = *reinterpret_cast<const u32x4*>(ep.residual + at);
+    } else {
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-    o[c] = bf16_pair(act_value<A>(z[2 * c]) + bf16_to_f32(res[c] & 0xFFFFu),
-                     act_value<A>(z[2 * c + 1]) + __uint_as_float(res[c] & 0xFFFF0000u));
-  *reinterpret_cast<u32x4*>(y + at) = o;
+      for (int c = 0; c < 8; ++c)
+        if (c < left) res[c >> 1] |= static_cast<uint32_t>(ep.residual[at + c]) << (16 * (c & 1));
+    }
+  }
+  const auto put = [&](uint16_t* to) {
+    const u32x4 o = {bf16_pair(z[0], z[1]), bf16_pair(z[2], z[3]), bf16_pair(z[4], z[5]), bf16_pair(z[6], z[7])};
+    if (whole) {
+      *reinterpret_cast<u32x4*>(to + at) = o;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < left) to[at + c] = static_cast<uint16_t>(o[c >> 1] >> (16 * (c & 1)));
+    }
+  };
+  if (ep.pre) put(ep.pre);
+  apply_act(ep.act, z);
+  if (ep.residual) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      z[2 * c] += bf16_to_f32(res[c] & 0xFFFFu);
+      z[2 * c + 1] += __uint_as_float(res[c] & 0xFFFF0000u);
+    }
+  }
+  put(y);
 }
 
 }  // namespace lin

@@ -1,0 +1,103 @@
+// The float16 operands of the linear kernels: weights as level times scale, the
+// power of two of a weight row, the table of level pairs, and the kernel that
+// brings x to float16 (k_linear_x16.hip).
+#pragma once
+
+#include "nf4_device.h"
+
+namespace nf4i {
+namespace f16 {
+
+typedef _Float16 half2 __attribute__((ext_vector_type(2)));
+typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Scaled values lie below 2^(kTop + 1): room for the largest of a row in float16.
+constexpr int kTop = 14;
+// 256 level pairs (element 2j = high nibble in the low half), one copy per lane:
+// entry e of lane l at byte 256 e + 4 l, so no two lanes meet in a bank and, with the
+// table at LDS address 0, one permute is a lookup's address.
+constexpr int kCopies = 64;
+constexpr int kTabWords = 256 * kCopies;
+
+__device__ __forceinline__ void wave_lds_order() {
+  // a wave's LDS accesses are served in order; this keeps the compiler to it
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float power(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// The exponent e such that v 2^-e lies in [2^kTop, 2^(kTop + 1)), at least kLow
+// (smaller v lie lower), so that adapters, which are brought to the same power,
+// keep room beside rows of zeros.
+constexpr int kLow = -60;
+__device__ __forceinline__ int exponent_of(float v) {
+  const int e = static_cast<int>((__float_as_uint(v) >> 23) & 0xFF) - 127 - kTop;
+  return e < kLow ? kLow : e;
+}
+
+__device__ __forceinline__ half2 twice(float s) {
+  const _Float16 h = static_cast<_Float16>(s);
+  return half2{h, h};
+}
+
+template <int kThreads>
+__device__ __forceinline__ void fill_table(uint32_t* tab, const Codebook& cb) {
+  // a pass of the threads writes kThreads / kCopies entries
+  constexpr int kPer = kThreads / kCopies;
+  static_assert(kPer <= 16 && 16 % kPer == 0, "whole passes per first level");
+  const int e0 = threadIdx.x / kCopies;
+  float second[16 / kPer];
+#pragma unroll
+  for (int i = 0; i < 16 / kPer; ++i) second[i] = cb.level[i * kPer + e0];
+#pragma unroll
+  for (int p = 0; p < 256 / kPer; ++p) {
+    const half2 h = {static_cast<_Float16>(cb.level[p * kPer / 16]), static_cast<_Float16>(second[p % (16 / kPer)])};
+    tab[p * kThreads + threadIdx.x] = __builtin_bit_cast(uint32_t, h);
+  }
+}
+
+// The level pair of byte b of a word of codes: a permute puts it above the lane's slot.
+__device__ __forceinline__ uint32_t table_slot(int lane) { return static_cast<uint32_t>(lane) << 2; }
+__device__ __forceinline__ uint32_t look_up(uint32_t word, int b, const char* tab, uint32_t slot) {
+  return *reinterpret_cast<const uint32_t*>(tab + __builtin_amdgcn_perm(word, slot, 0x0C0C0000u | ((4u + b) << 8)));
+}
+
+// A level pair times the block's scale.
+__device__ __forceinline__ uint32_t times(uint32_t pair, half2 s) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2, pair) * s);
+}
+
+// Four level pairs times the block's scale: an operand of eight weights.
+__device__ __forceinline__ halfx8 expand(const uint32_t (&l)[4], half2 s) {
+  u32x4 v;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) v[b] = times(l[b], s);
+  return __builtin_bit_cast(halfx8, v);
+}
+
+// The exponent of a weight row of nblk blocks from block blk0 on: that of its
+// largest block scale, or with double quantization of a bound on it, the
+// largest group scale plus the mean.  Lanes l and l + 32 hold the same row.
+template <bool kDQ>
+__device__ __forceinline__ int row_exponent(const Scales& sc, int64_t blk0, int64_t nblk, float mean, int lane) {
+  float top = 0.0f;
+  if constexpr (kDQ) {
+    for (int64_t g = blk0 >> 8; g <= (blk0 + nblk - 1) >> 8; ++g) top = fmaxf(top, fabsf(sc.absmax2[g]));
+    top += fabsf(mean);
+  } else {
+    for (int64_t b = lane >> 5; b < nblk; b += 2) top = fmaxf(top, fabsf(sc.absmax[blk0 + b]));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+  }
+  return exponent_of(top);
+}
+
+}  // namespace f16
+
+// x16[t] = x[t] 2^-xe[t] in float16 for the m rows of x [m][cols] (cols % 64 == 0).
+hipError_t launch_x16(const uint16_t* x, int64_t m, int64_t cols, uint16_t* x16, int32_t* xe, hipStream_t s);
+
+}  // namespace nf4i

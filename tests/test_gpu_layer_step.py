@@ -96,17 +96,21 @@ class Block:
 def test_step_against_autograd(act, m):
     """Relative Frobenius errors: each bf16 rounding on the way (h, z, dh, dz, the weights of
     each product) adds at most 2^-8 / sqrt(3) = 2.3e-3 in the mean square; six of them, 6e-3.
-    relu's slope flips where z rounds across zero: a share of 2^-8 of the values there, none in size."""
+    relu's slope flips where z's error d crosses zero: with z normal of deviation 1 a share of
+    0.4 E|d| of the values, E|d| at most sqrt(2) 2.3e-3 sqrt(2 / pi) = 2.6e-3 (the weights' and x's
+    roundings on both sides), so 1e-3 of them; each is wrong by its whole gradient, and half of all
+    have one: sqrt(2 1e-3) = 4.6e-2 of what passes the activation."""
     torch = need_gpu()
     say("layer step", act, m)
     block = Block(torch, act=act)
     x, dy = torch.randn((m, 256), device="cuda").bfloat16(), torch.randn((m, 256), device="cuda").bfloat16()
     y, loss, dx, grads, out, norm = block.step(x, dy, 1.0)
     ry, rl, rdx, rgrads = block.reference(x, dy)
-    assert rel(y, ry.detach()) < 1e-2 and rel(dx, rdx) < 1e-2
+    past = 5e-2 if act == "relu" else 1e-2  # what passes the activation's slope
+    assert rel(y, ry.detach()) < 1e-2 and rel(dx, rdx) < past
     assert abs(float(loss) - float(rl.detach())) < 1e-5 * float(rl.detach())
     for i, (g, r) in enumerate(zip(grads, rgrads)):
-        assert rel(g.reshape(r.shape), r) < (1e-2 if i < 6 else 1e-4), i
+        assert rel(g.reshape(r.shape), r) < (past if i < 3 else 1e-2 if i < 6 else 1e-4), i
     n = math.sqrt(sum(float(g.double().square().sum()) for g in grads))
     assert abs(float(norm) - n) < 1e-6 * n
     flat = torch.cat([g.reshape(-1) for g in grads]).double()
