@@ -37,6 +37,7 @@ using gt::kThreads;
 
 constexpr int kBN = gt::kTileN, kBK = gt::kStep;
 constexpr int kMI = 8;
+constexpr int64_t kMidRows = 512;  // up to so many rows of x: k_linear_mid.hip
 constexpr int kBM = 32 * kMI;
 constexpr int kStageBytes = gt::act_stage_bytes<kBM>();
 constexpr int kTurnRows = 64;
@@ -46,7 +47,7 @@ struct LinearArgs {
   const uint8_t* packed;
   int64_t rows, cols;
   Scales sc;
-  const uint16_t* x;   // the bf16 x as float16 [m][cols], row t scaled by 2^-xe[t]
+  const uint16_t* x;   // x in float16 blocks (launch_x16), row t scaled by 2^-xe[t]
   const int32_t* xe;
   int64_t m;
   uint16_t* y;
@@ -57,25 +58,6 @@ struct LinearArgs {
   int64_t whole, units;  // as in the forward GEMM
   Codebook cb;
 };
-
-// Eight adapter columns c .. c + 7 of weight row n: (B | B | 0), times `by`, a power of two.
-__device__ __forceinline__ bf16x8 adapter_w(const LinearArgs& a, int64_t n, int c, float by) {
-  typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-  const int j0 = c < a.r_pad ? c : c - a.r_pad;
-  const uint16_t* b = a.lb + n * a.r + j0;
-  gt::u32x4 v = {0, 0, 0, 0};
-  if (j0 + 8 <= a.r) {
-    v = *reinterpret_cast<const u32x4_any*>(b);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (j0 + i < a.r) v[i >> 1] |= static_cast<uint32_t>(b[i]) << (16 * (i & 1));
-  }
-  gt::u32x4 o;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) o[k] = lin::bf16_pair(bf16_to_f32(v[k] & 0xFFFFu) * by, __uint_as_float(v[k] & 0xFFFF0000u) * by);
-  return __builtin_bit_cast(bf16x8, o);
-}
 
 // The adapters' share of the sums, brought to their powers of two.  Lane half h
 // takes columns c + 8 h .. + 7 of each 16.
@@ -98,15 +80,9 @@ __device__ __forceinline__ void adapters(floatx16 (&acc)[MI][2], const LinearArg
     for (int i = 0; i < MI; ++i) v[i] = *reinterpret_cast<const gt::u32x4*>(a.u + tc[i] * a.kl + ch);
     bf16x8 bl[2], uf[MI];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) bl[j] = adapter_w(a, nrow[j], ch, f16::power(-we[j]));
+    for (int j = 0; j < 2; ++j) bl[j] = lin::adapter_w(a.lb, a.r, a.r_pad, nrow[j], ch, f16::power(-we[j]));
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      gt::u32x4 o;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        o[k] = lin::bf16_pair(bf16_to_f32(v[i][k] & 0xFFFFu) * by[i], __uint_as_float(v[i][k] & 0xFFFF0000u) * by[i]);
-      uf[i] = __builtin_bit_cast(bf16x8, o);
-    }
+    for (int i = 0; i < MI; ++i) uf[i] = lin::times(v[i], by[i]);
     gt::mfma16(uf, bl, acc);
   }
 }
@@ -227,11 +203,29 @@ __device__ __forceinline__ void mfma16(const f16::halfx8 (&af)[MI], const f16::h
   }
 }
 
+// Stage layout: as x16's, 4 KB for each 32 rows, of 4 blocks of 1 KB.
 template <int MI>
-__device__ __forceinline__ void read_act(const char* xa, int s, uint32_t sw, uint32_t h4, f16::halfx8 (&f)[MI]) {
-  const char* p = xa + (((h4 + s) ^ sw) << 4);
+__device__ __forceinline__ void read_act(const char* xa, int s, f16::halfx8 (&f)[MI]) {
 #pragma unroll
-  for (int i = 0; i < MI; ++i) f[i] = *reinterpret_cast<const f16::halfx8*>(p + i * 32 * gt::kActRowBytes);
+  for (int i = 0; i < MI; ++i) f[i] = *reinterpret_cast<const f16::halfx8*>(xa + (4 * i + s) * 1024);
+}
+
+// The tile's x of one step: wave w moves 32-row blocks w MI / 4 .. (MI of 1 KB each
+// instruction); rows past the last 32 of x16 repeat them (never stored).
+template <int MI>
+struct XTile {
+  const char* base;
+  int64_t band;    // bytes of a 32-row band
+  int64_t first, last;
+};
+template <int MI>
+__device__ __forceinline__ void dma_x(const XTile<MI>& x, int64_t ks, char* stage, int wave, int lane) {
+#pragma unroll
+  for (int q = 0; q < MI; ++q) {
+    const int b = MI * wave + q;  // block of the stage
+    const int64_t band = x.first + b / 4 < x.last ? x.first + b / 4 : x.last;
+    gt::dma16(reinterpret_cast<const uint8_t*>(x.base + band * x.band + ks * 4096 + (b & 3) * 1024 + lane * 16), stage + b * 1024);
+  }
 }
 
 // Per MFMA of a 16-wide k step: V VALU operations and L LDS reads of the next.
@@ -249,19 +243,18 @@ __device__ __forceinline__ void interleave() {
 // forward GEMM: while the products of 16-wide step s run, the weights of s + 1
 // are multiplied out and those of s + 2 looked up.
 template <int MI, bool kDQ, bool kF8>
-__device__ __forceinline__ void steps(const LinearArgs& a, const gt::ActPtrs<MI>& xp, const WPtrs& wp, const float (&up)[2], char* xs0,
+__device__ __forceinline__ void steps(const LinearArgs& a, const XTile<MI>& xp, const WPtrs& wp, const float (&up)[2], char* xs0,
                                       char* xs1, const char* tabc, uint32_t slot, float mean, int wave, int lane,
                                       floatx16 (&acc)[MI][2]) {
   constexpr int kV = 16 / MI > 1 ? 16 / MI : 1, kL = 8 / MI;
   const int64_t nk = a.cols / kBK;
   WRegs wc, wnx;
-  gt::dma_act(xp, 0, xs0, wave);
+  dma_x(xp, 0, xs0, wave, lane);
   load_w<kDQ>(wc, wp, a.sc, 0);
   f16::half2 sa[2];
   f16::halfx8 bf[2][2];
   Lookups lk[3];
   f16::halfx8 af[3][MI];
-  const uint32_t sw = ((lane & 31) >> 1) & 7, h4 = (lane >> 5) * 4;
   block_scales<kDQ, kF8>(wc, mean, up, sa);
   lookup_step(lk[0], wc.w, 0, tabc, slot);
   bf[0][0] = f16::expand(lk[0].l[0], sa[0]);
@@ -270,25 +263,25 @@ __device__ __forceinline__ void steps(const LinearArgs& a, const gt::ActPtrs<MI>
   __syncthreads();
   for (int64_t ks = 0; ks < nk; ++ks) {
     const int64_t kn = ks + 1 < nk ? ks + 1 : ks;
-    gt::dma_act(xp, kn, (ks & 1) ? xs0 : xs1, wave);  // the other stage was last read before the previous barrier
+    dma_x(xp, kn, (ks & 1) ? xs0 : xs1, wave, lane);  // the other stage was last read before the previous barrier
     load_w<kDQ>(wnx, wp, a.sc, kn);
     __builtin_amdgcn_sched_barrier(0);
-    const char* xa = ((ks & 1) ? xs1 : xs0) + (lane & 31) * gt::kActRowBytes;
-    read_act(xa, 0, sw, h4, af[0]);
-    read_act(xa, 1, sw, h4, af[1]);
+    const char* xa = ((ks & 1) ? xs1 : xs0) + 16 * lane;
+    read_act(xa, 0, af[0]);
+    read_act(xa, 1, af[1]);
     lookup_step(lk[1], wc.w, 1, tabc, slot);
     __builtin_amdgcn_sched_barrier(0);
     mfma16(af[0], bf[0], acc);
     bf[1][0] = f16::expand(lk[1].l[0], sa[0]);
     bf[1][1] = f16::expand(lk[1].l[1], sa[1]);
-    read_act(xa, 2, sw, h4, af[2]);
+    read_act(xa, 2, af[2]);
     lookup_step(lk[2], wc.w, 2, tabc, slot);
     interleave<2 * MI, kV, kL>();
     __builtin_amdgcn_sched_barrier(0);
     mfma16(af[1], bf[1], acc);
     bf[0][0] = f16::expand(lk[2].l[0], sa[0]);
     bf[0][1] = f16::expand(lk[2].l[1], sa[1]);
-    read_act(xa, 3, sw, h4, af[0]);
+    read_act(xa, 3, af[0]);
     lookup_step(lk[0], wc.w, 3, tabc, slot);
     interleave<2 * MI, kV, kL>();
     __builtin_amdgcn_sched_barrier(0);
@@ -316,7 +309,7 @@ __device__ __forceinline__ void linear_unit(const LinearArgs& a, int64_t m0, int
                                             uint32_t slot, float mean, int wave, int lane) {
   char *xs0 = xs, *xs1 = xs + kStageBytes;
   char* turn = xs + wave * (2 * kStageBytes / 4);  // the wave's own quarter, once the steps are through
-  const gt::ActPtrs<MI> xp = gt::make_act_ptrs<MI, 32 * MI>(a.x, a.cols, a.m, m0, wave, lane);
+  const XTile<MI> xp{reinterpret_cast<const char*>(a.x), a.cols / kBK * 4096, m0 / 32, (a.m - 1) / 32};
   WPtrs wp;
   int64_t nrow[2];
   int we[2];
@@ -369,31 +362,35 @@ __global__ __launch_bounds__(kThreads, 1) void k_linear(LinearArgs a) {
   }
 }
 
-// x in float16, its rows' exponents, the adapter columns: each at a multiple of 256 bytes.
+// x in float16, its rows' exponents, the adapter columns, the splits' sums: each at a multiple of 256 bytes.
 struct Workspace {
-  size_t xe, u, bytes;
+  size_t xe, u, part, bytes;
 };
-Workspace workspace_of(int64_t m, int64_t cols, int r) {
+Workspace workspace_of(int64_t m, int64_t rows, int64_t cols, int r) {
   const auto round = [](size_t n) { return (n + 255) & ~size_t(255); };
   Workspace w{};
-  w.xe = round(static_cast<size_t>(m) * static_cast<size_t>(cols) * sizeof(uint16_t));
+  w.xe = round(static_cast<size_t>(x16_rows(m)) * static_cast<size_t>(cols) * sizeof(uint16_t));
   w.u = w.xe + round(static_cast<size_t>(m) * sizeof(int32_t));
-  w.bytes = w.u + (r > 0 ? round(static_cast<size_t>(m) * gemm_lora_cols(r) * sizeof(uint16_t)) : 0);
+  w.part = w.u + (r > 0 ? round(static_cast<size_t>(m) * gemm_lora_cols(r) * sizeof(uint16_t)) : 0);
+  w.bytes = w.part;
+  if (m <= kMidRows) {
+    const MidPlan p = mid_plan(m, rows, cols);
+    if (p.splits > 1) w.bytes += round(static_cast<size_t>(p.splits) * m * rows * sizeof(float));
+  }
   return w;
 }
 
 }  // namespace
 
 size_t linear_workspace(int64_t m, int64_t rows, int64_t cols, int r) {
-  (void)rows;
-  return workspace_of(m, cols, r).bytes;
+  return workspace_of(m, rows, cols, r).bytes;
 }
 
 hipError_t launch_linear(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x, int64_t m,
                          uint16_t* y, const Epilogue& ep, const uint16_t* lora_a, const uint16_t* lora_b, int r,
                          float lora_scale, void* ws, hipStream_t s) {
   LinearArgs a{};
-  const Workspace at = workspace_of(m, cols, r);
+  const Workspace at = workspace_of(m, rows, cols, r);
   char* const w8 = static_cast<char*>(ws);
   a.packed = packed; a.rows = rows; a.cols = cols; a.sc = sc; a.m = m; a.y = y; a.ep = ep;
   a.x = reinterpret_cast<const uint16_t*>(w8);
@@ -408,6 +405,9 @@ hipError_t launch_linear(const uint8_t* packed, int64_t rows, int64_t cols, Scal
     a.kl = static_cast<int>(gemm_lora_cols(r));
     if (hipError_t e = launch_lora_u(x, lora_a, m, cols, r, lora_scale, reinterpret_cast<uint16_t*>(w8 + at.u), s)) return e;
   }
+  if (m <= kMidRows)
+    return launch_linear_mid(mid_plan(m, rows, cols), packed, rows, cols, sc, a.x, a.xe, m, y, ep, a.u, lora_b, r,
+                             reinterpret_cast<float*>(w8 + at.part), s);
   const int64_t tiles = ((rows + kBN - 1) / kBN) * ((m + kBM - 1) / kBM);
   const int64_t slots = device_cus();
   const int64_t last = tiles - tiles / slots * slots;

@@ -101,5 +101,34 @@ __device__ __forceinline__ void finish8(const Epilogue& ep, uint16_t* y, int64_t
   put(y);
 }
 
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Eight bf16 values times a power of two.
+__device__ __forceinline__ bf16x8 times(const u32x4& v, float by) {
+  u32x4 o;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o[k] = bf16_pair(bf16_to_f32(v[k] & 0xFFFFu) * by, __uint_as_float(v[k] & 0xFFFF0000u) * by);
+  return __builtin_bit_cast(bf16x8, o);
+}
+
+// Operands of the adapters' product, times a power of two: columns c .. c + 7 of
+// (B | B | 0) of weight row n (B [rows][r], halves of r_pad columns) ...
+__device__ __forceinline__ bf16x8 adapter_w(const uint16_t* lb, int r, int r_pad, int64_t n, int c, float by) {
+  typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+  const int j0 = c < r_pad ? c : c - r_pad;
+  const uint16_t* b = lb + n * r + j0;
+  u32x4 v = {0, 0, 0, 0};
+  if (j0 + 8 <= r) {
+    v = *reinterpret_cast<const u32x4_any*>(b);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (j0 + i < r) v[i >> 1] |= static_cast<uint32_t>(b[i]) << (16 * (i & 1));
+  }
+  return times(v, by);
+}
+// ... and eight columns of a row of (s T hi | s T lo).
+__device__ __forceinline__ bf16x8 adapter_x(const uint16_t* u, float by) { return times(*reinterpret_cast<const u32x4*>(u), by); }
+
 }  // namespace lin
 }  // namespace nf4i

@@ -3,6 +3,7 @@
 // brings x to float16 (k_linear_x16.hip).
 #pragma once
 
+#include "layer_ops.h"
 #include "nf4_device.h"
 
 namespace nf4i {
@@ -26,6 +27,9 @@ __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
+
+// A workgroup barrier for LDS data only: global loads stay in flight across it.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float power(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
@@ -97,7 +101,21 @@ __device__ __forceinline__ int row_exponent(const Scales& sc, int64_t blk0, int6
 
 }  // namespace f16
 
-// x16[t] = x[t] 2^-xe[t] in float16 for the m rows of x [m][cols] (cols % 64 == 0).
+// x16 = x[t] 2^-xe[t] in float16 for the m rows of x [m][cols] (cols % 64 == 0), in
+// blocks: the 16 bytes of row t, columns 64 k + 32 h + 8 s .. + 7 (h < 2, s < 4) are
+// number ((t / 32 cols / 64 + k) 4 + s) 64 + 32 h + t % 32 of x16, which holds m
+// rounded up to 32 rows (what lies past row m is not written).
+constexpr int64_t x16_rows(int64_t m) { return (m + 31) / 32 * 32; }
 hipError_t launch_x16(const uint16_t* x, int64_t m, int64_t cols, uint16_t* x16, int32_t* xe, hipStream_t s);
+
+// The linear product for up to a few hundred rows (k_linear_mid.hip).
+struct MidPlan {
+  int mi, tiles;     // 32-row bands of a workgroup, workgroups along the rows of x
+  int splits, per;   // of the reduction over workgroups, steps of a wave
+};
+MidPlan mid_plan(int64_t m, int64_t rows, int64_t cols);
+hipError_t launch_linear_mid(const MidPlan& p, const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x16,
+                             const int32_t* xe, int64_t m, uint16_t* y, const Epilogue& ep, const uint16_t* u,
+                             const uint16_t* lora_b, int r, float* part, hipStream_t s);
 
 }  // namespace nf4i

@@ -3,7 +3,8 @@ argument that may be left out.
 
 Bounds.  The weight enters the products in one of two readings (for a whole
 call): rounded once to bf16 after scaling, which the reference then takes too,
-or as fp16 levels with float32 scales, off by 2^-11 of each weight.  Sums of K
+or as the product of a level and a scale each rounded to fp16, rounded to fp16, off by
+3 2^-11 of each weight at most (levels alone in fp16: 2^-11).  Sums of K
 products in float32: K 2^-24 of the sum of magnitudes.  The adapters' thin
 factor is summed in float32 and carried as two bf16 parts: 2^-16.  The
 activation's slope is at most 1.13, its own evaluation good to 2^-16 of the
@@ -41,7 +42,7 @@ def check(torch, W, x, kw, y, pre=None, label=""):
     found = {}
     for reading, wd in dense.items():
         z = xd @ wd.t()
-        err = (terms * F32 + (2.0 ** -11 if reading == "levels" else 0.0)) * (xd.abs() @ wd.abs().t())
+        err = (terms * F32 + (3 * 2.0 ** -11 if reading == "levels" else 0.0)) * (xd.abs() @ wd.abs().t())
         if kw.get("lora_a") is not None:
             a, b, s = kw["lora_a"].double(), kw["lora_b"].double(), kw["lora_scale"]
             z = z + s * (xd @ a.t()) @ b.t()
