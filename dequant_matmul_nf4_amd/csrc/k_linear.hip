@@ -37,7 +37,8 @@ using gt::kThreads;
 
 constexpr int kBN = gt::kTileN, kBK = gt::kStep;
 constexpr int kMI = 8;
-constexpr int64_t kMidRows = 512;  // up to so many rows of x: k_linear_mid.hip
+// Few rows of x, wide enough for a group of steps: k_linear_mid.hip.
+bool mid(int64_t m, int64_t cols) { return m <= 512 && cols >= 256; }
 constexpr int kBM = 32 * kMI;
 constexpr int kStageBytes = gt::act_stage_bytes<kBM>();
 constexpr int kTurnRows = 64;
@@ -47,8 +48,8 @@ struct LinearArgs {
   const uint8_t* packed;
   int64_t rows, cols;
   Scales sc;
-  const uint16_t* x;   // x in float16 blocks (launch_x16), row t scaled by 2^-xe[t]
-  const int32_t* xe;
+  const uint16_t* x;   // x in float16 blocks (launch_linear_prep), row t scaled by 2^-xe[t]
+  const int32_t *xe, *we;
   int64_t m;
   uint16_t* y;
   Epilogue ep;
@@ -320,7 +321,7 @@ __device__ __forceinline__ void linear_unit(const LinearArgs& a, int64_t m0, int
     nrow[j] = n < a.rows ? n : a.rows - 1;  // rows past the end: never stored
     wp.c[j] = a.packed + nrow[j] * (a.cols / 2) + (lane >> 5) * 16;
     wp.blk[j] = nrow[j] * (a.cols / 64);
-    we[j] = f16::row_exponent<kDQ>(a.sc, wp.blk[j], a.cols / 64, mean, lane);
+    we[j] = a.we[nrow[j]];
     up[j] = f16::power(-we[j]);
   }
   floatx16 acc[MI][2];
@@ -362,18 +363,19 @@ __global__ __launch_bounds__(kThreads, 1) void k_linear(LinearArgs a) {
   }
 }
 
-// x in float16, its rows' exponents, the adapter columns, the splits' sums: each at a multiple of 256 bytes.
+// x in float16, its rows' exponents and the weight's, the adapter columns, the splits' sums: each at a multiple of 256 bytes.
 struct Workspace {
-  size_t xe, u, part, bytes;
+  size_t xe, we, u, part, bytes;
 };
 Workspace workspace_of(int64_t m, int64_t rows, int64_t cols, int r) {
   const auto round = [](size_t n) { return (n + 255) & ~size_t(255); };
   Workspace w{};
   w.xe = round(static_cast<size_t>(x16_rows(m)) * static_cast<size_t>(cols) * sizeof(uint16_t));
-  w.u = w.xe + round(static_cast<size_t>(m) * sizeof(int32_t));
+  w.we = w.xe + round(static_cast<size_t>(m) * sizeof(int32_t));
+  w.u = w.we + round(static_cast<size_t>(rows) * sizeof(int32_t));
   w.part = w.u + (r > 0 ? round(static_cast<size_t>(m) * gemm_lora_cols(r) * sizeof(uint16_t)) : 0);
   w.bytes = w.part;
-  if (m <= kMidRows) {
+  if (mid(m, cols)) {
     const MidPlan p = mid_plan(m, rows, cols);
     if (p.splits > 1) w.bytes += round(static_cast<size_t>(p.splits) * m * rows * sizeof(float));
   }
@@ -395,7 +397,10 @@ hipError_t launch_linear(const uint8_t* packed, int64_t rows, int64_t cols, Scal
   a.packed = packed; a.rows = rows; a.cols = cols; a.sc = sc; a.m = m; a.y = y; a.ep = ep;
   a.x = reinterpret_cast<const uint16_t*>(w8);
   a.xe = reinterpret_cast<const int32_t*>(w8 + at.xe);
-  if (hipError_t e = launch_x16(x, m, cols, reinterpret_cast<uint16_t*>(w8), reinterpret_cast<int32_t*>(w8 + at.xe), s)) return e;
+  a.we = reinterpret_cast<const int32_t*>(w8 + at.we);
+  if (hipError_t e = launch_linear_prep(x, m, cols, reinterpret_cast<uint16_t*>(w8), reinterpret_cast<int32_t*>(w8 + at.xe), sc, rows,
+                                        reinterpret_cast<int32_t*>(w8 + at.we), s))
+    return e;
   a.cb = codebook(sc.fp4);
   if (r > 0) {
     a.u = reinterpret_cast<const uint16_t*>(w8 + at.u);
@@ -405,8 +410,8 @@ hipError_t launch_linear(const uint8_t* packed, int64_t rows, int64_t cols, Scal
     a.kl = static_cast<int>(gemm_lora_cols(r));
     if (hipError_t e = launch_lora_u(x, lora_a, m, cols, r, lora_scale, reinterpret_cast<uint16_t*>(w8 + at.u), s)) return e;
   }
-  if (m <= kMidRows)
-    return launch_linear_mid(mid_plan(m, rows, cols), packed, rows, cols, sc, a.x, a.xe, m, y, ep, a.u, lora_b, r,
+  if (mid(m, cols))
+    return launch_linear_mid(mid_plan(m, rows, cols), packed, rows, cols, sc, a.x, a.xe, a.we, m, y, ep, a.u, lora_b, r,
                              reinterpret_cast<float*>(w8 + at.part), s);
   const int64_t tiles = ((rows + kBN - 1) / kBN) * ((m + kBM - 1) / kBM);
   const int64_t slots = device_cus();

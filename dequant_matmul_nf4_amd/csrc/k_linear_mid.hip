@@ -34,8 +34,8 @@ struct MidArgs {
   const uint8_t* packed;
   int64_t rows, cols;
   Scales sc;
-  const uint16_t* x;   // x in float16 blocks (launch_x16)
-  const int32_t* xe;
+  const uint16_t* x;   // x in float16 blocks (launch_linear_prep)
+  const int32_t *xe, *we;
   int64_t m;
   uint16_t* y;
   Epilogue ep;
@@ -48,12 +48,19 @@ struct MidArgs {
   Codebook cb;
 };
 
-struct Codes {
-  u32x4 c[kJ][kGroup];
-};
+// The scale inputs of a row's four blocks of a group, from block `at` on (as many as
+// the row has): int8 codes and the two group scales that can occur, or the absmax.
+typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef float floatx4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+template <bool kDQ>
 struct ScaleInputs {
-  int q[kJ][kGroup];
-  float s[kJ][kGroup];
+  uint32_t q[kJ];
+  float lo[kJ], hi[kJ];
+};
+template <>
+struct ScaleInputs<false> {
+  floatx4 v[kJ];
 };
 
 // The adapters' share, brought to the sums' powers of two: as in k_linear.hip.
@@ -79,6 +86,8 @@ __device__ __forceinline__ void adapters(floatx16 (&acc)[MI][kJ], const MidArgs&
 
 template <int MI, bool kDQ, bool kF8>
 __global__ __launch_bounds__(kThreads, 1) void k_linear_mid(MidArgs a) {
+  constexpr int kX = MI < 2 ? 4 : 2;              // steps of x in registers
+  constexpr int kC = MI < 3 ? 2 * kGroup : kGroup;  // steps of codes
   constexpr int kMeet = kWaves * MI * 4096;  // a 32-column tile of all waves
   constexpr int kTab = 4 * f16::kTabWords;
   constexpr int kLds = kTab > kMeet ? kTab : kMeet;
@@ -109,27 +118,25 @@ __global__ __launch_bounds__(kThreads, 1) void k_linear_mid(MidArgs a) {
     soff[j] = wr * nblk;
   }
   auto clamp = [&](int k) { return k < nk ? k : nk - 1; };  // past the end: the last again, its scale zero
-  auto load_scales = [&](ScaleInputs& g, int k0) {
+  auto load_scales = [&](ScaleInputs<kDQ>& g, int k0) {
+    const int64_t b = blk + (k0 < nk - kGroup ? k0 : nk - kGroup);
 #pragma unroll
-    for (int s = 0; s < kGroup; ++s) {
-      const int64_t b = blk + clamp(k0 + s);
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        if constexpr (kDQ) {
-          g.q[j][s] = (a.sc.q + b)[soff[j]];
-          g.s[j][s] = (a.sc.absmax2 + (b >> 8))[(static_cast<uint32_t>(b & 255) + soff[j]) >> 8];
-        } else {
-          g.s[j][s] = (a.sc.absmax + b)[soff[j]];
-        }
+    for (int j = 0; j < kJ; ++j) {
+      if constexpr (kDQ) {
+        g.q[j] = *reinterpret_cast<const u32_any*>(a.sc.q + b + soff[j]);
+        const float* s2 = a.sc.absmax2 + (b >> 8);
+        const uint32_t at = static_cast<uint32_t>(b & 255) + soff[j];
+        g.lo[j] = s2[at >> 8];
+        g.hi[j] = s2[(at + 3) >> 8];
+      } else {
+        g.v[j] = *reinterpret_cast<const floatx4_any*>(a.sc.absmax + b + soff[j]);
       }
     }
   };
-  auto load_codes = [&](Codes& g, int k0) {
+  auto load_codes = [&](u32x4 (&c)[kJ], int k) {
+    const uint8_t* p = cop + static_cast<int64_t>(clamp(k)) * (kBK / 2);
 #pragma unroll
-    for (int j = 0; j < kJ; ++j)
-#pragma unroll
-      for (int s = 0; s < kGroup; ++s)
-        g.c[j][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(cop + static_cast<int64_t>(clamp(k0 + s)) * (kBK / 2) + coff[j]));
+    for (int j = 0; j < kJ; ++j) c[j] = *reinterpret_cast<const u32x4*>(p + coff[j]);
   };
   // x of a step: blocks of the 32-row bands (past the last band: the last)
   const int64_t band = static_cast<int64_t>(nk) * 4096, last = (a.m - 1) / 32;
@@ -147,37 +154,59 @@ __global__ __launch_bounds__(kThreads, 1) void k_linear_mid(MidArgs a) {
         x[i][s] = *reinterpret_cast<const f16::halfx8*>(xb[i] + static_cast<int64_t>(clamp(k)) * 4096 + s * 1024 + 16 * lane);
   };
 
-  Codes gc, gn;
-  ScaleInputs in;
-  f16::halfx8 xv[2][MI][4];
-  load_scales(in, kb);
-  load_codes(gc, kb);
-  load_x(xv[0], kb);
+  // rings of registers
+  u32x4 c[kC][kJ];
+  ScaleInputs<kDQ> in[kC / kGroup];
+  f16::halfx8 xv[kX][MI][4];
+  int we[kJ];
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) we[j] = a.we[nrow[j]];
+  load_scales(in[0], kb);
+#pragma unroll
+  for (int s = 0; s < kGroup; ++s) load_codes(c[s], kb + s);
+#pragma unroll
+  for (int s = 0; s < kX - 1; ++s) load_x(xv[s], kb + s);
+  if constexpr (kC > kGroup) {
+    load_scales(in[1], kb + kGroup);
+#pragma unroll
+    for (int s = kGroup; s < kC; ++s) load_codes(c[s], kb + s);
+  }
   if constexpr (kF8) rtab[threadIdx.x] = kE4m3Ratio.v[threadIdx.x];
   f16::fill_table<kThreads>(reinterpret_cast<uint32_t*>(lds), a.cb);
-  int we[kJ];
   float up[kJ];
 #pragma unroll
-  for (int j = 0; j < kJ; ++j) {
-    we[j] = f16::row_exponent<kDQ>(a.sc, nrow[j] * nblk, nblk, mean, lane);
-    up[j] = f16::power(-we[j]);
-  }
+  for (int j = 0; j < kJ; ++j) up[j] = f16::power(-we[j]);
   if (wave == 0 && lane < 32)
 #pragma unroll
     for (int j = 0; j < kJ; ++j) wex[32 * j + lane] = we[j];
   f16::lds_barrier();
 
-  f16::half2 sa[kJ][kGroup];
-  auto scales = [&](int k0) {
+  // the float16 scales of a group's steps, zero past the wave's last
+  f16::half2 sa[kGroup][kJ];
+  auto scales = [&](const ScaleInputs<kDQ>& g, int k0) {
+    const int off = k0 < nk - kGroup ? 0 : k0 - (nk - kGroup);  // of the loaded blocks the group begins here
 #pragma unroll
-    for (int s = 0; s < kGroup; ++s)
+    for (int j = 0; j < kJ; ++j) {
+      float v[kGroup];
+      if constexpr (kDQ) {
+        const int64_t b = blk + k0 - off;
+        const int cross = 256 - static_cast<int>((static_cast<uint32_t>(b & 255) + soff[j]) & 255);  // the first block under hi
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        float v;
-        if constexpr (kDQ) v = (kF8 ? rtab[in.q[j][s] & 0xFF] : div127(in.q[j][s])) * in.s[j][s] + mean;  // a_hat, three roundings
-        else v = in.s[j][s];
-        sa[j][s] = f16::twice(k0 + s < ke ? v * up[j] : 0.0f);
+        for (int s = 0; s < kGroup; ++s) {
+          const int q = static_cast<int>(g.q[j] << (24 - 8 * s)) >> 24;
+          v[s] = (kF8 ? rtab[q & 0xFF] : div127(q)) * (s >= cross ? g.hi[j] : g.lo[j]) + mean;  // a_hat, three roundings
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < kGroup; ++s) v[s] = g.v[j][s];
       }
+      if (off > 0) {  // the row's last blocks, loaded from before the group's first
+#pragma unroll
+        for (int s = 0; s < kGroup; ++s) v[s] = off + s == 1 ? v[1] : off + s == 2 ? v[2] : v[3];
+      }
+#pragma unroll
+      for (int s = 0; s < kGroup; ++s) sa[s][j] = f16::twice(k0 + s < ke ? v[s] * up[j] : 0.0f);
+    }
   };
   floatx16 acc[MI][kJ];
 #pragma unroll
@@ -187,32 +216,57 @@ __global__ __launch_bounds__(kThreads, 1) void k_linear_mid(MidArgs a) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  for (int k0 = kb; k0 < ke; k0 += kGroup) {
-    scales(k0);
-    load_scales(in, k0 + kGroup);
-    load_codes(gn, k0 + kGroup);
-    __builtin_amdgcn_sched_barrier(0);
+  // The products of a 16-wide step q, and pinned between them (left to the compiler it
+  // all collects behind or before them) what comes next: the weights of q + 1
+  // multiplied out, the levels of q + 2 looked up (its code words w), and more(i).
+  uint32_t lk[2][kJ][4];
+  u32x4 bf[2][kJ];
+  constexpr int kN = MI * kJ;
+  auto products = [&](int q, const f16::halfx8 (&x)[MI][4], int xq, const u32x4 (&w)[kJ], int word, const f16::half2 (&sc)[kJ], const auto& more) {
+    const int cur = q & 1, nxt = cur ^ 1;
 #pragma unroll
-    for (int s = 0; s < kGroup; ++s) {
-      load_x(xv[(s + 1) & 1], k0 + s + 1);
+    for (int i = 0; i < kN; ++i) {
+      acc[i / kJ][i % kJ] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16::halfx8, bf[cur][i % kJ]), x[i / kJ][xq], acc[i / kJ][i % kJ], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
+      more(i);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        f16::halfx8 bf[kJ];
+      for (int e = 4 * kJ * i / kN; e < 4 * kJ * (i + 1) / kN; ++e) bf[nxt][e >> 2][e & 3] = opaque(f16::times(lk[nxt][e >> 2][e & 3], sc[e >> 2]));
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          uint32_t l[4];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) l[b] = f16::look_up(gc.c[j][s][q], b, tabc, slot);
-          bf[j] = f16::expand(l, sa[j][s]);
-        }
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-          for (int j = 0; j < kJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bf[j], xv[s & 1][i][q], acc[i][j], 0, 0, 0);
-      }
+      for (int e = 4 * kJ * i / kN; e < 4 * kJ * (i + 1) / kN; ++e) lk[cur][e >> 2][e & 3] = f16::look_up(w[e >> 2][word], e & 3, tabc, slot);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    gc = gn;
+  };
+  if (kb < ke) {
+    scales(in[0], kb);
+#pragma unroll
+    for (int j = 0; j < kJ; ++j)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        bf[0][j][b] = f16::times(f16::look_up(c[0][j][0], b, tabc, slot), sa[0][j]);
+        lk[1][j][b] = f16::look_up(c[0][j][1], b, tabc, slot);
+      }
+  }
+  for (int k0 = kb; k0 < ke; k0 += kC) {
+#pragma unroll
+    for (int s = 0; s < kC; ++s) {
+      const int sn = (s + 1) % kC;
+      // x of kX - 1 steps ahead; and two steps' codes at a time, half a line of each
+      // row, kC steps ahead into the places of what is done
+      products(0, xv[s % kX], 0, c[s], 2, sa[s % kGroup], [&](int i) {
+        if (i == 0) load_x(xv[(s + kX - 1) % kX], k0 + s + kX - 1);
+      });
+      products(1, xv[s % kX], 1, c[s], 3, sa[s % kGroup], [](int) {});
+      products(2, xv[s % kX], 2, c[sn], 0, sa[s % kGroup], [&](int i) {
+        if (s % 2 == 1 && i == 0) {
+          load_codes(c[s - 1], k0 + s - 1 + kC);
+          if (s % kGroup == 1) load_scales(in[s / kGroup], k0 + s - 1 + kC);
+        }
+        if (s % 2 == 1 && i == kN / 2) load_codes(c[s], k0 + s + kC);
+      });
+      products(3, xv[s % kX], 3, c[sn], 1, sa[sn % kGroup], [&](int i) {
+        if (sn % kGroup == 0 && i == 0) scales(in[sn / kGroup], k0 + s + 1);
+      });
+    }
   }
   if (a.r > 0 && blockIdx.z == 0 && wave == 0) adapters<MI>(acc, a, m0, nrow, we, lane);
 
@@ -327,16 +381,16 @@ MidPlan mid_plan(int64_t m, int64_t rows, int64_t cols) {
   splits = splits < most ? splits : most;
   p.splits = static_cast<int>(splits < 1 ? 1 : splits < 16 ? splits : 16);
   int64_t per = (nk + p.splits * kWaves - 1) / (p.splits * kWaves);
-  p.per = static_cast<int>((per + kGroup - 1) / kGroup * kGroup);
+  p.per = static_cast<int>((per + 2 * kGroup - 1) / (2 * kGroup) * (2 * kGroup));
   p.splits = static_cast<int>((nk + static_cast<int64_t>(p.per) * kWaves - 1) / (static_cast<int64_t>(p.per) * kWaves));
   return p;
 }
 
 hipError_t launch_linear_mid(const MidPlan& p, const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x16,
-                             const int32_t* xe, int64_t m, uint16_t* y, const Epilogue& ep, const uint16_t* u,
+                             const int32_t* xe, const int32_t* we, int64_t m, uint16_t* y, const Epilogue& ep, const uint16_t* u,
                              const uint16_t* lora_b, int r, float* part, hipStream_t s) {
   MidArgs a{};
-  a.packed = packed; a.rows = rows; a.cols = cols; a.sc = sc; a.x = x16; a.xe = xe; a.m = m; a.y = y; a.ep = ep;
+  a.packed = packed; a.rows = rows; a.cols = cols; a.sc = sc; a.x = x16; a.xe = xe; a.we = we; a.m = m; a.y = y; a.ep = ep;
   a.u = u; a.lb = lora_b; a.r = r; a.r_pad = (r + 15) / 16 * 16; a.kl = static_cast<int>(gemm_lora_cols(r));
   a.splits = p.splits; a.per = p.per; a.part = part;
   a.cb = codebook(sc.fp4);

@@ -1,6 +1,6 @@
 // The float16 operands of the linear kernels: weights as level times scale, the
 // power of two of a weight row, the table of level pairs, and the kernel that
-// brings x to float16 (k_linear_x16.hip).
+// brings x to float16 (k_linear_prep.hip).
 #pragma once
 
 #include "layer_ops.h"
@@ -83,30 +83,16 @@ __device__ __forceinline__ halfx8 expand(const uint32_t (&l)[4], half2 s) {
   return __builtin_bit_cast(halfx8, v);
 }
 
-// The exponent of a weight row of nblk blocks from block blk0 on: that of its
-// largest block scale, or with double quantization of a bound on it, the
-// largest group scale plus the mean.  Lanes l and l + 32 hold the same row.
-template <bool kDQ>
-__device__ __forceinline__ int row_exponent(const Scales& sc, int64_t blk0, int64_t nblk, float mean, int lane) {
-  float top = 0.0f;
-  if constexpr (kDQ) {
-    for (int64_t g = blk0 >> 8; g <= (blk0 + nblk - 1) >> 8; ++g) top = fmaxf(top, fabsf(sc.absmax2[g]));
-    top += fabsf(mean);
-  } else {
-    for (int64_t b = lane >> 5; b < nblk; b += 2) top = fmaxf(top, fabsf(sc.absmax[blk0 + b]));
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
-  }
-  return exponent_of(top);
-}
-
 }  // namespace f16
 
 // x16 = x[t] 2^-xe[t] in float16 for the m rows of x [m][cols] (cols % 64 == 0), in
 // blocks: the 16 bytes of row t, columns 64 k + 32 h + 8 s .. + 7 (h < 2, s < 4) are
 // number ((t / 32 cols / 64 + k) 4 + s) 64 + 32 h + t % 32 of x16, which holds m
-// rounded up to 32 rows (what lies past row m is not written).
+// rounded up to 32 rows (what lies past row m is not written).  we: the exponents of
+// the weight's rows.
 constexpr int64_t x16_rows(int64_t m) { return (m + 31) / 32 * 32; }
-hipError_t launch_x16(const uint16_t* x, int64_t m, int64_t cols, uint16_t* x16, int32_t* xe, hipStream_t s);
+hipError_t launch_linear_prep(const uint16_t* x, int64_t m, int64_t cols, uint16_t* x16, int32_t* xe, const Scales& sc,
+                              int64_t rows, int32_t* we, hipStream_t s);
 
 // The linear product for up to a few hundred rows (k_linear_mid.hip).
 struct MidPlan {
@@ -115,7 +101,7 @@ struct MidPlan {
 };
 MidPlan mid_plan(int64_t m, int64_t rows, int64_t cols);
 hipError_t launch_linear_mid(const MidPlan& p, const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x16,
-                             const int32_t* xe, int64_t m, uint16_t* y, const Epilogue& ep, const uint16_t* u,
+                             const int32_t* xe, const int32_t* we, int64_t m, uint16_t* y, const Epilogue& ep, const uint16_t* u,
                              const uint16_t* lora_b, int r, float* part, hipStream_t s);
 
 }  // namespace nf4i
