@@ -9,6 +9,8 @@
 // and the block scale is applied once per chunk; the per-lane partial sums are
 // reduced across the wave with shuffles at the end.
 #include "gemv_rows.h"
+#include "linear_epilogue.h"
+#include "linear_f16.h"
 
 namespace nf4i {
 namespace {
@@ -328,12 +330,11 @@ struct RowsPlan {
   int wpr;           // waves per segment (row parts)
 };
 
-// MC rows of x per launch (x and y point at the first of them; the x rows
-// are cols apart, the y rows `rows` apart).
-template <int U, int kWaves, int MC, bool kDQ, bool kF8, bool kBf16Out>
-__global__ __launch_bounds__(kWaves * 64) void k_gemv_rows(const uint8_t* packed, int64_t rows,
-                                                           int64_t cols, Scales sc, const uint16_t* x,
-                                                           void* __restrict__ y, Codebook cb, RowsPlan pl) {
+// MC rows of x per launch (x points at the first of them, cols apart).
+// out.store(c, row, s): takes the finished sum of x row c and weight row `row`.
+template <int U, int kWaves, int MC, bool kDQ, bool kF8, class Out>
+__device__ __forceinline__ void gemv_rows(const uint8_t* packed, int64_t rows, int64_t cols, const Scales& sc,
+                                          const uint16_t* x, const Out& out, const Codebook& cb, const RowsPlan& pl) {
   constexpr int kRowsWg = kRowsMaxWg / MC;
   __shared__ uint32_t tab[256 * 64];
   __shared__ float part[kRowsWg * kSegMax * MC];
@@ -425,9 +426,32 @@ __global__ __launch_bounds__(kWaves * 64) void k_gemv_rows(const uint8_t* packed
     if (row >= rows) continue;
     float s = part[(rt * kSegMax) * MC + c];
     for (int k = 1; k < pl.nseg; ++k) s += part[(rt * kSegMax + k) * MC + c];
+    out.store(c, row, s);
+  }
+}
+
+// The product itself (y points at the first of the rows, `rows` apart) ...
+template <bool kBf16Out>
+struct StoreY {
+  void* __restrict__ y;
+  int64_t rows;
+  __device__ __forceinline__ void store(int c, int64_t row, float s) const {
     if constexpr (kBf16Out) static_cast<uint16_t*>(y)[c * rows + row] = static_cast<uint16_t>(f32_to_bf16(s));
     else static_cast<float*>(y)[c * rows + row] = s;
   }
+};
+template <int U, int kWaves, int MC, bool kDQ, bool kF8, bool kBf16Out>
+__global__ __launch_bounds__(kWaves * 64) void k_gemv_rows(const uint8_t* packed, int64_t rows,
+                                                           int64_t cols, Scales sc, const uint16_t* x,
+                                                           void* __restrict__ y, Codebook cb, RowsPlan pl) {
+  gemv_rows<U, kWaves, MC, kDQ, kF8>(packed, rows, cols, sc, x, StoreY<kBf16Out>{y, rows}, cb, pl);
+}
+
+// ... and one token through a layer: the product with its epilogue.
+template <int kWaves, bool kDQ, bool kF8>
+__global__ __launch_bounds__(kWaves * 64) void k_linear_row(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc,
+                                                            const uint16_t* x, lin::FewOut out, Codebook cb, RowsPlan pl) {
+  gemv_rows<1, kWaves, 1, kDQ, kF8>(packed, rows, cols, sc, x, out, cb, pl);
 }
 
 // Plan for k_gemv_rows: rows split evenly over at least one workgroup per CU
@@ -859,7 +883,35 @@ void launch_m1(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, con
   else hipLaunchKernelGGL((k_gemv_m1<R, kDQ, false>), gd, b, 0, s, packed, rows, cols, sc, x, y, cb);
 }
 
+// Waves of a workgroup for one row of x: 8 for one column segment, else 16, or 8
+// where 16 would leave row parts without rows.
+int row_waves(int64_t rows, int64_t nseg) {
+  return nseg == 1 || (nseg <= 8 && rows < device_cus() * (16 / nseg)) ? 8 : 16;
+}
+
+template <int kWaves>
+hipError_t launch_linear_row_of(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x,
+                                const lin::FewOut& out, hipStream_t s) {
+  const RowsPlan pl = rows_plan(rows, cols, kWaves, kRowsMaxWg);
+  if (pl.nseg > kSegMax || pl.wpr < 1 || (cols / 64) * 32 >= (int64_t{1} << 32)) return hipErrorInvalidValue;
+  const Codebook& cb = codebook(sc.fp4);
+  const dim3 gd(static_cast<unsigned>(pl.grid)), bd(64 * kWaves);
+  if (sc.absmax) hipLaunchKernelGGL((k_linear_row<kWaves, false, false>), gd, bd, 0, s, packed, rows, cols, sc, x, out, cb, pl);
+  else if (sc.f8) hipLaunchKernelGGL((k_linear_row<kWaves, true, true>), gd, bd, 0, s, packed, rows, cols, sc, x, out, cb, pl);
+  else hipLaunchKernelGGL((k_linear_row<kWaves, true, false>), gd, bd, 0, s, packed, rows, cols, sc, x, out, cb, pl);
+  return hipGetLastError();
+}
+
 }  // namespace
+
+bool linear_row_fits(int64_t cols) { return (cols / 64 + 63) / 64 <= kSegMax; }
+
+hipError_t launch_linear_row(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x, uint16_t* y,
+                             const Epilogue& ep, const uint16_t* u, const uint16_t* lora_b, int r, hipStream_t s) {
+  const lin::FewOut out = lin::few_out(rows, y, ep, u, lora_b, r);
+  return row_waves(rows, (cols / 64 + 63) / 64) == 8 ? launch_linear_row_of<8>(packed, rows, cols, sc, x, out, s)
+                                                     : launch_linear_row_of<16>(packed, rows, cols, sc, x, out, s);
+}
 
 hipError_t launch_gemv(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x,
                        int64_t m, void* y, int y_bf16, hipStream_t s) {
@@ -870,14 +922,8 @@ hipError_t launch_gemv(const uint8_t* packed, int64_t rows, int64_t cols, Scales
   const int mm = static_cast<int>(m);
   if (m == 1) {
     const int64_t nseg = (cols / 64 + 63) / 64;
-    if (nseg == 1) {
-      // one column segment: 8 waves
-      return launch_rows_sc<1, 8, 1>(packed, rows, cols, sc, x, y, y_bf16, s);
-    }
     if (nseg <= kSegMax) {
-      // 16 waves, or 8 where 16 would leave row parts without rows
-      if (nseg <= 8 && rows < device_cus() * (16 / nseg))
-        return launch_rows_sc<1, 8, 1>(packed, rows, cols, sc, x, y, y_bf16, s);
+      if (row_waves(rows, nseg) == 8) return launch_rows_sc<1, 8, 1>(packed, rows, cols, sc, x, y, y_bf16, s);
       return launch_rows_sc<1, 16, 1>(packed, rows, cols, sc, x, y, y_bf16, s);
     }
     // wider than 16 segments (cols > 65536): one row group per wave

@@ -37,7 +37,10 @@ using gt::kThreads;
 
 constexpr int kBN = gt::kTileN, kBK = gt::kStep;
 constexpr int kMI = 8;
-// Few rows of x, wide enough for a group of steps: k_linear_mid.hip.
+// Which kernels take m rows of x: one row or a decode batch stream the codes past x as
+// it is; up to some hundreds, of rows wide enough for a group of steps, cut the
+// reduction (k_linear_mid.hip); this file's the rest.
+bool few(int64_t m) { return m <= 16; }
 bool mid(int64_t m, int64_t cols) { return m <= 512 && cols >= 256; }
 constexpr int kBM = 32 * kMI;
 constexpr int kStageBytes = gt::act_stage_bytes<kBM>();
@@ -370,6 +373,10 @@ struct Workspace {
 Workspace workspace_of(int64_t m, int64_t rows, int64_t cols, int r) {
   const auto round = [](size_t n) { return (n + 255) & ~size_t(255); };
   Workspace w{};
+  if (few(m)) {
+    w.bytes = r > 0 ? round(static_cast<size_t>(m) * gemm_lora_cols(r) * sizeof(uint16_t)) : 0;
+    return w;
+  }
   w.xe = round(static_cast<size_t>(x16_rows(m)) * static_cast<size_t>(cols) * sizeof(uint16_t));
   w.we = w.xe + round(static_cast<size_t>(m) * sizeof(int32_t));
   w.u = w.we + round(static_cast<size_t>(rows) * sizeof(int32_t));
@@ -391,9 +398,14 @@ size_t linear_workspace(int64_t m, int64_t rows, int64_t cols, int r) {
 hipError_t launch_linear(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x, int64_t m,
                          uint16_t* y, const Epilogue& ep, const uint16_t* lora_a, const uint16_t* lora_b, int r,
                          float lora_scale, void* ws, hipStream_t s) {
-  LinearArgs a{};
   const Workspace at = workspace_of(m, rows, cols, r);
   char* const w8 = static_cast<char*>(ws);
+  uint16_t* const u = reinterpret_cast<uint16_t*>(w8 + at.u);
+  if (r > 0)
+    if (hipError_t e = launch_lora_u(x, lora_a, m, cols, r, lora_scale, u, s)) return e;
+  if (m == 1 && linear_row_fits(cols)) return launch_linear_row(packed, rows, cols, sc, x, y, ep, u, lora_b, r, s);
+  if (few(m)) return launch_linear_few(packed, rows, cols, sc, x, m, y, ep, u, lora_b, r, s);
+  LinearArgs a{};
   a.packed = packed; a.rows = rows; a.cols = cols; a.sc = sc; a.m = m; a.y = y; a.ep = ep;
   a.x = reinterpret_cast<const uint16_t*>(w8);
   a.xe = reinterpret_cast<const int32_t*>(w8 + at.xe);
@@ -402,14 +414,11 @@ hipError_t launch_linear(const uint8_t* packed, int64_t rows, int64_t cols, Scal
                                         reinterpret_cast<int32_t*>(w8 + at.we), s))
     return e;
   a.cb = codebook(sc.fp4);
-  if (r > 0) {
-    a.u = reinterpret_cast<const uint16_t*>(w8 + at.u);
-    a.lb = lora_b;
-    a.r = r;
-    a.r_pad = (r + 15) / 16 * 16;
-    a.kl = static_cast<int>(gemm_lora_cols(r));
-    if (hipError_t e = launch_lora_u(x, lora_a, m, cols, r, lora_scale, reinterpret_cast<uint16_t*>(w8 + at.u), s)) return e;
-  }
+  a.u = u;
+  a.lb = lora_b;
+  a.r = r;
+  a.r_pad = (r + 15) / 16 * 16;
+  a.kl = static_cast<int>(gemm_lora_cols(r));
   if (mid(m, cols))
     return launch_linear_mid(mid_plan(m, rows, cols), packed, rows, cols, sc, a.x, a.xe, a.we, m, y, ep, a.u, lora_b, r,
                              reinterpret_cast<float*>(w8 + at.part), s);

@@ -130,5 +130,48 @@ __device__ __forceinline__ bf16x8 adapter_w(const uint16_t* lb, int r, int r_pad
 // ... and eight columns of a row of (s T hi | s T lo).
 __device__ __forceinline__ bf16x8 adapter_x(const uint16_t* u, float by) { return times(*reinterpret_cast<const u32x4*>(u), by); }
 
+// What takes the sums of a few rows of x one by one: row t of x and weight row n.
+struct FewOut {
+  int64_t rows;
+  uint16_t* y;
+  Epilogue ep;
+  const uint16_t* u;   // adapter columns of x: [m][kl] (s T hi | s T lo | 0)
+  const uint16_t* lb;  // B [rows][r]
+  int r, r_pad, kl;    // 0 without adapters
+
+  __device__ __forceinline__ void store(int64_t t, int64_t n, float z) const {
+    if (r > 0) z += adapters(t, n);
+    if (ep.bias) z += ep.bias_f32 ? static_cast<const float*>(ep.bias)[n] : bf16_to_f32(static_cast<const uint16_t*>(ep.bias)[n]);
+    finish1(ep, y, t * rows + n, z);
+  }
+  // sum_j (hi + lo)[t][j] B[n][j]
+  __device__ __forceinline__ float adapters(int64_t t, int64_t n) const {
+    typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+    const uint16_t* h = u + t * kl;
+    const uint16_t* b = lb + n * r;
+    float s = 0.0f;
+    for (int j = 0; j < r; j += 8) {
+      const u32x4 hi = *reinterpret_cast<const u32x4*>(h + j), lo = *reinterpret_cast<const u32x4*>(h + r_pad + j);
+      u32x4 w = {0, 0, 0, 0};
+      if (j + 8 <= r) {
+        w = *reinterpret_cast<const u32x4_any*>(b + j);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (j + i < r) w[i >> 1] |= static_cast<uint32_t>(b[j + i]) << (16 * (i & 1));
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        s = fmaf(bf16_to_f32(hi[c] & 0xFFFFu) + bf16_to_f32(lo[c] & 0xFFFFu), bf16_to_f32(w[c] & 0xFFFFu), s);
+        s = fmaf(__uint_as_float(hi[c] & 0xFFFF0000u) + __uint_as_float(lo[c] & 0xFFFF0000u), __uint_as_float(w[c] & 0xFFFF0000u), s);
+      }
+    }
+    return s;
+  }
+};
+inline FewOut few_out(int64_t rows, uint16_t* y, const Epilogue& ep, const uint16_t* u, const uint16_t* lora_b, int r) {
+  return FewOut{rows, y, ep, u, lora_b, r, (r + 15) / 16 * 16, static_cast<int>(gemm_lora_cols(r))};
+}
+
 }  // namespace lin
 }  // namespace nf4i
