@@ -331,7 +331,7 @@ struct RowsPlan {
 };
 
 // MC rows of x per launch (x points at the first of them, cols apart).
-// out.store(c, row, s): takes the finished sum of x row c and weight row `row`.
+// out.store(c, 1, row, s): takes the finished sum of x row c and weight row `row`.
 template <int U, int kWaves, int MC, bool kDQ, bool kF8, class Out>
 __device__ __forceinline__ void gemv_rows(const uint8_t* packed, int64_t rows, int64_t cols, const Scales& sc,
                                           const uint16_t* x, const Out& out, const Codebook& cb, const RowsPlan& pl) {
@@ -426,7 +426,8 @@ __device__ __forceinline__ void gemv_rows(const uint8_t* packed, int64_t rows, i
     if (row >= rows) continue;
     float s = part[(rt * kSegMax) * MC + c];
     for (int k = 1; k < pl.nseg; ++k) s += part[(rt * kSegMax + k) * MC + c];
-    out.store(c, row, s);
+    float z[1] = {s};
+    out.store(c, 1, row, z);
   }
 }
 
@@ -435,9 +436,9 @@ template <bool kBf16Out>
 struct StoreY {
   void* __restrict__ y;
   int64_t rows;
-  __device__ __forceinline__ void store(int c, int64_t row, float s) const {
-    if constexpr (kBf16Out) static_cast<uint16_t*>(y)[c * rows + row] = static_cast<uint16_t>(f32_to_bf16(s));
-    else static_cast<float*>(y)[c * rows + row] = s;
+  __device__ __forceinline__ void store(int c, int, int64_t row, const float (&z)[1]) const {
+    if constexpr (kBf16Out) static_cast<uint16_t*>(y)[c * rows + row] = static_cast<uint16_t>(f32_to_bf16(z[0]));
+    else static_cast<float*>(y)[c * rows + row] = z[0];
   }
 };
 template <int U, int kWaves, int MC, bool kDQ, bool kF8, bool kBf16Out>
@@ -447,11 +448,11 @@ __global__ __launch_bounds__(kWaves * 64) void k_gemv_rows(const uint8_t* packed
   gemv_rows<U, kWaves, MC, kDQ, kF8>(packed, rows, cols, sc, x, StoreY<kBf16Out>{y, rows}, cb, pl);
 }
 
-// ... and one token through a layer: the product with its epilogue.
-template <int kWaves, bool kDQ, bool kF8>
+// ... and one or two tokens through a layer: the product with its epilogue.
+template <int kWaves, int MC, bool kDQ, bool kF8>
 __global__ __launch_bounds__(kWaves * 64) void k_linear_row(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc,
                                                             const uint16_t* x, lin::FewOut out, Codebook cb, RowsPlan pl) {
-  gemv_rows<1, kWaves, 1, kDQ, kF8>(packed, rows, cols, sc, x, out, cb, pl);
+  gemv_rows<1, kWaves, MC, kDQ, kF8>(packed, rows, cols, sc, x, out, cb, pl);
 }
 
 // Plan for k_gemv_rows: rows split evenly over at least one workgroup per CU
@@ -889,28 +890,31 @@ int row_waves(int64_t rows, int64_t nseg) {
   return nseg == 1 || (nseg <= 8 && rows < device_cus() * (16 / nseg)) ? 8 : 16;
 }
 
-template <int kWaves>
+template <int kWaves, int MC>
 hipError_t launch_linear_row_of(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x,
                                 const lin::FewOut& out, hipStream_t s) {
   const RowsPlan pl = rows_plan(rows, cols, kWaves, kRowsMaxWg);
   if (pl.nseg > kSegMax || pl.wpr < 1 || (cols / 64) * 32 >= (int64_t{1} << 32)) return hipErrorInvalidValue;
   const Codebook& cb = codebook(sc.fp4);
   const dim3 gd(static_cast<unsigned>(pl.grid)), bd(64 * kWaves);
-  if (sc.absmax) hipLaunchKernelGGL((k_linear_row<kWaves, false, false>), gd, bd, 0, s, packed, rows, cols, sc, x, out, cb, pl);
-  else if (sc.f8) hipLaunchKernelGGL((k_linear_row<kWaves, true, true>), gd, bd, 0, s, packed, rows, cols, sc, x, out, cb, pl);
-  else hipLaunchKernelGGL((k_linear_row<kWaves, true, false>), gd, bd, 0, s, packed, rows, cols, sc, x, out, cb, pl);
+  if (sc.absmax) hipLaunchKernelGGL((k_linear_row<kWaves, MC, false, false>), gd, bd, 0, s, packed, rows, cols, sc, x, out, cb, pl);
+  else if (sc.f8) hipLaunchKernelGGL((k_linear_row<kWaves, MC, true, true>), gd, bd, 0, s, packed, rows, cols, sc, x, out, cb, pl);
+  else hipLaunchKernelGGL((k_linear_row<kWaves, MC, true, false>), gd, bd, 0, s, packed, rows, cols, sc, x, out, cb, pl);
   return hipGetLastError();
 }
 
 }  // namespace
 
-bool linear_row_fits(int64_t cols) { return (cols / 64 + 63) / 64 <= kSegMax; }
+bool linear_row_fits(int64_t m, int64_t rows, int64_t cols) {
+  return m <= 2 && (cols / 64 + 63) / 64 <= (m == 1 ? kSegMax : 8) && (cols > 2048 || rows * cols >= (int64_t{1} << 23));
+}
 
-hipError_t launch_linear_row(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x, uint16_t* y,
-                             const Epilogue& ep, const uint16_t* u, const uint16_t* lora_b, int r, hipStream_t s) {
+hipError_t launch_linear_row(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x, int64_t m,
+                             uint16_t* y, const Epilogue& ep, const uint16_t* u, const uint16_t* lora_b, int r, hipStream_t s) {
   const lin::FewOut out = lin::few_out(rows, y, ep, u, lora_b, r);
-  return row_waves(rows, (cols / 64 + 63) / 64) == 8 ? launch_linear_row_of<8>(packed, rows, cols, sc, x, out, s)
-                                                     : launch_linear_row_of<16>(packed, rows, cols, sc, x, out, s);
+  if (m == 2) return launch_linear_row_of<8, 2>(packed, rows, cols, sc, x, out, s);
+  return row_waves(rows, (cols / 64 + 63) / 64) == 8 ? launch_linear_row_of<8, 1>(packed, rows, cols, sc, x, out, s)
+                                                     : launch_linear_row_of<16, 1>(packed, rows, cols, sc, x, out, s);
 }
 
 hipError_t launch_gemv(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x,

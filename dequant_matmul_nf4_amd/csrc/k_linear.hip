@@ -37,11 +37,21 @@ using gt::kThreads;
 
 constexpr int kBN = gt::kTileN, kBK = gt::kStep;
 constexpr int kMI = 8;
-// Which kernels take m rows of x: one row or a decode batch stream the codes past x as
-// it is; up to some hundreds, of rows wide enough for a group of steps, cut the
-// reduction (k_linear_mid.hip); this file's the rest.
-bool few(int64_t m) { return m <= 16; }
-bool mid(int64_t m, int64_t cols) { return m <= 512 && cols >= 256; }
+// Which kernels take m rows of x.  A decode batch, and as many more as leave little work for a
+// workgroup (in tiles of 16 x 16 outputs, each with about 512 columns' worth of its own): the codes
+// streamed past x as it is.
+bool few(int64_t m, int64_t rows, int64_t cols) {
+  const int64_t groups = (rows + 15) / 16, tiles = (m + 15) / 16, cus = device_cus();
+  if (tiles == 1) return true;
+  if (tiles > cus) return false;
+  const int64_t each = (groups + cus / tiles - 1) / (cus / tiles);
+  return each * (cols + 512) <= 40960;
+}
+// Up to about 96 of this file's tiles, fewer of short rows: the kernel that cuts the reduction (k_linear_mid.hip).
+bool mid(int64_t m, int64_t rows, int64_t cols) {
+  const int64_t most = cols >= 3584 ? 96 : 40 + cols / 64;
+  return cols >= 256 && m <= 65536 && m <= (most * 65536 + rows - 1) / rows;
+}
 constexpr int kBM = 32 * kMI;
 constexpr int kStageBytes = gt::act_stage_bytes<kBM>();
 constexpr int kTurnRows = 64;
@@ -373,7 +383,7 @@ struct Workspace {
 Workspace workspace_of(int64_t m, int64_t rows, int64_t cols, int r) {
   const auto round = [](size_t n) { return (n + 255) & ~size_t(255); };
   Workspace w{};
-  if (few(m)) {
+  if (few(m, rows, cols)) {
     w.bytes = r > 0 ? round(static_cast<size_t>(m) * gemm_lora_cols(r) * sizeof(uint16_t)) : 0;
     return w;
   }
@@ -382,7 +392,7 @@ Workspace workspace_of(int64_t m, int64_t rows, int64_t cols, int r) {
   w.u = w.we + round(static_cast<size_t>(rows) * sizeof(int32_t));
   w.part = w.u + (r > 0 ? round(static_cast<size_t>(m) * gemm_lora_cols(r) * sizeof(uint16_t)) : 0);
   w.bytes = w.part;
-  if (mid(m, cols)) {
+  if (mid(m, rows, cols)) {
     const MidPlan p = mid_plan(m, rows, cols);
     if (p.splits > 1) w.bytes += round(static_cast<size_t>(p.splits) * m * rows * sizeof(float));
   }
@@ -403,8 +413,8 @@ hipError_t launch_linear(const uint8_t* packed, int64_t rows, int64_t cols, Scal
   uint16_t* const u = reinterpret_cast<uint16_t*>(w8 + at.u);
   if (r > 0)
     if (hipError_t e = launch_lora_u(x, lora_a, m, cols, r, lora_scale, u, s)) return e;
-  if (m == 1 && linear_row_fits(cols)) return launch_linear_row(packed, rows, cols, sc, x, y, ep, u, lora_b, r, s);
-  if (few(m)) return launch_linear_few(packed, rows, cols, sc, x, m, y, ep, u, lora_b, r, s);
+  if (linear_row_fits(m, rows, cols)) return launch_linear_row(packed, rows, cols, sc, x, m, y, ep, u, lora_b, r, s);
+  if (few(m, rows, cols)) return launch_linear_few(packed, rows, cols, sc, x, m, y, ep, u, lora_b, r, s);
   LinearArgs a{};
   a.packed = packed; a.rows = rows; a.cols = cols; a.sc = sc; a.m = m; a.y = y; a.ep = ep;
   a.x = reinterpret_cast<const uint16_t*>(w8);
@@ -419,7 +429,7 @@ hipError_t launch_linear(const uint8_t* packed, int64_t rows, int64_t cols, Scal
   a.r = r;
   a.r_pad = (r + 15) / 16 * 16;
   a.kl = static_cast<int>(gemm_lora_cols(r));
-  if (mid(m, cols))
+  if (mid(m, rows, cols))
     return launch_linear_mid(mid_plan(m, rows, cols), packed, rows, cols, sc, a.x, a.xe, a.we, m, y, ep, a.u, lora_b, r,
                              reinterpret_cast<float*>(w8 + at.part), s);
   const int64_t tiles = ((rows + kBN - 1) / kBN) * ((m + kBM - 1) / kBM);

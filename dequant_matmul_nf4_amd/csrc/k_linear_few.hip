@@ -1,63 +1,344 @@
-// A layer's product with its epilogue for a decode batch (up to 32 rows of x): the
-// streaming walk over the codes that the product grouped by expert takes for few
-// rows (skinny_walk.h, skinny_tile.h), one weight, with the epilogue where the
-// waves' sums have met.  Levels enter in float16, x exactly (scaled by a power of two
-// per row and up to 512 columns), scales in float32 on the blocks' sums.
+// A layer's product with its epilogue for a decode batch: tiles of up to 16 rows of x.
 #include "linear_epilogue.h"
 #include "linear_f16.h"
-#include "skinny_walk.h"
+#include "skinny_tile.h"
 
 namespace nf4i {
 namespace {
 
+using sk::floatx4;
+using sk::u32x4;
+
+constexpr int kWaves = 16;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kRows = 16;    // of the weight and of x per product
+constexpr int kNb = 4;       // blocks of a weight row per step
+constexpr int kCopies = 64;  // of the level table (64 KB): each lane has its own, no two meet in a bank
+
 struct FewArgs {
-  sk::WalkArgs walk;
+  const uint8_t* packed;
+  int64_t rows;
+  Scales sc;
+  Codebook cb;
   const uint16_t* x;   // [m][cols]
   int64_t m;
+  int nblk;            // blocks of a weight row
+  int ks, rs, segs;    // waves that share a group's columns, groups at a time (a power of two), steps of a wave
+  int64_t each, more;  // groups of a workgroup; the first `more` workgroups take one more
   lin::FewOut out;
 };
 
-struct FewJob {
-  const FewArgs& a;
-  struct Tile {
-    int64_t e, row0;
-    int cnt;
-  };
-  __device__ __forceinline__ int64_t tiles() const { return (a.m + sk::kRows - 1) / sk::kRows; }
-  __device__ __forceinline__ Tile tile(int64_t tid) const {
-    const int64_t row0 = tid * sk::kRows;
-    return Tile{0, row0, static_cast<int>(a.m - row0 < sk::kRows ? a.m - row0 : sk::kRows)};
-  }
-  __device__ __forceinline__ const uint16_t* x_row(int64_t p) const { return a.x + p * a.walk.cols; }
-  __device__ __forceinline__ void store(int64_t p, int64_t row, float v) const { a.out.store(p, row, v); }
+// LDS of a wave: x, then each step's codes in operand order; the scales of a step.
+constexpr int kStage = 4096;
+constexpr int kLoads = 2;  // 16-byte loads of a lane per step
+
+template <bool kDQ>
+struct Step {
+  u32x4 c[kLoads];  // rows 8 i + lane / 8
+  int8_t q;         // of row lane / 4, block lane % 4: second-level code and its group's scale, or the absmax
+  float s;
 };
 
-template <bool kDQ, bool kF8, bool kOnce>
-__global__ __launch_bounds__(sk::kThreads, 2) void k_linear_few(FewArgs a) {
-  __shared__ sk::WalkLds<4, kF8> lds;
-  sk::walk<kDQ, kF8, 4, kOnce>(a.walk, lds, FewJob{a});
+// Codes of 16 rows x 256 columns: row r holds 16-byte piece p at slot p ^ (r % 8) of its 128 bytes.
+__device__ __forceinline__ int code_row(int i, int lane) { return 8 * i + (lane >> 3); }
+__device__ __forceinline__ int code_piece(int i, int lane) { return (lane & 7) ^ (code_row(i, lane) & 7); }
+__device__ __forceinline__ uint32_t code_slot(int row, int piece) {
+  return static_cast<uint32_t>(row * 128 + ((piece ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ uint32_t half_pair(float a, float b) {
+  typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, half2_t{static_cast<_Float16>(a), static_cast<_Float16>(b)});
+}
+// Two bf16 values times a power of two (one instruction each).
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t v, float f) {
+  return half_pair(__builtin_fmaf(bf16_to_f32(v & 0xFFFFu), f, 0.0f), __builtin_fmaf(__uint_as_float(v & 0xFFFF0000u), f, 0.0f));
+}
+
+// The level pairs of a lane's 8 code bytes: one permute puts a byte above the
+// lane's copy (an entry is 256 bytes), one LDS read brings the pair.
+__device__ __forceinline__ void look_up(u32x4 (&t)[2], const uint2& w, const char* tab, uint32_t slot) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t at = __builtin_amdgcn_perm(c < 4 ? w.x : w.y, slot, 0x0C0C0000u | ((4u + (c & 3)) << 8));
+    t[c >> 2][c & 3] = *reinterpret_cast<const uint32_t*>(tab + at);
+  }
+}
+
+// kG: groups of 16 weight rows a wave takes per batch, x being read once for all of them.
+template <bool kDQ, bool kF8, int kG>
+__global__ __launch_bounds__(kThreads, 4) void k_linear_few(FewArgs a) {
+  __shared__ __attribute__((aligned(16))) uint32_t tab[256 * kCopies];
+  __shared__ __attribute__((aligned(16))) char lds[kWaves][kStage];
+  __shared__ __attribute__((aligned(16))) float scales[kWaves][kRows * kNb];
+  __shared__ float rtab[kF8 ? 256 : 1];
+  static_assert(kG * 1024 <= kStage, "a wave's partial tiles take its codes' place");
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ln = lane & 15, g = lane >> 4;
+  const uint32_t level = half_pair(a.cb.level[ln], 0.0f);
+  const float mean = kDQ ? *a.sc.mean : 0.0f;
+  const int64_t w = blockIdx.x;
+  const int ng = static_cast<int>(a.each + (w < a.more ? 1 : 0));  // groups w, w + gridDim.x, ..
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * kRows;   // of x
+  const int cnt = static_cast<int>(a.m - row0 < kRows ? a.m - row0 : kRows);
+  int rw = 0;  // the wave's share of the groups, of the columns
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i) rw += wave >= i * a.ks ? 1 : 0;
+  const int kw = wave - rw * a.ks;
+  const int batch = a.rs * kG;
+  const bool live = rw < a.rs && rw < ng;
+  const uint32_t nblk = static_cast<uint32_t>(a.nblk), row_bytes = nblk * 32;
+  const int first = kw * a.segs * kNb;  // the wave's first block
+  const int span = a.nblk - first < a.segs * kNb ? a.nblk - first : a.segs * kNb;  // its blocks
+  const int nseg = (span + kNb - 1) / kNb;
+  const char* tabc = reinterpret_cast<const char*>(tab);
+  char* stage = lds[wave];
+  float* scl = scales[wave];
+  const uint32_t slot = static_cast<uint32_t>(lane) << 2;
+  // every load's lanes lie side by side in a few lines (one whose every lane is in another line
+  // takes the address unit a clock for each)
+  const int sn = lane >> 2, sj = lane & 3;
+  uint32_t coff[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) coff[i] = code_row(i, lane) * row_bytes + 16 * code_piece(i, lane);
+  const uint32_t soff = sn * nblk + sj;
+  const char* const x0 = reinterpret_cast<const char*>(a.x + (row0 * a.nblk + first) * 64);
+
+  auto load_step = [&](Step<kDQ>& st, int k, int seg) {
+    const bool wanted = k < ng;
+    const int64_t group = w + static_cast<int64_t>(wanted ? k : 0) * gridDim.x;
+    const int64_t left = a.rows - group * kRows;
+    const int nb = span - seg * kNb;
+    const int64_t b0 = group * kRows * a.nblk + first + seg * kNb;
+    uint32_t off[kLoads], so = soff;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) off[i] = coff[i];
+    if (left < kRows || nb < kNb) {  // what lies past the last repeats it
+      const int l2 = opaque(lane), rows = left < kRows ? static_cast<int>(left) : kRows, blocks = nb < kNb ? nb : kNb;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int row = code_row(i, l2), piece = code_piece(i, l2);
+        off[i] = (row < rows ? row : rows - 1) * row_bytes + 16 * (piece < 2 * blocks ? piece : 2 * blocks - 1);
+      }
+      const int row = l2 >> 2, j = l2 & 3;
+      so = (row < rows ? row : rows - 1) * nblk + (j < blocks ? j : blocks - 1);
+    }
+    const uint32_t keep = wanted ? ~0u : 0u;  // no branch around a load; one that is not wanted reads one place
+    const uint8_t* codes = a.packed + b0 * 32;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) st.c[i] = *reinterpret_cast<const u32x4*>(codes + (off[i] & keep));
+    so &= keep;
+    if constexpr (kDQ) {
+      st.q = (a.sc.q + b0)[so];
+      st.s = a.sc.absmax2[(b0 + so) >> 8];
+    } else {
+      st.s = (a.sc.absmax + b0)[so];
+    }
+  };
+
+  u32x4 xv[kNb][2];
+  floatx4 back;  // the powers of two that scale the sums of x rows 4 g .. back
+  auto fetch_x = [&](int seg) {
+    // 256 bytes of 4 rows per load; load i of a half takes row 4 i + g, the piece that belongs in
+    // slot ln of it.  Rows past the tile's repeat its last and are not stored.  The offsets are made
+    // here: kept, they take registers that the steps want
+    const int l2 = opaque(lane), last = 8 * (span - seg * kNb) - 1;
+    const char* p = x0 + seg * (kNb * 128);
+    uint32_t off[4], at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = sk::code_row(i, l2);
+      off[i] = static_cast<uint32_t>(row < cnt ? row : cnt - 1) * (nblk * 128);
+      at[i] = sk::code_piece(i, l2);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int piece = 16 * c + static_cast<int>(at[i]);
+        xv[2 * c + (i >> 1)][i & 1] = *reinterpret_cast<const u32x4*>(p + (off[i] + 16 * (piece < last ? piece : last)));
+      }
+  };
+  auto convert_x = [&](int seg) {
+    // turned in the wave's LDS: lane (row ln, g) takes columns 16 g .. + 15 of each block
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4*>(stage + i * 1024 + lane * 16) = xv[2 * c + (i >> 1)][i & 1];
+      sk::wave_lds_order();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        xv[2 * c + (i >> 1)][i & 1] = *reinterpret_cast<const u32x4*>(stage + sk::slot_of(ln, 8 * (i >> 1) + 2 * g + (i & 1)));
+      sk::wave_lds_order();
+    }
+    // the largest of the row's magnitudes in the segment, as bfloat16 bits
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    const int nb = span - seg * kNb;
+    u16x2 top2 = {0, 0};
+#pragma unroll
+    for (int b = 0; b < kNb; ++b)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) top2 = __builtin_elementwise_max(top2, __builtin_bit_cast(u16x2, xv[b][u][c] & 0x7FFF7FFFu));
+    uint32_t top = static_cast<uint32_t>(top2.x > top2.y ? top2.x : top2.y) << 16;
+#pragma unroll
+    for (int off = 16; off < 64; off <<= 1) {
+      const uint32_t o = __shfl_xor(top, off, 64);
+      top = o > top ? o : top;
+    }
+    // 2^e <= top < 2^(e + 1): the row times 2^(14 - e), its sums times 2^(e - 14).  The exponent
+    // is kept in -112 .. 127, where both factors are normal numbers
+    const int e = static_cast<int>(top >> 23) - 127 < -112 ? -112 : static_cast<int>(top >> 23) - 127;
+    const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+#pragma unroll
+    for (int b = 0; b < kNb; ++b) {
+      const float f = b < nb ? up : 0.0f;  // zeros past the columns' end
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) xv[b][u][c] = scaled_pair(xv[b][u][c], f);
+    }
+    const float down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) back[i] = __shfl(down, 4 * g + i, 64);  // lane 4 g + i holds row 4 g + i
+  };
+
+  // two steps on their way in two register sets: step p of a batch is group p % kG of segment p / kG
+  Step<kDQ> set[2];
+  auto load_at = [&](Step<kDQ>& st, int base, int seg, int gi) {
+    if (seg >= nseg) {
+      seg -= nseg;
+      base += batch;
+    }
+    load_step(st, base + gi * a.rs + rw, seg < nseg ? seg : 0);
+  };
+  auto multiply = [&](floatx4& acc) {
+    sk::wave_lds_order();
+    const floatx4 f = *reinterpret_cast<const floatx4*>(scl + ln * kNb);
+    floatx4 sum = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    uint2 cw[kNb];
+#pragma unroll
+    for (int b = 0; b < kNb; ++b) cw[b] = *reinterpret_cast<const uint2*>(stage + code_slot(ln, 2 * b + (g >> 1)) + 8 * (g & 1));
+    u32x4 lk[2][2];
+    look_up(lk[0], cw[0], tabc, slot);
+#pragma unroll
+    for (int b = 0; b < kNb; ++b) {
+      // the lookups of block b + 1 on their way while block b is multiplied
+      if (b + 1 < kNb) look_up(lk[(b + 1) & 1], cw[b + 1], tabc, slot);
+      __builtin_amdgcn_sched_barrier(0);
+      floatx4 d = sk::mfma<true>(xv[b][0], lk[b & 1][0], floatx4{0.0f, 0.0f, 0.0f, 0.0f});
+      d = sk::mfma<true>(xv[b][1], lk[b & 1][1], d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] = fmaf(f[b], d[i], sum[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = fmaf(back[i], sum[i], acc[i]);
+    sk::wave_lds_order();
+  };
+  auto stepped = [&](Step<kDQ>& st, floatx4& acc, int base, int seg, int gi) {
+    const bool here = base + gi * a.rs + rw < ng;
+    if (here) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) *reinterpret_cast<u32x4*>(stage + i * 1024 + lane * 16) = st.c[i];
+      if constexpr (kDQ) scl[lane] = (kF8 ? rtab[st.q & 0xFF] : div127(st.q)) * st.s + mean;  // a_hat, three roundings
+      else scl[lane] = st.s;
+    }
+    // the next segment's x goes out ahead of the codes after it: loads return in order
+    const bool turn = gi == kG - 1 && nseg > 1;
+    if (!turn) load_at(st, base, seg + (gi + 2) / kG, (gi + 2) % kG);
+    if (here) multiply(acc);
+    if (turn) {
+      fetch_x(seg + 1 < nseg ? seg + 1 : 0);
+      load_at(st, base, seg + (gi + 2) / kG, (gi + 2) % kG);
+    }
+  };
+  if (live) {
+    fetch_x(0);
+    load_at(set[0], 0, 0, 0);
+    load_at(set[1], 0, 1 / kG, 1 % kG);
+  }
+  {
+    // Entry e of the table is levels e / 16 and e % 16; 16 lanes write an entry's copies, so
+    // a pass of the threads writes 64 entries, a lane those of one second level.
+    const uint32_t second = static_cast<uint32_t>(__shfl(static_cast<int>(level), (4 * wave + g) & 15, 64)) << 16;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const uint32_t e = static_cast<uint32_t>(__builtin_amdgcn_readlane(level, 4 * p + (wave >> 2))) | second;
+      *reinterpret_cast<u32x4*>(tab + p * 4 * kThreads + 4 * threadIdx.x) = u32x4{e, e, e, e};
+    }
+    if constexpr (kF8)
+      if (threadIdx.x < 256) rtab[threadIdx.x] = kE4m3Ratio.v[threadIdx.x];
+    sk::lds_barrier();
+  }
+  for (int base = 0; base < ng; base += batch) {
+    if (live) {
+      floatx4 acc[kG];
+#pragma unroll
+      for (int i = 0; i < kG; ++i) acc[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+      auto segment = [&](int seg, int odd) {
+        if (nseg > 1 || base == 0) convert_x(seg);
+#pragma unroll
+        for (int gi = 0; gi < kG; ++gi) stepped(set[(odd * kG + gi) & 1], acc[gi], base, seg, gi);
+      };
+      for (int seg = 0; seg < nseg; ++seg) {
+        segment(seg, 0);
+        if constexpr (kG % 2 != 0) {
+          if (++seg < nseg) segment(seg, 1);
+        }
+      }
+      sk::wave_lds_order();
+#pragma unroll
+      for (int gi = 0; gi < kG; ++gi) *reinterpret_cast<floatx4*>(stage + (gi * 64 + lane) * 16) = acc[gi];
+    }
+    sk::lds_barrier();
+    // the waves' partial tiles, added in wave order
+    const int here = ng - base < batch ? ng - base : batch;
+    const int rs_log = __builtin_ctz(a.rs);
+    for (int t = opaque(threadIdx.x); t < here * 256; t += kThreads) {
+      const int l = t & 63, i = (t >> 6) & 3, k = t >> 8, gi = k >> rs_log, r = k & (a.rs - 1);
+      const char* from = lds[r * a.ks] + (gi * 64 + l) * 16 + 4 * i;
+      float z[1] = {*reinterpret_cast<const float*>(from)};
+      for (int q = 1; q < a.ks; ++q) z[0] += *reinterpret_cast<const float*>(from + q * kStage);
+      const int64_t row = (w + static_cast<int64_t>(base + k) * gridDim.x) * kRows + (l & 15);
+      const int xm = 4 * (l >> 4) + i;
+      if (row < a.rows && xm < cnt) a.out.store(row0 + xm, 1, row, z);
+    }
+    if constexpr (kG == 1) break;  // one batch
+    sk::lds_barrier();
+  }
 }
 
 template <bool kDQ, bool kF8>
-void launch(const FewArgs& a, hipStream_t s) {
-  const int64_t ngr = (a.walk.rows + 15) / 16, tiles = (a.m + sk::kRows - 1) / sk::kRows;
-  const int64_t want = (ngr * tiles + a.walk.pl.rs - 1) / a.walk.pl.rs;
-  int64_t grid = want < device_cus() ? want : device_cus();
-  while (ngr / grid >= (int64_t{1} << 26)) grid *= 2;
-  const dim3 gd(static_cast<unsigned>(grid)), bd(sk::kThreads);
-  if (a.walk.pl.per <= sk::kSeg) hipLaunchKernelGGL((k_linear_few<kDQ, kF8, true>), gd, bd, 0, s, a);
-  else hipLaunchKernelGGL((k_linear_few<kDQ, kF8, false>), gd, bd, 0, s, a);
+void launch(const FewArgs& a, dim3 grid, hipStream_t s) {
+  const int64_t groups = a.each + (a.more > 0 ? 1 : 0);
+  if (groups <= a.rs) hipLaunchKernelGGL((k_linear_few<kDQ, kF8, 1>), grid, dim3(kThreads), 0, s, a);
+  else if (groups <= 2 * a.rs) hipLaunchKernelGGL((k_linear_few<kDQ, kF8, 2>), grid, dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((k_linear_few<kDQ, kF8, 4>), grid, dim3(kThreads), 0, s, a);
 }
 
 }  // namespace
 
 hipError_t launch_linear_few(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x, int64_t m,
                              uint16_t* y, const Epilogue& ep, const uint16_t* u, const uint16_t* lora_b, int r, hipStream_t s) {
-  const FewArgs a{sk::WalkArgs{packed, rows, cols, sc, codebook(sc.fp4), sk::make_plan(cols)}, x, m,
-                  lin::few_out(rows, y, ep, u, lora_b, r)};
-  if (sc.absmax) launch<false, false>(a, s);
-  else if (sc.f8) launch<true, true>(a, s);
-  else launch<true, false>(a, s);
+  FewArgs a{};
+  a.packed = packed; a.rows = rows; a.sc = sc; a.cb = codebook(sc.fp4); a.x = x; a.m = m;
+  a.nblk = static_cast<int>(cols / 64);
+  const int segs = (a.nblk + kNb - 1) / kNb;
+  a.segs = (segs + kWaves - 1) / kWaves;
+  a.ks = (segs + a.segs - 1) / a.segs;
+  for (a.rs = 1; 2 * a.rs * a.ks <= kWaves; a.rs *= 2) {}
+  const int64_t ngr = (rows + kRows - 1) / kRows, tiles = (m + kRows - 1) / kRows, room = device_cus() / tiles;
+  int64_t wpt = ngr < room ? ngr : room > 0 ? room : 1;
+  while (ngr / wpt >= (int64_t{1} << 24)) wpt *= 2;
+  a.each = ngr / wpt;
+  a.more = ngr % wpt;
+  a.out = lin::few_out(rows, y, ep, u, lora_b, r);
+  const dim3 grid(static_cast<unsigned>(wpt), static_cast<unsigned>(tiles));
+  if (sc.absmax) launch<false, false>(a, grid, s);
+  else if (sc.f8) launch<true, true>(a, grid, s);
+  else launch<true, false>(a, grid, s);
   return hipGetLastError();
 }
 

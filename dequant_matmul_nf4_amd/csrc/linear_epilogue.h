@@ -57,13 +57,26 @@ __device__ __forceinline__ void apply_act(int act, float (&z)[N]) {
   }
 }
 
-// One value at `at` of the outputs.
-__device__ __forceinline__ void finish1(const Epilogue& ep, uint16_t* y, int64_t at, float z) {
-  if (ep.pre) ep.pre[at] = static_cast<uint16_t>(bf16_pair(z, 0.0f));
-  float v[1] = {z};
-  apply_act(ep.act, v);
-  if (ep.residual) v[0] += bf16_to_f32(ep.residual[at]);
-  y[at] = static_cast<uint16_t>(bf16_pair(v[0], 0.0f));
+// N values of one column, `step` apart from `at` on, the first `n` of which exist.
+template <int N>
+__device__ __forceinline__ void finish_column(const Epilogue& ep, uint16_t* y, int64_t at, int64_t step, int n, float (&z)[N]) {
+  float res[N];
+  if (ep.residual) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) res[c] = c < n ? bf16_to_f32(ep.residual[at + c * step]) : 0.0f;
+  }
+  const auto put = [&](uint16_t* to) {
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      if (c < n) to[at + c * step] = static_cast<uint16_t>(bf16_pair(z[c], 0.0f));
+  };
+  if (ep.pre) put(ep.pre);
+  apply_act(ep.act, z);
+  if (ep.residual) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) z[c] += res[c];
+  }
+  put(y);
 }
 
 // Eight consecutive values of a row, the first `left` of which exist; `whole`:
@@ -130,7 +143,8 @@ __device__ __forceinline__ bf16x8 adapter_w(const uint16_t* lb, int r, int r_pad
 // ... and eight columns of a row of (s T hi | s T lo).
 __device__ __forceinline__ bf16x8 adapter_x(const uint16_t* u, float by) { return times(*reinterpret_cast<const u32x4*>(u), by); }
 
-// What takes the sums of a few rows of x one by one: row t of x and weight row n.
+// What takes the sums of a few rows of x: N rows from t on, n of which exist, and
+// weight row `row`.
 struct FewOut {
   int64_t rows;
   uint16_t* y;
@@ -139,20 +153,29 @@ struct FewOut {
   const uint16_t* lb;  // B [rows][r]
   int r, r_pad, kl;    // 0 without adapters
 
-  __device__ __forceinline__ void store(int64_t t, int64_t n, float z) const {
-    if (r > 0) z += adapters(t, n);
-    if (ep.bias) z += ep.bias_f32 ? static_cast<const float*>(ep.bias)[n] : bf16_to_f32(static_cast<const uint16_t*>(ep.bias)[n]);
-    finish1(ep, y, t * rows + n, z);
+  template <int N>
+  __device__ __forceinline__ void store(int64_t t, int n, int64_t row, float (&z)[N]) const {
+    if (r > 0) adapters(t, n, row, z);
+    float bias[1];
+    load_bias(bias, ep, row, 1);
+#pragma unroll
+    for (int c = 0; c < N; ++c) z[c] += bias[0];
+    finish_column(ep, y, t * rows + row, rows, n, z);
   }
-  // sum_j (hi + lo)[t][j] B[n][j]
-  __device__ __forceinline__ float adapters(int64_t t, int64_t n) const {
+  // z[c] += sum_j (hi + lo)[t + c][j] B[row][j]
+  template <int N>
+  __device__ __forceinline__ void adapters(int64_t t, int n, int64_t row, float (&z)[N]) const {
     typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
     const uint16_t* h = u + t * kl;
-    const uint16_t* b = lb + n * r;
-    float s = 0.0f;
+    const uint16_t* b = lb + row * r;
     for (int j = 0; j < r; j += 8) {
-      const u32x4 hi = *reinterpret_cast<const u32x4*>(h + j), lo = *reinterpret_cast<const u32x4*>(h + r_pad + j);
-      u32x4 w = {0, 0, 0, 0};
+      u32x4 w = {0, 0, 0, 0}, hi[N], lo[N];
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        const uint16_t* hc = h + (c < n ? c : n - 1) * kl + j;
+        hi[c] = *reinterpret_cast<const u32x4*>(hc);
+        lo[c] = *reinterpret_cast<const u32x4*>(hc + r_pad);
+      }
       if (j + 8 <= r) {
         w = *reinterpret_cast<const u32x4_any*>(b + j);
       } else {
@@ -161,12 +184,13 @@ struct FewOut {
           if (j + i < r) w[i >> 1] |= static_cast<uint32_t>(b[j + i]) << (16 * (i & 1));
       }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        s = fmaf(bf16_to_f32(hi[c] & 0xFFFFu) + bf16_to_f32(lo[c] & 0xFFFFu), bf16_to_f32(w[c] & 0xFFFFu), s);
-        s = fmaf(__uint_as_float(hi[c] & 0xFFFF0000u) + __uint_as_float(lo[c] & 0xFFFF0000u), __uint_as_float(w[c] & 0xFFFF0000u), s);
-      }
+      for (int c = 0; c < N; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          z[c] = fmaf(bf16_to_f32(hi[c][k] & 0xFFFFu) + bf16_to_f32(lo[c][k] & 0xFFFFu), bf16_to_f32(w[k] & 0xFFFFu), z[c]);
+          z[c] = fmaf(__uint_as_float(hi[c][k] & 0xFFFF0000u) + __uint_as_float(lo[c][k] & 0xFFFF0000u), __uint_as_float(w[k] & 0xFFFF0000u), z[c]);
+        }
     }
-    return s;
   }
 };
 inline FewOut few_out(int64_t rows, uint16_t* y, const Epilogue& ep, const uint16_t* u, const uint16_t* lora_b, int r) {

@@ -94,11 +94,11 @@ constexpr int64_t x16_rows(int64_t m) { return (m + 31) / 32 * 32; }
 hipError_t launch_linear_prep(const uint16_t* x, int64_t m, int64_t cols, uint16_t* x16, int32_t* xe, const Scales& sc,
                               int64_t rows, int32_t* we, hipStream_t s);
 
-// The linear product of one row of x (k_gemv.hip) and of a decode batch
+// The linear product of one or two rows of x (k_gemv.hip) and of a decode batch
 // (k_linear_few.hip): x as it is, no exponents.
-bool linear_row_fits(int64_t cols);
-hipError_t launch_linear_row(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x, uint16_t* y,
-                             const Epilogue& ep, const uint16_t* u, const uint16_t* lora_b, int r, hipStream_t s);
+bool linear_row_fits(int64_t m, int64_t rows, int64_t cols);
+hipError_t launch_linear_row(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x, int64_t m,
+                             uint16_t* y, const Epilogue& ep, const uint16_t* u, const uint16_t* lora_b, int r, hipStream_t s);
 hipError_t launch_linear_few(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x, int64_t m,
                              uint16_t* y, const Epilogue& ep, const uint16_t* u, const uint16_t* lora_b, int r, hipStream_t s);
 
