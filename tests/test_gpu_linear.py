@@ -191,6 +191,25 @@ def test_same_twice_and_rows_apart(m):
         assert torch.equal(z[keep], y[keep]) and z[m // 2].isnan().all()
 
 
+# one or two rows of wide and of many-rowed weights; a decode batch over one and many groups of weight rows per
+# workgroup, one and many column segments per wave; cut reductions; whole tiles
+@pytest.mark.parametrize("m,rows,cols", [
+    (1, 1003, 4160), (2, 1003, 4160), (1, 12301, 704), (2, 12301, 704), (1, 40, 33024), (2, 40, 33024), (1, 3, 66048), (2, 9, 66048),
+    (3, 14343, 640), (16, 14343, 640), (7, 20001, 448), (3, 70001, 64), (5, 300007, 64), (11, 9001, 4416), (6, 24013, 4416),
+    (4, 24013, 1088), (2, 33, 14400), (13, 5, 33024), (9, 4099, 14400),
+    (20, 9001, 320), (37, 4099, 576), (49, 2000, 2112), (700, 33, 1088), (1100, 70, 320), (2050, 16, 64), (4100, 3, 128),
+    (17, 9001, 4416), (40, 9001, 4416), (150, 2001, 4160), (330, 2001, 4160), (600, 1999, 4160), (1000, 1003, 3648), (97, 8199, 2112), (1300, 259, 2112),
+    (300, 9007, 640), (700, 9007, 640), (513, 7001, 1088), (2500, 515, 1088), (400, 14343, 192), (5000, 70, 192)])
+def test_sizes_of_every_kernel(m, rows, cols):
+    torch = need_gpu()
+    say("linear sizes", m, rows, cols)
+    W = weight(torch, rows, cols, ("int8", "fp8", "plain")[(m + rows) % 3], fp4=m % 5 == 0)
+    x, kw = inputs(torch, m, rows, cols, "f32", residual=True, rank=(m % 4) * 5)
+    y, pre = nf4.nf4_linear(W, x, act="gelu", save_pre=True, **kw)
+    check(torch, W, x, dict(kw, act="gelu"), y, pre)
+    assert torch.equal(y, nf4.nf4_linear(W, x, act="gelu", **kw))
+
+
 def test_many_tiles():
     """More work units than compute units, the last round cut in halves, and widths of several column tiles."""
     torch = need_gpu()
