@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import operator
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -1191,37 +1192,46 @@ def nf4_expert_balance_backward(logits, counts, slots: int, coef: float, mask=No
     return dlogits
 
 
+_DTYPE_OF = operator.attrgetter("dtype")
+
+
 def _grad_list(grads, out=None):
     """(array of nf4_grad, device) of gradients that are scaled in place, or into
-    the flat tensor out, one after another."""
+    the flat tensor out, one after another.  There may be a thousand: what is
+    asked of each goes through map (a loop over them takes half as long again)."""
     torch = _torch()
+    T = torch.Tensor
     codes = {torch.float32: NF4_F32, torch.bfloat16: NF4_BF16, torch.float16: NF4_F16}
-    kinds = {(t.dtype, t.device, t.is_contiguous()) for t in grads}
-    dev = grads[0].device
-    for dtype, d, whole in kinds:
+    dtypes = list(map(_DTYPE_OF, grads))
+    kinds = set(dtypes)
+    for dtype in kinds:
         if dtype not in codes:
             raise TypeError(f"unsupported dtype {dtype}")
-        if d.type != "cuda" or not whole:
-            raise ValueError("gradients must be contiguous device tensors")
-        if d != dev:
-            raise ValueError(f"gradient on {d}, expected {dev}")
-    words = array.array("q")
+    dev, at_devices = grads[0].device, set(map(T.get_device, grads))
+    if min(at_devices) < 0 or not all(map(T.is_contiguous, grads)):
+        raise ValueError("gradients must be contiguous device tensors")
+    if len(at_devices) > 1:
+        raise ValueError(f"gradients on several devices, expected {dev}")
+    n = len(grads)
+    at, sizes = array.array("q", map(T.data_ptr, grads)), array.array("q", map(T.numel, grads))
+    kind = array.array("q", [codes[dtypes[0]]]) * n if len(kinds) == 1 else array.array("q", map(codes.__getitem__, dtypes))
+    words = array.array("q", bytes(32 * n))
+    words[0::4], words[2::4] = at, sizes
     if out is None:
-        for t in grads:
-            p, c = t.data_ptr(), codes[t.dtype]
-            words.extend((p, p, t.numel(), c | c << 32))
+        words[1::4] = at
+        pair = [c | c << 32 for c in range(3)]
+        words[3::4] = array.array("q", [pair[kind[0]]]) * n if len(kinds) == 1 else array.array("q", map(pair.__getitem__, kind))
         return words, dev
     if out.dtype not in codes:
         raise TypeError(f"unsupported dtype {out.dtype}")
-    _need("out", out, out.dtype, sum(t.numel() for t in grads), dev)
-    at, size, code = out.data_ptr(), out.element_size(), codes[out.dtype]
-    lo, hi = at, at + out.numel() * size
-    for t in grads:
-        p, n, c = t.data_ptr(), t.numel(), codes[t.dtype]
-        if p < hi and p + n * (4 if c == NF4_F32 else 2) > lo and n and (p != at or c != code):
+    _need("out", out, out.dtype, sum(sizes), dev)
+    to, size, code = out.data_ptr(), out.element_size(), codes[out.dtype]
+    lo, hi = to, to + out.numel() * size
+    for i, (p, c, k) in enumerate(zip(at, sizes, kind)):
+        if p < hi and p + c * (4 if k == NF4_F32 else 2) > lo and c and (p != to or k != code):
             raise ValueError("out shares memory with a gradient that does not lie exactly in its place")
-        words.extend((p, at, n, c | code << 32))
-        at += n * size
+        words[4 * i + 1], words[4 * i + 3] = to, k | code << 32
+        to += c * size
     return words, dev
 
 
