@@ -19,6 +19,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kCols = 8;        // columns of a thread
 constexpr int kUnroll = 4;      // rows on their way at a time
+constexpr int kTail = 2;        // of them where the columns are taken one by one
+constexpr int kMaxTx = 64;      // threads across the columns
 constexpr int kMaxChunks = 256;
 
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
@@ -26,7 +28,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 struct Plan {
-  int tx;            // threads across the columns (a power of two up to 256)
+  int tx;            // threads across the columns (a power of two up to kMaxTx)
   int ctiles;        // workgroups across the columns
   int chunks;        // workgroups along the rows
   int64_t per;       // rows of a chunk
@@ -36,7 +38,7 @@ Plan make_plan(int64_t m, int64_t rows) {
   Plan p{};
   const int64_t vec = (rows + kCols - 1) / kCols;
   p.tx = 1;
-  while (p.tx < kThreads && p.tx < vec) p.tx *= 2;
+  while (p.tx < kMaxTx && p.tx < vec) p.tx *= 2;
   const int64_t ctiles = (vec + p.tx - 1) / p.tx;
   const int ty = kThreads / p.tx;
   // about 8 workgroups per compute unit of a full chip, each with at least kUnroll rows per thread
@@ -107,16 +109,30 @@ __global__ __launch_bounds__(kThreads) void k_act_backward(const uint16_t* dy, c
       one(d, z, at);
     }
   } else {
-    for (int64_t t = t0 + yy; t < t1; t += ty)
+    // the columns past the last whole 8: all that a few rows need is asked for before the first is stored
+    // (dz may be dy, so the compiler would not; one at a time these threads took longer than all others)
+    for (int64_t t = t0 + yy; t < t1; t += kTail * ty) {
+      uint16_t d[kTail][kCols] = {}, z[kTail][kCols] = {};
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        if (c >= left) break;
-        const int64_t at = t * rows + col + c;
-        float v = bf16_to_f32(dy[at]);
-        if constexpr (A != kActNone) v *= act_slope<A>(bf16_to_f32(pre[at]));
-        sum[c] += v;
-        if constexpr (kDz) dz[at] = static_cast<uint16_t>(pair(v, 0.0f));
-      }
+      for (int u = 0; u < kTail; ++u)
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          if (c < left && t + u * ty < t1) {
+            const int64_t at = (t + u * ty) * rows + col + c;
+            d[u][c] = dy[at];
+            if constexpr (A != kActNone) z[u][c] = pre[at];
+          }
+#pragma unroll
+      for (int u = 0; u < kTail; ++u)
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          if (c < left && t + u * ty < t1) {
+            float v = bf16_to_f32(d[u][c]);
+            if constexpr (A != kActNone) v *= act_slope<A>(bf16_to_f32(z[u][c]));
+            if constexpr (kBias) sum[c] += v;
+            if constexpr (kDz) dz[(t + u * ty) * rows + col + c] = static_cast<uint16_t>(pair(v, 0.0f));
+          }
+    }
   }
 
   if constexpr (kBias) {

@@ -45,12 +45,31 @@ __device__ __forceinline__ float from16(uint32_t bits, int type) {
   return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits)));
 }
 
-// kV logits of a row from column c on; columns past the row's end are -inf.
+// kV logits of a row from column c on; columns past the row's end are -inf.  kWhole: rows of
+// a multiple of kV, so that no lane's columns are cut and no branch stands around a load (with
+// one, every load is waited for before the next is asked for).
 template <int T>
 struct Row {
   static constexpr int kV = T == kF32 ? 4 : 8;
+  template <bool kWhole>
   static __device__ __forceinline__ void load(float (&v)[kV], const void* base, int64_t row, int experts, int c) {
-    if constexpr (T == kF32) {
+    if constexpr (kWhole) {
+      const int64_t at = row * experts + (c < experts ? c : 0);
+      if constexpr (T == kF32) {
+        const u32x4_any4 w = *reinterpret_cast<const u32x4_any4*>(static_cast<const float*>(base) + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+      } else {
+        const u32x4_any w = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(base) + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[2 * i] = from16(w[i] & 0xFFFFu, T);
+          v[2 * i + 1] = from16(w[i] >> 16, T);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kV; ++i) v[i] = c < experts ? v[i] : -INFINITY;
+    } else if constexpr (T == kF32) {
       const float* p = static_cast<const float*>(base) + row * experts + c;
       if (c + kV <= experts) {
         const u32x4_any4 w = *reinterpret_cast<const u32x4_any4*>(p);
@@ -110,11 +129,26 @@ struct Row {
   }
 };
 
-template <int L>
+// The value of another lane: within 16 lanes by the operand's own lane patterns (pairs and
+// fours exchanged; halves of 8 and rows of 16 mirrored, which is as good once all lanes of a
+// half agree), beyond through LDS.  With every step through LDS its latency was most of a row's time.
+template <int off>
+__device__ __forceinline__ float across(float v) {
+  constexpr int kPattern = off == 1 ? 0xB1 : off == 2 ? 0x4E : off == 4 ? 0x141 : 0x140;
+  if constexpr (off < 16)
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kPattern, 0xF, 0xF, true));
+  else
+    return __shfl_xor(v, off, 64);
+}
+template <int L, int off = 1>
 __device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-  for (int off = 1; off < L; off <<= 1) v += __shfl_xor(v, off, 64);
-  return v;
+  if constexpr (off < L) return lanes_sum<L, 2 * off>(v + across<off>(v));
+  else return v;
+}
+template <int L, int off = 1>
+__device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (off < L) return lanes_max<L, 2 * off>(fmaxf(v, across<off>(v)));
+  else return v;
 }
 
 // The softmax of a group's row in place; rows without any probability become zeros.
@@ -125,7 +159,7 @@ __device__ __forceinline__ void softmax(float (&v)[IT][kV]) {
   for (int it = 0; it < IT; ++it)
 #pragma unroll
     for (int i = 0; i < kV; ++i) top = fmaxf(top, v[it][i]);
-  top = group_max<L>(top);
+  top = lanes_max<L>(top);
   const float base = top == -INFINITY ? 0.0f : top;
   float sum = 0.0f;
 #pragma unroll
@@ -174,7 +208,7 @@ template <int T, int IT, int L>
 __global__ __launch_bounds__(kThreads) void k_balance(Args a) {
   constexpr int kV = Row<T>::kV, kStep = L * kV;
   constexpr int kRows = 64 / L;      // rows of a wave at a time
-  constexpr int kUnroll = IT > 1 ? 1 : 4;
+  constexpr int kUnroll = IT > 1 ? 1 : kV > 4 ? 8 : 4;
   __shared__ float probs[kWaves][IT * kStep];
   __shared__ int32_t hist[4][kMaxE + 1];
   __shared__ double red[kWaves];
@@ -185,36 +219,69 @@ __global__ __launch_bounds__(kThreads) void k_balance(Args a) {
   __syncthreads();
 
   const int64_t t0 = a.tokens * blockIdx.x / gridDim.x, t1 = a.tokens * (blockIdx.x + 1) / gridDim.x;
+  // a thread's first slots and whether their tokens are kept, asked for before the logits
+  constexpr int kIds = 4;
+  const int64_t slots0 = t0 * a.slots, slots1 = t1 * a.slots;
+  const int turn = kThreads / a.slots, rest = kThreads - turn * a.slots;  // a thread's next slot is of the token `turn` on, or the next
+  int64_t slot = slots0 + threadIdx.x, token = t0 + threadIdx.x / a.slots;
+  int place = threadIdx.x % a.slots;
+  auto next_ids = [&](int (&id)[kIds]) {
+#pragma unroll
+    for (int i = 0; i < kIds; ++i) {
+      const bool have = slot < slots1;
+      const int got = a.ids[have ? slot : 0];
+      const bool keep = have && (!a.mask || a.mask[token < t1 ? token : 0]);
+      id[i] = keep && got >= 0 && got < E ? got : -1;
+      slot += kThreads;
+      token += turn;
+      place += rest;
+      if (place >= a.slots) {
+        place -= a.slots;
+        ++token;
+      }
+    }
+  };
+  int id[kIds];
+  next_ids(id);
   float sum[IT][kV];
 #pragma unroll
   for (int it = 0; it < IT; ++it)
 #pragma unroll
     for (int i = 0; i < kV; ++i) sum[it][i] = 0.0f;
-  for (int64_t t = t0 + (wave * kUnroll) * kRows; t < t1; t += kWaves * kUnroll * kRows) {
-    float v[kUnroll][IT][kV];
-    bool live[kUnroll];
+  const uint8_t* const mask = a.mask ? a.mask : reinterpret_cast<const uint8_t*>(a.ids);  // read either way
+  auto rows = [&](auto whole) {
+    for (int64_t t = t0 + (wave * kUnroll) * kRows; t < t1; t += kWaves * kUnroll * kRows) {
+      float v[kUnroll][IT][kV];
+      bool live[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t r = t + u * kRows + g;
-      live[u] = r < t1 && (!a.mask || a.mask[r < t1 ? r : t1 - 1]);
+      for (int u = 0; u < kUnroll; ++u) {
+        const int64_t r = t + u * kRows + g;
+        const uint8_t keep = mask[!a.mask ? 0 : r < t1 ? r : t1 - 1];
+        live[u] = r < t1 && (!a.mask || keep);
 #pragma unroll
-      for (int it = 0; it < IT; ++it) Row<T>::load(v[u][it], a.logits, r < t1 ? r : t1 - 1, E, it * kStep + l * kV);
+        for (int it = 0; it < IT; ++it) Row<T>::template load<decltype(whole)::value>(v[u][it], a.logits, r < t1 ? r : t1 - 1, E, it * kStep + l * kV);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        softmax<kV, IT, L>(v[u]);
+#pragma unroll
+        for (int it = 0; it < IT; ++it)
+#pragma unroll
+          for (int i = 0; i < kV; ++i) sum[it][i] += live[u] ? v[u][it][i] : 0.0f;
+      }
     }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      softmax<kV, IT, L>(v[u]);
-#pragma unroll
-      for (int it = 0; it < IT; ++it)
-#pragma unroll
-        for (int i = 0; i < kV; ++i) sum[it][i] += live[u] ? v[u][it][i] : 0.0f;
-    }
-  }
+  };
+  if (E % kV == 0) rows(std::true_type{});
+  else rows(std::false_type{});
   // the counts: four tables, so that fewer of a wave's lanes meet in one place
   int kept = 0;
   for (int64_t t = t0 + threadIdx.x; t < t1; t += kThreads) kept += !a.mask || a.mask[t];
-  for (int64_t i = t0 * a.slots + threadIdx.x; i < t1 * a.slots; i += kThreads) {
-    const int id = a.ids[i];
-    if (id >= 0 && id < E && (!a.mask || a.mask[i / a.slots])) atomicAdd(&hist[threadIdx.x & 3][id], 1);
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < kIds; ++i)
+      if (id[i] >= 0) atomicAdd(&hist[threadIdx.x & 3][id[i]], 1);
+    if (slot >= slots1) break;
+    next_ids(id);
   }
   if (kept) atomicAdd(&hist[threadIdx.x & 3][E], kept);
   // a lane's columns over the wave's rows, then over the waves
@@ -366,35 +433,41 @@ __global__ __launch_bounds__(256) void k_balance_backward(BackArgs a) {
   const double dl = a.dloss ? static_cast<double>(*a.dloss) : 1.0;
   const float by = kept > 0 ? static_cast<float>(dl * a.coef * E / (kept * kept * a.slots)) : 0.0f;
 
-  for (int64_t t = at * kUnroll * kRows; t < a.tokens; t += waves * kUnroll * kRows) {
-    float v[kUnroll][IT][kV];
-    bool live[kUnroll];
+  const uint8_t* const mask = a.mask ? a.mask : reinterpret_cast<const uint8_t*>(a.counts);  // read either way
+  auto rows = [&](auto whole) {
+    for (int64_t t = at * kUnroll * kRows; t < a.tokens; t += waves * kUnroll * kRows) {
+      float v[kUnroll][IT][kV];
+      bool live[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t r = t + u * kRows + g, rc = r < a.tokens ? r : a.tokens - 1;
-      live[u] = !a.mask || a.mask[rc];
+      for (int u = 0; u < kUnroll; ++u) {
+        const int64_t r = t + u * kRows + g, rc = r < a.tokens ? r : a.tokens - 1;
+        const uint8_t keep = mask[a.mask ? rc : 0];
+        live[u] = !a.mask || keep;
 #pragma unroll
-      for (int it = 0; it < IT; ++it) Row<T>::load(v[u][it], a.logits, rc, E, it * kStep + l * kV);
-    }
+        for (int it = 0; it < IT; ++it) Row<T>::template load<decltype(whole)::value>(v[u][it], a.logits, rc, E, it * kStep + l * kV);
+      }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t r = t + u * kRows + g;
-      softmax<kV, IT, L>(v[u]);
-      float dot = 0.0f;
+      for (int u = 0; u < kUnroll; ++u) {
+        const int64_t r = t + u * kRows + g;
+        softmax<kV, IT, L>(v[u]);
+        float dot = 0.0f;
 #pragma unroll
-      for (int it = 0; it < IT; ++it)
+        for (int it = 0; it < IT; ++it)
 #pragma unroll
-        for (int i = 0; i < kV; ++i) dot = fmaf(v[u][it][i], w[it][i], dot);
-      dot = lanes_sum<L>(dot);
+          for (int i = 0; i < kV; ++i) dot = fmaf(v[u][it][i], w[it][i], dot);
+        dot = lanes_sum<L>(dot);
 #pragma unroll
-      for (int it = 0; it < IT; ++it) {
+        for (int it = 0; it < IT; ++it) {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) v[u][it][i] = live[u] ? by * v[u][it][i] * (w[it][i] - dot) : 0.0f;
-        const int col = it * kStep + l * kV;
-        if (r < a.tokens && col < E) Row<T>::store(v[u][it], a.dlogits, r, E, col);
+          for (int i = 0; i < kV; ++i) v[u][it][i] = live[u] ? by * v[u][it][i] * (w[it][i] - dot) : 0.0f;
+          const int col = it * kStep + l * kV;
+          if (r < a.tokens && col < E) Row<T>::store(v[u][it], a.dlogits, r, E, col);
+        }
       }
     }
-  }
+  };
+  if (E % kV == 0) rows(std::true_type{});
+  else rows(std::false_type{});
 }
 
 // Calls f<T, IT, L>() for a row of `experts` logits of `type`.
