@@ -65,13 +65,22 @@ __device__ __forceinline__ void look_up(u32x4 (&t)[2], const uint2& w, const cha
   }
 }
 
+// The table comes first: at address 0 the permute makes a lookup's whole address.
+template <bool kF8>
+struct __attribute__((aligned(16))) FewLds {
+  uint32_t tab[256 * kCopies];
+  char stage[kWaves][kStage];
+  float scales[kWaves][kRows * kNb];
+  float rtab[kF8 ? 256 : 1];
+};
+
 // kG: groups of 16 weight rows a wave takes per batch, x being read once for all of them.
 template <bool kDQ, bool kF8, int kG>
 __global__ __launch_bounds__(kThreads, 4) void k_linear_few(FewArgs a) {
-  __shared__ __attribute__((aligned(16))) uint32_t tab[256 * kCopies];
-  __shared__ __attribute__((aligned(16))) char lds[kWaves][kStage];
-  __shared__ __attribute__((aligned(16))) float scales[kWaves][kRows * kNb];
-  __shared__ float rtab[kF8 ? 256 : 1];
+  __shared__ FewLds<kF8> shared;
+  auto& tab = shared.tab;
+  auto& lds = shared.stage;
+  auto& rtab = shared.rtab;
   static_assert(kG * 1024 <= kStage, "a wave's partial tiles take its codes' place");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -94,7 +103,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_linear_few(FewArgs a) {
   const int nseg = (span + kNb - 1) / kNb;
   const char* tabc = reinterpret_cast<const char*>(tab);
   char* stage = lds[wave];
-  float* scl = scales[wave];
+  float* scl = shared.scales[wave];
   const uint32_t slot = static_cast<uint32_t>(lane) << 2;
   // every load's lanes lie side by side in a few lines (one whose every lane is in another line
   // takes the address unit a clock for each)
