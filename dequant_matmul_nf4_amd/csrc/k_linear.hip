@@ -411,24 +411,28 @@ hipError_t launch_linear(const uint8_t* packed, int64_t rows, int64_t cols, Scal
   const Workspace at = workspace_of(m, rows, cols, r);
   char* const w8 = static_cast<char*>(ws);
   uint16_t* const u = reinterpret_cast<uint16_t*>(w8 + at.u);
-  if (r > 0)
-    if (hipError_t e = launch_lora_u(x, lora_a, m, cols, r, lora_scale, u, s)) return e;
-  if (linear_row_fits(m, rows, cols)) return launch_linear_row(packed, rows, cols, sc, x, m, y, ep, u, lora_b, r, s);
-  if (few(m, rows, cols)) return launch_linear_few(packed, rows, cols, sc, x, m, y, ep, u, lora_b, r, s);
+  const AdapterU ad{lora_a, r, (r + 15) / 16 * 16, static_cast<int>(gemm_lora_cols(r)), lora_scale, u};
+  const bool row = linear_row_fits(m, rows, cols);
+  if (row || few(m, rows, cols)) {
+    if (r > 0)
+      if (hipError_t e = launch_adapter_u(x, m, cols, ad, s)) return e;
+    return row ? launch_linear_row(packed, rows, cols, sc, x, m, y, ep, u, lora_b, r, s)
+               : launch_linear_few(packed, rows, cols, sc, x, m, y, ep, u, lora_b, r, s);
+  }
   LinearArgs a{};
   a.packed = packed; a.rows = rows; a.cols = cols; a.sc = sc; a.m = m; a.y = y; a.ep = ep;
   a.x = reinterpret_cast<const uint16_t*>(w8);
   a.xe = reinterpret_cast<const int32_t*>(w8 + at.xe);
   a.we = reinterpret_cast<const int32_t*>(w8 + at.we);
   if (hipError_t e = launch_linear_prep(x, m, cols, reinterpret_cast<uint16_t*>(w8), reinterpret_cast<int32_t*>(w8 + at.xe), sc, rows,
-                                        reinterpret_cast<int32_t*>(w8 + at.we), s))
+                                        reinterpret_cast<int32_t*>(w8 + at.we), ad, s))
     return e;
   a.cb = codebook(sc.fp4);
   a.u = u;
   a.lb = lora_b;
   a.r = r;
-  a.r_pad = (r + 15) / 16 * 16;
-  a.kl = static_cast<int>(gemm_lora_cols(r));
+  a.r_pad = ad.r_pad;
+  a.kl = ad.kl;
   if (mid(m, rows, cols))
     return launch_linear_mid(mid_plan(m, rows, cols), packed, rows, cols, sc, a.x, a.xe, a.we, m, y, ep, a.u, lora_b, r,
                              reinterpret_cast<float*>(w8 + at.part), s);

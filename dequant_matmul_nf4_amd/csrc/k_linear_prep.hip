@@ -53,7 +53,8 @@ struct PrepArgs {
   Scales sc;
   int64_t rows;      // of the weight
   int32_t* we;
-  int64_t xgroups;   // workgroups of x, those of the weight behind them
+  int64_t xgroups, wgroups;  // workgroups of x, behind them those of the weight, then the adapters'
+  AdapterU ad;
 };
 
 __device__ __forceinline__ void weight_rows(const PrepArgs& a, int64_t group) {
@@ -75,10 +76,79 @@ __device__ __forceinline__ void weight_rows(const PrepArgs& a, int64_t group) {
   }
 }
 
+// Sums of 16 values over the 64 lanes: half of them given away at a time, so that lane l ends
+// with the sum of value 8 l5 + 4 l4 + 2 l3 + l2 (the bits of l).
+template <int off, int N>
+__device__ __forceinline__ void halve(float (&v)[16], bool upper) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float give = upper ? v[i] : v[N + i];
+    v[i] = (upper ? v[N + i] : v[i]) + __shfl_xor(give, off, 64);
+  }
+}
+
+// A row of x times 16 rows of A: (s T hi | s T lo) of them.  Products of bf16 values are exact in
+// float32, the sums are float32.  All of a workgroup's loads are whole lines; A comes from L2 for
+// all rows of x but the first.
+__device__ __forceinline__ void adapter_row(const PrepArgs& a, int64_t group, float (&red)[kWaves][16]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const AdapterU& d = a.ad;
+  const int chunks = d.r_pad / 16;
+  const int64_t t = group / chunks, n = a.cols / 8;
+  const int j0 = static_cast<int>(group - t * chunks) * 16;
+  const u32x4* in = reinterpret_cast<const u32x4*>(a.x + t * a.cols);
+  const u32x4* la = reinterpret_cast<const u32x4*>(d.a);
+  float v[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+  for (int64_t k = threadIdx.x; k < n; k += kThreads) {
+    const u32x4 x = in[k];
+    u32x4 w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = la[(j0 + j < d.r ? j0 + j : d.r - 1) * n + k];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        v[j] = fmaf(bf16_to_f32(x[c] & 0xFFFFu), bf16_to_f32(w[j][c] & 0xFFFFu), v[j]);
+        v[j] = fmaf(__uint_as_float(x[c] & 0xFFFF0000u), __uint_as_float(w[j][c] & 0xFFFF0000u), v[j]);
+      }
+  }
+  halve<32, 8>(v, lane & 32);
+  halve<16, 4>(v, lane & 16);
+  halve<8, 2>(v, lane & 8);
+  halve<4, 1>(v, lane & 4);
+  v[0] += __shfl_xor(v[0], 2, 64);
+  v[0] += __shfl_xor(v[0], 1, 64);
+  if ((lane & 3) == 0) red[wave][(lane >> 5) * 8 + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1)] = v[0];
+  __syncthreads();
+  uint16_t* u = d.u + t * d.kl;
+  if (threadIdx.x < 16) {
+    const int j = j0 + threadIdx.x;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) sum += red[w][threadIdx.x];
+    sum = j < d.r ? d.s * sum : 0.0f;
+    const uint32_t hi = f32_to_bf16(sum);
+    u[j] = static_cast<uint16_t>(hi);
+    u[d.r_pad + j] = static_cast<uint16_t>(f32_to_bf16(sum - bf16_to_f32(hi)));
+  }
+  if (j0 == 0)
+    for (int c = 2 * d.r_pad + threadIdx.x; c < d.kl; c += kThreads) u[c] = 0;
+}
+
+// The adapters' columns of x alone, for the kernels that take x as it is.
+__global__ __launch_bounds__(kThreads) void k_adapter_rows(PrepArgs a) {
+  __shared__ float red[kWaves][16];
+  adapter_row(a, blockIdx.x, red);
+}
+
 // One row of x: 16-byte pieces threadIdx, + 1024, ..: N of a thread, kept; 0: read twice.
 template <int N>
 __global__ __launch_bounds__(kThreads) void k_prep_row(PrepArgs a) {
   __shared__ uint32_t tops[kWaves];
+  __shared__ float red[kWaves][16];
+  if (static_cast<int64_t>(blockIdx.x) >= a.xgroups + a.wgroups) return adapter_row(a, blockIdx.x - a.xgroups - a.wgroups, red);
   if (static_cast<int64_t>(blockIdx.x) >= a.xgroups) return weight_rows(a, blockIdx.x - a.xgroups);
   const int64_t t = blockIdx.x, n = a.cols / 8, nk = a.cols / 64;
   const u32x4* in = reinterpret_cast<const u32x4*>(a.x + t * a.cols);
@@ -183,13 +253,24 @@ __global__ __launch_bounds__(kThreads) void k_prep_rows(PrepArgs a) {
 
 }  // namespace
 
+hipError_t launch_adapter_u(const uint16_t* x, int64_t m, int64_t cols, const AdapterU& ad, hipStream_t s) {
+  if (m > kFewRows) return launch_lora_u(x, ad.a, m, cols, ad.r, ad.s, ad.u, s);
+  PrepArgs a{};
+  a.x = x; a.m = m; a.cols = cols; a.ad = ad;
+  hipLaunchKernelGGL(k_adapter_rows, dim3(static_cast<unsigned>(m * (ad.r_pad / 16))), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
 hipError_t launch_linear_prep(const uint16_t* x, int64_t m, int64_t cols, uint16_t* x16, int32_t* xe, const Scales& sc,
-                              int64_t rows, int32_t* we, hipStream_t s) {
+                              int64_t rows, int32_t* we, const AdapterU& ad, hipStream_t s) {
   const bool few = m <= kFewRows;
+  if (!few && ad.r > 0)
+    if (hipError_t e = launch_lora_u(x, ad.a, m, cols, ad.r, ad.s, ad.u, s)) return e;
+  const int64_t ug = few && ad.r > 0 ? m * (ad.r_pad / 16) : 0;
   const int64_t xg = few ? m : (m + kRows - 1) / kRows, wg = (rows + kWeightRows - 1) / kWeightRows;
-  if (xg + wg > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const PrepArgs a{x, m, cols, x16, xe, sc, rows, we, xg};
-  const dim3 grid(static_cast<unsigned>(xg + wg)), block(kThreads);
+  if (xg + wg + ug > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const PrepArgs a{x, m, cols, x16, xe, sc, rows, we, xg, wg, ad};
+  const dim3 grid(static_cast<unsigned>(xg + wg + ug)), block(kThreads);
   const int64_t per = few ? (cols / 8 + kThreads - 1) / kThreads : (cols / 64 + kWaves - 1) / kWaves;
   if (few && per <= 2) hipLaunchKernelGGL((k_prep_row<2>), grid, block, 0, s, a);
   else if (few) hipLaunchKernelGGL((k_prep_row<0>), grid, block, 0, s, a);

@@ -85,14 +85,25 @@ __device__ __forceinline__ halfx8 expand(const uint32_t (&l)[4], half2 s) {
 
 }  // namespace f16
 
+// The adapters' columns of x: u[t] = (hi | lo | 0), kl values, with hi + lo = s x[t] . A^T in two
+// bf16 parts of r_pad values each (zeros past r); A [r][cols].
+struct AdapterU {
+  const uint16_t* a;
+  int r, r_pad, kl;
+  float s;
+  uint16_t* u;
+};
+hipError_t launch_adapter_u(const uint16_t* x, int64_t m, int64_t cols, const AdapterU& ad, hipStream_t s);
+
 // x16 = x[t] 2^-xe[t] in float16 for the m rows of x [m][cols] (cols % 64 == 0), in
 // blocks: the 16 bytes of row t, columns 64 k + 32 h + 8 s .. + 7 (h < 2, s < 4) are
 // number ((t / 32 cols / 64 + k) 4 + s) 64 + 32 h + t % 32 of x16, which holds m
 // rounded up to 32 rows (what lies past row m is not written).  we: the exponents of
 // the weight's rows.
+// ad: what the adapters' thin product needs, also left by this call where r > 0.
 constexpr int64_t x16_rows(int64_t m) { return (m + 31) / 32 * 32; }
 hipError_t launch_linear_prep(const uint16_t* x, int64_t m, int64_t cols, uint16_t* x16, int32_t* xe, const Scales& sc,
-                              int64_t rows, int32_t* we, hipStream_t s);
+                              int64_t rows, int32_t* we, const AdapterU& ad, hipStream_t s);
 
 // The linear product of one or two rows of x (k_gemv.hip) and of a decode batch
 // (k_linear_few.hip): x as it is, no exponents.
