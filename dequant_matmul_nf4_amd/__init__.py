@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import itertools
 import operator
 import os
 from dataclasses import dataclass
@@ -1216,32 +1217,38 @@ def _grad_list(grads, out=None):
     at, sizes = array.array("q", map(T.data_ptr, grads)), array.array("q", map(T.numel, grads))
     kind = array.array("q", [codes[dtypes[0]]]) * n if len(kinds) == 1 else array.array("q", map(codes.__getitem__, dtypes))
     words = array.array("q", bytes(32 * n))
-    words[0::4], words[2::4] = at, sizes
+    words[0::4], words[2::4], words[3::4] = at, sizes, kind
     if out is None:
-        words[1::4] = at
-        pair = [c | c << 32 for c in range(3)]
-        words[3::4] = array.array("q", [pair[kind[0]]]) * n if len(kinds) == 1 else array.array("q", map(pair.__getitem__, kind))
+        words[1::4], words[3::4] = at, array.array("q", map((1 + (1 << 32)).__mul__, kind))  # both types the gradient's
         return words, dev
     if out.dtype not in codes:
         raise TypeError(f"unsupported dtype {out.dtype}")
     _need("out", out, out.dtype, sum(sizes), dev)
     to, size, code = out.data_ptr(), out.element_size(), codes[out.dtype]
-    lo, hi = to, to + out.numel() * size
-    for i, (p, c, k) in enumerate(zip(at, sizes, kind)):
-        if p < hi and p + c * (4 if k == NF4_F32 else 2) > lo and c and (p != to or k != code):
+    places = array.array("q", itertools.accumulate(map(size.__mul__, sizes), initial=to))
+    end = places.pop()
+    for i, (lo, hi) in enumerate(_spans(words)):
+        if lo < end and hi > to and lo < hi and (lo != places[i] or kind[i] != code):
             raise ValueError("out shares memory with a gradient that does not lie exactly in its place")
-        words[4 * i + 1], words[4 * i + 3] = to, k | code << 32
-        to += c * size
+    words[1::4], words[3::4] = places, array.array("q", map((code << 32).__or__, kind))
     return words, dev
+
+
+def _spans(words):
+    """The memory of each gradient of a list."""
+    at, kinds = words[0::4], words[3::4]
+    kinds = [k & 3 for k in kinds]
+    return zip(at, map(operator.add, at, map(operator.mul, words[2::4], map((4, 2, 2).__getitem__, kinds))))
 
 
 def _apart(words) -> None:
     """Gradients that are scaled in place must not share memory."""
-    size = (4, 2, 2)
-    spans = sorted((p, p + n * size[c & 3]) for p, n, c in zip(words[0::4], words[2::4], words[3::4]) if n)
-    for (_, end), (begin, _) in zip(spans, spans[1:]):
-        if begin < end:
+    last = 0
+    for lo, hi in sorted(_spans(words)):
+        if lo < last and lo < hi:
             raise ValueError("two of the gradients share memory: scaled in place, each may be given once")
+        if hi > last:
+            last = hi
 
 
 def nf4_grad_norm(grads, norm=None, workspace=None, stream=None):
