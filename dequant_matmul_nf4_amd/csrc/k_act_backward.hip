@@ -10,6 +10,10 @@
 // and a second kernel adds the chunks in order (results do not depend on timing).
 // Rows of any length: loads and stores of 16 bytes need no alignment but the
 // element's, and the columns past the last whole 8 are taken one by one.
+//
+// Measured: 4096 x 14336 with gelu_tanh 70 us and 4.8 for the chunks' sums (352 MB, 5.0
+// TB/s); 333 x 11007 with gelu 13.4 and 3.9 (22 MB in one round of loads: latency).
+// 64 threads across, not 256: a fourth of the chunks, and so of their sums.
 #include "epilogue.h"
 #include "layer_ops.h"
 

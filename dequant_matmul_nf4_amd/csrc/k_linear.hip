@@ -39,7 +39,10 @@ constexpr int kBN = gt::kTileN, kBK = gt::kStep;
 constexpr int kMI = 8;
 // Which kernels take m rows of x.  A decode batch, and as many more as leave little work for a
 // workgroup (in tiles of 16 x 16 outputs, each with about 512 columns' worth of its own): the codes
-// streamed past x as it is.
+// streamed past x as it is, in one launch instead of two or three.  Measured against the best of the
+// others, us: 4096x4096 with 128 rows 24 and 30, with 192 43 and 34; 28672x8192 with 16 rows 42 and 61,
+// with 32 69 and 60; 1024x4096 with 512 rows 27 and 35, with 768 44 and 36; 4096x64 with 512 rows 14 and
+// 19, with 1024 23 and 19; 512x512 with 64 rows 5 and 20.
 bool few(int64_t m, int64_t rows, int64_t cols) {
   const int64_t groups = (rows + 15) / 16, tiles = (m + 15) / 16, cus = device_cus();
   if (tiles == 1) return true;
@@ -47,7 +50,11 @@ bool few(int64_t m, int64_t rows, int64_t cols) {
   const int64_t each = (groups + cus / tiles - 1) / (cus / tiles);
   return each * (cols + 512) <= 40960;
 }
-// Up to about 96 of this file's tiles, fewer of short rows: the kernel that cuts the reduction (k_linear_mid.hip).
+// Up to about 96 of this file's tiles, fewer of short rows: the kernel that cuts the reduction
+// (k_linear_mid.hip).  There and here, us: 14336x4096 with 384 rows (84 tiles) 79 and 97, with 512 (112)
+// 115 and 100; 28672x8192 with 192 rows (84) 131 and 185, with 256 (112) 188 and 185; 4096x14336 with 1024
+// (64) 190 and 292; 4096x1024 with 768 (48) 28 and 35, with 1024 (64) 46 and 35; 14336x256 with 192 (42)
+// 21 and 22, with 256 (56) 34 and 23.
 bool mid(int64_t m, int64_t rows, int64_t cols) {
   const int64_t most = cols >= 3584 ? 96 : 40 + cols / 64;
   return cols >= 256 && m <= 65536 && m <= (most * 65536 + rows - 1) / rows;

@@ -1,4 +1,30 @@
-// A layer's product with its epilogue for a decode batch: tiles of up to 16 rows of x.
+// A layer's product with its epilogue for a decode batch, and for more rows where
+// there is little work: tiles of 16 rows of x and 16 of the weight.
+//
+// A product of v_mfma_f32_16x16x32 spans half a block of each of its 16 weight
+// rows: the weight enters as its levels in float16 (rounded by 2^-11 at most), the two
+// products of a block run into an accumulator of their own, and the block's scale is
+// applied to that in float32, so no scaled weight is rounded.  x enters exactly but
+// for values 2^-29 of the largest of its row's 256 columns: scaled by a power of two of
+// those columns, taken back on their sums.
+//
+// Few rows are bound by reading the codes, small weights by latency, so a
+// workgroup of 16 waves (one per compute unit, 4 waves to a SIMD) covers up to 4096
+// columns at once: a wave takes 256 of them, holds x's share in registers and walks
+// over groups of 16 weight rows in steps of 2 KiB of codes, two steps on their way.
+// Every load's lanes lie side by side in memory, and codes, x and scales are
+// turned into operand order in the wave's own LDS: with a row to each lane the address
+// unit took 64 clocks a load, and 4096x4096 with 16 rows 23 us instead of 10.  Longer
+// rows have a wave take several segments, x of the next asked for before the
+// codes after it, because loads return in order.  The waves' partial tiles meet in
+// LDS and are added in wave order; then every output value has a thread of its own
+// for the epilogue (four to a thread spilled the walk's registers).
+//
+// Measured (int8 scales, time in a graph over changing weights): 16 rows of 512x512
+// 4.9 us, of 4096x4096 9.8, of 14336x4096 15.6, of 4096x14336 22, of 28672x8192 42.5
+// (2.9 TB/s: issue bounds it, about 100 vector and 40 LDS instructions a step; codes that
+// stay in cache take 29); 8 waves of 512 columns 11.4, 12.1, 15.4, 31 and 51, 8
+// waves of 256 with x a segment ahead and four steps on their way 43.9 for the last.
 #include "linear_epilogue.h"
 #include "linear_f16.h"
 #include "skinny_tile.h"
@@ -321,6 +347,9 @@ __global__ __launch_bounds__(kThreads, 4) void k_linear_few(FewArgs a) {
 
 template <bool kDQ, bool kF8>
 void launch(const FewArgs& a, dim3 grid, hipStream_t s) {
+  // A workgroup's groups in one go of one a wave, of two, or batches of four: what is held for more
+  // groups costs registers and loads that find nothing (4096x4096 with 16 rows 10.1 us by the first,
+  // 15 by the last; with 32 rows 11.4 by the second, 12.4 by the last).
   const int64_t groups = a.each + (a.more > 0 ? 1 : 0);
   if (groups <= a.rs) hipLaunchKernelGGL((k_linear_few<kDQ, kF8, 1>), grid, dim3(kThreads), 0, s, a);
   else if (groups <= 2 * a.rs) hipLaunchKernelGGL((k_linear_few<kDQ, kF8, 2>), grid, dim3(kThreads), 0, s, a);

@@ -1,5 +1,5 @@
-// A layer's product with its epilogue for a few to a few hundred rows of x
-// (decode batches, chunks of prompts): what bounds it is reading the codes once.
+// A layer's product with its epilogue for some tens to some hundreds of rows of x
+// (large decode batches, chunks of prompts): what bounds it is reading the codes once.
 //
 // Operands as in k_linear.hip: weights as level times scale in float16, x in
 // float16 blocks.  A workgroup of 4 waves takes 128 columns of y for up to 32 MI
@@ -13,6 +13,13 @@
 // Where the columns alone give too few workgroups the reduction is cut over
 // workgroups too: their sums go to the workspace in float32, and a second kernel
 // adds them in order and has the epilogue.
+//
+// Measured, us in all: 4096x14336 with 96 rows 39.5 (x's preparation 6, this kernel
+// 28, the joining 5.5), 14336x4096 with 96 rows 37, with 384 79 (570 TFLOP/s),
+// 28672x8192 with 64 rows 67.  The first loads and the level table are 10 us of
+// each, a step of 64 columns 0.95 us per 32 rows; what a product waits for is spelled
+// out between the products before it (left to the compiler, loads sank to their
+// use: 70 us instead of 41).
 #include "gemm_tiles.h"
 #include "linear_epilogue.h"
 #include "linear_f16.h"

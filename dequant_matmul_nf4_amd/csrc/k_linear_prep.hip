@@ -9,6 +9,11 @@
 // lines.  Of few rows, one to a workgroup: latency counts.  Of many, a workgroup of 16
 // waves takes 8, a wave instruction 8 rows x 64 columns (8 lines in, 8 lines out).
 //
+// The adapters' thin product, for the same rows: a workgroup takes a row of x and 16
+// rows of A, whole lines of both, and its waves' sums meet in LDS.  4096x14336 with rank
+// 16 pays 4 us for it with 96 rows and 8 with 16; on the matrix cores with a row to a
+// lane, as the product of many rows forms it, 27.
+//
 // The weight rows' exponents: that of the largest block scale, or with double
 // quantization of a bound on it, the largest of the row's group scales plus the
 // mean; a row per wave.
