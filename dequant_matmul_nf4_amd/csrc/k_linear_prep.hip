@@ -77,7 +77,7 @@ __device__ __forceinline__ void weight_rows(const PrepArgs& a, int64_t group) {
       for (int64_t g = (n * nblk >> 8) + lane; g <= (n * nblk + nblk - 1) >> 8; g += 64) top = fmaxf(top, fabsf(a.sc.absmax2[g]));
     }
     top = group_max<64>(top) + mean;
-    if (lane == 0) a.we[n] = f16::exponent_of(top);
+    if (lane == 0) a.we[n] = f16::exponent_of(top, a.ad.r > 0 ? f16::kLowAdapted : f16::kLow);
   }
 }
 
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(kThreads) void k_prep_row(PrepArgs a) {
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) top = tops[w] > top ? tops[w] : top;
-  const int e = f16::exponent_of(__uint_as_float(top));
+  const int e = f16::exponent_of(__uint_as_float(top), f16::kLow);
   const float up = f16::power(-e);
   if (threadIdx.x == 0) a.xe[t] = e;
   if constexpr (N > 0) {
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(kThreads) void k_prep_rows(PrepArgs a) {
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) top = tops[w][r] > top ? tops[w][r] : top;
-  const int e = f16::exponent_of(__uint_as_float(top));
+  const int e = f16::exponent_of(__uint_as_float(top), f16::kLow);
   const float up = f16::power(-e);
   if (t >= m) return;
   if (threadIdx.x < kRows) a.xe[t] = e;

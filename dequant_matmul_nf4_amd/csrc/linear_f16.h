@@ -34,13 +34,14 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float power(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// The exponent e such that v 2^-e lies in [2^kTop, 2^(kTop + 1)), at least kLow
-// (smaller v lie lower), so that adapters, which are brought to the same power,
-// keep room beside rows of zeros.
-constexpr int kLow = -60;
-__device__ __forceinline__ int exponent_of(float v) {
+// The exponent e such that v 2^-e lies in [2^kTop, 2^(kTop + 1)), at least `low`
+// (smaller v lie lower): what keeps 2^-e a normal number, but for the weight's rows
+// beside adapters, which are brought to the same power and need room beside rows of
+// zeros.
+constexpr int kLow = -112, kLowAdapted = -60;
+__device__ __forceinline__ int exponent_of(float v, int low) {
   const int e = static_cast<int>((__float_as_uint(v) >> 23) & 0xFF) - 127 - kTop;
-  return e < kLow ? kLow : e;
+  return e < low ? low : e;
 }
 
 __device__ __forceinline__ half2 twice(float s) {

@@ -210,6 +210,81 @@ def test_sizes_of_every_kernel(m, rows, cols):
     assert torch.equal(y, nf4.nf4_linear(W, x, act="gelu", **kw))
 
 
+# sizes of the kernel that cuts the reduction, with and without a second launch to join it, and of whole tiles
+LARGER = [(330, 2001, 4160), (520, 4001, 2112), (700, 9007, 640), (2100, 4100, 192)]
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m,rows,cols", LARGER)
+def test_activations_of_larger_sizes(act, m, rows, cols):
+    torch = need_gpu()
+    say("linear", act, m, rows, cols)
+    W = weight(torch, rows, cols)
+    x, kw = inputs(torch, m, rows, cols, "bf16", residual=True)
+    x = x * 3
+    y, pre = nf4.nf4_linear(W, x, act=act, save_pre=True, **kw)
+    check(torch, W, x, dict(kw, act=act), y, pre, act)
+
+
+@pytest.mark.parametrize("scales,fp4", [("plain", False), ("int8", False), ("fp8", False), ("int8", True), ("fp8", True), ("plain", True)])
+@pytest.mark.parametrize("m,rows,cols", LARGER)
+def test_scale_forms_of_larger_sizes(scales, fp4, m, rows, cols):
+    torch = need_gpu()
+    say("linear", scales, fp4, m, rows, cols)
+    W = weight(torch, rows, cols, scales, fp4)
+    x, kw = inputs(torch, m, rows, cols)
+    check(torch, W, x, kw, nf4.nf4_linear(W, x), label=scales)
+
+
+@pytest.mark.parametrize("rank", [1, 7, 16, 17, 48, 64])
+@pytest.mark.parametrize("m,rows,cols", LARGER + [(3, 1000, 5184), (1, 1000, 5184), (200, 515, 576)])
+def test_adapters_of_larger_sizes(rank, m, rows, cols):
+    torch = need_gpu()
+    say("linear adapters", rank, m, rows, cols)
+    W = weight(torch, rows, cols)
+    x, kw = inputs(torch, m, rows, cols, "f32", rank=rank)
+    check(torch, W, x, kw, nf4.nf4_linear(W, x, **kw))
+    zero = dict(kw, lora_b=torch.zeros_like(kw["lora_b"]))
+    assert torch.equal(nf4.nf4_linear(W, x, **zero), nf4.nf4_linear(W, x, bias=kw["bias"]))
+
+
+@pytest.mark.parametrize("m,rows,cols", LARGER + [(2, 1001, 4160), (16, 9001, 4416)])
+def test_buffers_and_rows_apart_of_larger_sizes(m, rows, cols):
+    """The residual added in place, given outputs and workspace, rows outside left alone; a row that is not finite reaches no other."""
+    torch = need_gpu()
+    say("linear buffers", m, rows, cols)
+    W = weight(torch, rows, cols)
+    x, kw = inputs(torch, m, rows, cols, "f32", residual=True, rank=5)
+    want, want_pre = nf4.nf4_linear(W, x, act="silu", save_pre=True, **kw)
+    y, pre = torch.full((2, m * rows + 64), 7.0, dtype=torch.bfloat16, device="cuda").unbind()
+    pre = torch.full_like(pre, 7.0)
+    y[:m * rows].copy_(kw["residual"].reshape(-1))
+    ws = torch.full((nf4.nf4_linear_workspace(m, rows, cols, 5) + 256,), 255, dtype=torch.uint8, device="cuda")
+    nf4.nf4_linear(W, x, act="silu", **dict(kw, residual=y[:m * rows]), y=y[:m * rows], pre=pre[:m * rows], workspace=ws[:-256])
+    assert torch.equal(y[:m * rows].view(m, rows), want) and torch.equal(pre[:m * rows].view(m, rows), want_pre)
+    assert (y[m * rows:] == 7).all() and (pre[m * rows:] == 7).all() and (ws[-256:] == 255).all()
+    for value in (float("nan"), float("inf")):
+        bad = x.clone()
+        bad[m // 2, 3] = value
+        z = nf4.nf4_linear(W, bad, act="silu", **kw)
+        keep = torch.arange(m, device="cuda") != m // 2
+        assert torch.equal(z[keep], want[keep])
+        if value != value:
+            assert z[m // 2].isnan().all()
+
+
+@pytest.mark.parametrize("m,rows,cols", LARGER + [(1, 1001, 4160), (2, 1001, 4160), (9, 4099, 4160)])
+@pytest.mark.parametrize("up,down", [(60, -50), (-60, 50), (90, -100), (-100, 90)])
+def test_range_of_larger_sizes(m, rows, cols, up, down):
+    """Weights and activations of any magnitude, whose products are ordinary numbers; rows of x of zeros."""
+    torch = need_gpu()
+    say("linear range", m, rows, cols, up)
+    W = nf4.quantize_weight(torch.randn((rows, cols), device="cuda").bfloat16() * 2.0 ** up)
+    x = (torch.randn((m, cols), device="cuda") * 2.0 ** down).bfloat16()
+    x[m // 3] = 0
+    check(torch, W, x, dict(act="silu"), nf4.nf4_linear(W, x, act="silu"))
+
+
 def test_many_tiles():
     """More work units than compute units, the last round cut in halves, and widths of several column tiles."""
     torch = need_gpu()
