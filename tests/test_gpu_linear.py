@@ -285,6 +285,35 @@ def test_range_of_larger_sizes(m, rows, cols, up, down):
     check(torch, W, x, dict(act="silu"), nf4.nf4_linear(W, x, act="silu"))
 
 
+@pytest.mark.parametrize("m,rows,cols", LARGER + [(2, 1001, 4160), (20, 9001, 4416)])
+def test_graph_of_larger_sizes(m, rows, cols):
+    """Captured once and replayed with other inputs, eager work between: each replay equals the eager call bit for bit."""
+    torch = need_gpu()
+    say("linear graph", m, rows, cols)
+    W = weight(torch, rows, cols)
+    x, kw = inputs(torch, m, rows, cols, "bf16", residual=True, rank=16)
+    y, pre = (torch.empty((m, rows), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws = torch.empty(nf4.nf4_linear_workspace(m, rows, cols, 16), dtype=torch.uint8, device="cuda")
+    call = lambda y, pre: nf4.nf4_linear(W, x, act="gelu", y=y, pre=pre, workspace=ws, **kw)  # noqa: E731
+    call(y, pre)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, capture_error_mode="relaxed"):
+        call(y, pre)
+    for rep in range(3):
+        x.copy_(torch.randn_like(x))
+        kw["residual"].copy_(torch.randn_like(kw["residual"]))
+        want = [torch.empty_like(y) for _ in range(2)]
+        call(*want)
+        y.zero_()
+        pre.zero_()
+        ws.fill_(255)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(pre, want[1]), rep
+
+
 def test_many_tiles():
     """More work units than compute units, the last round cut in halves, and widths of several column tiles."""
     torch = need_gpu()
