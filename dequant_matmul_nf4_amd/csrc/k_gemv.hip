@@ -8,6 +8,7 @@
 // 64-block).  Within a chunk the level values are summed against x in float32
 // and the block scale is applied once per chunk; the per-lane partial sums are
 // reduced across the wave with shuffles at the end.
+#include "gemv_plan.h"
 #include "gemv_rows.h"
 #include "linear_epilogue.h"
 #include "linear_f16.h"
@@ -320,24 +321,13 @@ __global__ __launch_bounds__(1024) void k_gemv_m1(const uint8_t* __restrict__ pa
 //    segments of each row are added in a fixed order, so the result does not
 //    depend on timing.
 
-constexpr int kRowsMaxWg = 512;   // rows per workgroup (LDS for the partial sums)
-constexpr int kSegMax = 16;       // column segments per workgroup (cols <= 65536)
-
-struct RowsPlan {
-  int grid;          // number of workgroups
-  int nseg;          // column segments
-  int seg_blocks;    // blocks per segment (<= 64)
-  int wpr;           // waves per segment (row parts)
-};
-
 // MC rows of x per launch (x points at the first of them, cols apart).
 // out.store(c, 1, row, s): takes the finished sum of x row c and weight row `row`.
 template <int U, int kWaves, int MC, bool kDQ, bool kF8, class Out>
 __device__ __forceinline__ void gemv_rows(const uint8_t* packed, int64_t rows, int64_t cols, const Scales& sc,
                                           const uint16_t* x, const Out& out, const Codebook& cb, const RowsPlan& pl) {
-  constexpr int kRowsWg = kRowsMaxWg / MC;
   __shared__ uint32_t tab[256 * 64];
-  __shared__ float part[kRowsWg * kSegMax * MC];
+  __shared__ float part[rows_room(MC) * kSegMax * MC];
   __shared__ float rtab[kDQ ? 256 : 1];
   const char* smem = reinterpret_cast<const char*>(tab);
   const int lane = threadIdx.x & 63;
@@ -455,29 +445,11 @@ __global__ __launch_bounds__(kWaves * 64) void k_linear_row(const uint8_t* packe
   gemv_rows<1, kWaves, MC, kDQ, kF8>(packed, rows, cols, sc, x, out, cb, pl);
 }
 
-// Plan for k_gemv_rows: rows split evenly over at least one workgroup per CU
-// (at most rows_wg rows each), columns into the fewest segments of at most 64
-// blocks, balanced, and the waves spread over the segments.
-RowsPlan rows_plan(int64_t rows, int64_t cols, int waves, int rows_wg) {
-  const int64_t cus = device_cus();
-  const int64_t nblk = cols / 64;
-  RowsPlan pl{};
-  pl.nseg = static_cast<int>((nblk + 63) / 64);
-  pl.seg_blocks = static_cast<int>((nblk + pl.nseg - 1) / pl.nseg);
-  pl.wpr = waves / pl.nseg;
-  // grid: one workgroup per CU, more if a workgroup would own more than
-  // rows_wg rows (wpr parts of ceil(rows / (grid * wpr)) rows each)
-  int64_t g = cus;
-  while (pl.wpr > 0 && pl.wpr * ((rows + g * pl.wpr - 1) / (g * pl.wpr)) > rows_wg) ++g;
-  pl.grid = static_cast<int>(g);
-  return pl;
-}
-
 template <int U, int kWaves, int MC, bool kDQ, bool kF8>
 hipError_t launch_rows(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x, void* y,
                        int y_bf16, hipStream_t s) {
-  const RowsPlan pl = rows_plan(rows, cols, kWaves, kRowsMaxWg / MC);
-  if (pl.nseg > kSegMax || pl.wpr < 1 || (cols / 64) * 32 >= (int64_t{1} << 32)) return hipErrorInvalidValue;
+  const RowsPlan pl = rows_plan(rows, cols, kWaves, MC, device_cus());
+  if (!rows_plan_fits(pl, rows, cols, MC)) return hipErrorInvalidValue;
   const int64_t g = pl.grid;
   const Codebook& cb = codebook(sc.fp4);
   const dim3 gd(static_cast<unsigned>(g)), bd(64 * kWaves);
@@ -893,8 +865,8 @@ int row_waves(int64_t rows, int64_t nseg) {
 template <int kWaves, int MC>
 hipError_t launch_linear_row_of(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x,
                                 const lin::FewOut& out, hipStream_t s) {
-  const RowsPlan pl = rows_plan(rows, cols, kWaves, kRowsMaxWg);
-  if (pl.nseg > kSegMax || pl.wpr < 1 || (cols / 64) * 32 >= (int64_t{1} << 32)) return hipErrorInvalidValue;
+  const RowsPlan pl = rows_plan(rows, cols, kWaves, MC, device_cus());
+  if (!rows_plan_fits(pl, rows, cols, MC)) return hipErrorInvalidValue;
   const Codebook& cb = codebook(sc.fp4);
   const dim3 gd(static_cast<unsigned>(pl.grid)), bd(64 * kWaves);
   if (sc.absmax) hipLaunchKernelGGL((k_linear_row<kWaves, MC, false, false>), gd, bd, 0, s, packed, rows, cols, sc, x, out, cb, pl);
