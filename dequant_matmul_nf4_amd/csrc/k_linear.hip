@@ -49,11 +49,14 @@ constexpr int kMI = 8;
 // others, us: 4096x4096 with 128 rows 24 and 30, with 192 43 and 34; 28672x8192 with 16 rows 42 and 61,
 // with 32 69 and 60; 1024x4096 with 512 rows 27 and 35, with 768 44 and 36; 4096x64 with 512 rows 14 and
 // 19, with 1024 23 and 19; 512x512 with 64 rows 5 and 20.
+// For a full chip, whatever the device: what a call needs of its workspace and how it rounds the
+// weight follow from the sizes alone.
+constexpr int64_t kChip = 256;
 bool few(int64_t m, int64_t rows, int64_t cols) {
-  const int64_t groups = (rows + 15) / 16, tiles = (m + 15) / 16, cus = device_cus();
+  const int64_t groups = (rows + 15) / 16, tiles = (m + 15) / 16;
   if (tiles == 1) return true;
-  if (tiles > cus) return false;
-  const int64_t each = (groups + cus / tiles - 1) / (cus / tiles);
+  if (tiles > kChip) return false;
+  const int64_t each = (groups + kChip / tiles - 1) / (kChip / tiles);
   return each * (cols + 512) <= 40960;
 }
 // Up to about 96 of this file's tiles, fewer of short rows: the kernel that cuts the reduction

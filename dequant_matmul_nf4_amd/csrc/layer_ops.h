@@ -17,7 +17,7 @@ struct Epilogue {
   const uint16_t* residual;  // [m][rows] bf16, or null; may be y itself
   uint16_t* pre;             // [m][rows] bf16, or null
 };
-size_t linear_workspace(int64_t m, int64_t rows, int64_t cols, int r);
+size_t linear_workspace(int64_t m, int64_t rows, int64_t cols, int r);  // by the sizes alone
 hipError_t launch_linear(const uint8_t* packed, int64_t rows, int64_t cols, Scales sc, const uint16_t* x, int64_t m,
                          uint16_t* y, const Epilogue& ep, const uint16_t* lora_a, const uint16_t* lora_b, int r,
                          float lora_scale, void* ws, hipStream_t s);
