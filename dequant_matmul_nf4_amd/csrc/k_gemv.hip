@@ -323,6 +323,8 @@ __global__ __launch_bounds__(1024) void k_gemv_m1(const uint8_t* __restrict__ pa
 
 // MC rows of x per launch (x points at the first of them, cols apart).
 // out.store(c, 1, row, s): takes the finished sum of x row c and weight row `row`.
+// Out::kZeroTail: lanes past a segment's end, whose loads repeat its last block, hold zeros of x; without
+// it their sums are multiplied by zero, which an infinity in that block turns into NaN.
 template <int U, int kWaves, int MC, bool kDQ, bool kF8, class Out>
 __device__ __forceinline__ void gemv_rows(const uint8_t* packed, int64_t rows, int64_t cols, const Scales& sc,
                                           const uint16_t* x, const Out& out, const Codebook& cb, const RowsPlan& pl) {
@@ -383,6 +385,15 @@ __device__ __forceinline__ void gemv_rows(const uint8_t* packed, int64_t rows, i
   for (int c = 0; c < MC; ++c)
 #pragma unroll
     for (int j = 0; j < 2; ++j) x_half_block_to_half(xv[c][j], xh[c][j], xinv[c][j]);
+  if constexpr (Out::kZeroTail)
+    if (seg_end < 64) {  // (the same in all of a wave)
+#pragma unroll
+      for (int c = 0; c < MC; ++c)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) xh[c][j][i] = on[j] ? xh[c][j][i] : 0u;
+    }
   float xsel[MC];
   lane_x_scales<MC>(xinv, on, xsel);
   const float mean = kDQ ? *sc.mean : 0.0f;
@@ -424,6 +435,7 @@ __device__ __forceinline__ void gemv_rows(const uint8_t* packed, int64_t rows, i
 // The product itself (y points at the first of the rows, `rows` apart) ...
 template <bool kBf16Out>
 struct StoreY {
+  static constexpr bool kZeroTail = false;
   void* __restrict__ y;
   int64_t rows;
   __device__ __forceinline__ void store(int c, int, int64_t row, const float (&z)[1]) const {

@@ -146,6 +146,7 @@ __device__ __forceinline__ bf16x8 adapter_x(const uint16_t* u, float by) { retur
 // What takes the sums of a few rows of x: N rows from t on, n of which exist, and
 // weight row `row`.
 struct FewOut {
+  static constexpr bool kZeroTail = true;
   int64_t rows;
   uint16_t* y;
   Epilogue ep;

@@ -1,0 +1,72 @@
+"""Rows of x with an infinity through nf4_linear: the definition's infinities, of its
+signs, and its NaN (an infinity times a weight of zero) in that row and nothing in
+any other, wherever the infinity lies, the last columns of a row above all, which the
+kernels read again where a row ends inside what they take at a time."""
+
+from __future__ import annotations
+
+import pytest
+
+import dequant_matmul_nf4_amd as nf4
+from tests.gpu_common import need_gpu, say
+from tests.linear_common import inputs, weight
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+@pytest.fixture(autouse=True)
+def _seed():
+    need_gpu().manual_seed(59)
+
+
+def same_class(torch, got, want):
+    """NaN in the same places, infinities of the same signs, everything else finite."""
+    w = torch.where(want.abs() > 3.4e38, want * INF, want)
+    return (torch.equal(got.isnan(), w.isnan()) and torch.equal(got == INF, w == INF)
+            and torch.equal(got == -INF, w == -INF))
+
+
+# one and two rows over one segment and several; widths that end inside a segment and whole ones
+ROW = [(1, 300, 4160), (2, 300, 4160), (1, 301, 2112), (2, 301, 2112), (1, 12301, 704), (2, 12301, 704), (1, 100, 8192), (2, 33, 14400)]
+
+
+@pytest.mark.parametrize("scales", ["int8", "fp8", "plain"])
+@pytest.mark.parametrize("m,rows,cols", ROW)
+def test_infinity_anywhere_in_a_row(m, rows, cols, scales):
+    torch = need_gpu()
+    say("linear infinite", m, rows, cols, scales)
+    W = weight(torch, rows, cols, scales)
+    x, kw = inputs(torch, m, rows, cols, "f32", residual=True)
+    clean = nf4.nf4_linear(W, x, **kw)
+    wd = nf4.nf4_dequantize(W, out_dtype=torch.float32).double()
+    t = m // 2
+    keep = torch.arange(m, device="cuda") != t
+    for places in ((cols - 1,), (cols - 8,), (cols - 33,), (cols - 64,), (0,), (cols // 2,), (cols - 1, cols - 2)):
+        for sign in (1.0, -1.0):
+            bad = x.clone()
+            for p in places:
+                bad[t, p] = sign * INF
+            y, pre = nf4.nf4_linear(W, bad, save_pre=True, **kw)
+            want = torch.zeros(rows, dtype=torch.float64, device="cuda")
+            for p in places:  # finite terms change nothing beside an infinity
+                want = want + bad[t, p].double() * wd[:, p]
+            assert same_class(torch, y[t].double(), want), (places, sign, int(y[t].isnan().sum()), int(want.isnan().sum()))
+            assert same_class(torch, pre[t].double(), want), (places, sign, "pre")
+            assert torch.equal(y[keep], clean[keep]), (places, sign, "other rows")
+
+
+@pytest.mark.parametrize("m,rows,cols", [(1, 300, 4160), (2, 301, 2112)])
+def test_row_of_nan(m, rows, cols):
+    """A NaN makes its whole row NaN and touches no other."""
+    torch = need_gpu()
+    say("linear nan", m, rows, cols)
+    W = weight(torch, rows, cols)
+    x, kw = inputs(torch, m, rows, cols, "bf16")
+    clean = nf4.nf4_linear(W, x, **kw)
+    for p in (0, cols - 1):
+        bad = x.clone()
+        bad[m - 1, p] = float("nan")
+        y = nf4.nf4_linear(W, bad, **kw)
+        assert y[m - 1].isnan().all() and torch.equal(y[:m - 1], clean[:m - 1])
