@@ -228,12 +228,18 @@ __global__ __launch_bounds__(kThreads, 4) void k_linear_few(FewArgs a) {
     const int e = static_cast<int>(top >> 23) - 127 < -112 ? -112 : static_cast<int>(top >> 23) - 127;
     const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
 #pragma unroll
-    for (int b = 0; b < kNb; ++b) {
-      const float f = b < nb ? up : 0.0f;  // zeros past the columns' end
+    for (int b = 0; b < kNb; ++b)
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) xv[b][u][c] = scaled_pair(xv[b][u][c], f);
+        for (int c = 0; c < 4; ++c) xv[b][u][c] = scaled_pair(xv[b][u][c], up);
+    if (nb < kNb) {  // zeros past the columns' end, whose loads repeat the last (times zero an infinity would be NaN)
+#pragma unroll
+      for (int b = 1; b < kNb; ++b)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) xv[b][u][c] = b < nb ? xv[b][u][c] : 0u;
     }
     const float down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
 #pragma unroll

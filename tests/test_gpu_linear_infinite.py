@@ -28,12 +28,13 @@ def same_class(torch, got, want):
             and torch.equal(got == -INF, w == -INF))
 
 
-# one and two rows over one segment and several; widths that end inside a segment and whole ones
+# one and two rows over one segment and several; a decode batch over both; widths that end inside a segment and whole ones
 ROW = [(1, 300, 4160), (2, 300, 4160), (1, 301, 2112), (2, 301, 2112), (1, 12301, 704), (2, 12301, 704), (1, 100, 8192), (2, 33, 14400)]
+FEW = [(3, 100, 64), (7, 100, 192), (16, 333, 576), (5, 40, 1088), (9, 300, 4416), (3, 17, 14400), (16, 64, 1024), (40, 70, 320), (2, 33, 576)]
 
 
 @pytest.mark.parametrize("scales", ["int8", "fp8", "plain"])
-@pytest.mark.parametrize("m,rows,cols", ROW)
+@pytest.mark.parametrize("m,rows,cols", ROW + FEW)
 def test_infinity_anywhere_in_a_row(m, rows, cols, scales):
     torch = need_gpu()
     say("linear infinite", m, rows, cols, scales)
@@ -57,7 +58,7 @@ def test_infinity_anywhere_in_a_row(m, rows, cols, scales):
             assert torch.equal(y[keep], clean[keep]), (places, sign, "other rows")
 
 
-@pytest.mark.parametrize("m,rows,cols", [(1, 300, 4160), (2, 301, 2112)])
+@pytest.mark.parametrize("m,rows,cols", [(1, 300, 4160), (2, 301, 2112), (7, 100, 192), (16, 333, 576)])
 def test_row_of_nan(m, rows, cols):
     """A NaN makes its whole row NaN and touches no other."""
     torch = need_gpu()
