@@ -323,8 +323,9 @@ __global__ __launch_bounds__(1024) void k_gemv_m1(const uint8_t* __restrict__ pa
 
 // MC rows of x per launch (x points at the first of them, cols apart).
 // out.store(c, 1, row, s): takes the finished sum of x row c and weight row `row`.
-// Out::kZeroTail: lanes past a segment's end, whose loads repeat its last block, hold zeros of x; without
-// it their sums are multiplied by zero, which an infinity in that block turns into NaN.
+// Out::kZeroTail: lanes past a segment's end, whose codes repeat its last block, take zeros for x; without
+// it they take that block's x and their sums are multiplied by zero, which an infinity in it turns into NaN.
+__device__ uint4 kZeros[4];  // 32 values of x, never written
 template <int U, int kWaves, int MC, bool kDQ, bool kF8, class Out>
 __device__ __forceinline__ void gemv_rows(const uint8_t* packed, int64_t rows, int64_t cols, const Scales& sc,
                                           const uint16_t* x, const Out& out, const Codebook& cb, const RowsPlan& pl) {
@@ -367,6 +368,7 @@ __device__ __forceinline__ void gemv_rows(const uint8_t* packed, int64_t rows, i
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const uint4* xp = reinterpret_cast<const uint4*>(x + c * cols + static_cast<int64_t>(blk[j]) * 64 + 32 * half);
+      if constexpr (Out::kZeroTail) xp = on[j] ? xp : kZeros;
 #pragma unroll
       for (int i = 0; i < 4; ++i) xv[c][j][i] = xp[i];
     }
@@ -385,15 +387,6 @@ __device__ __forceinline__ void gemv_rows(const uint8_t* packed, int64_t rows, i
   for (int c = 0; c < MC; ++c)
 #pragma unroll
     for (int j = 0; j < 2; ++j) x_half_block_to_half(xv[c][j], xh[c][j], xinv[c][j]);
-  if constexpr (Out::kZeroTail)
-    if (seg_end < 64) {  // (the same in all of a wave)
-#pragma unroll
-      for (int c = 0; c < MC; ++c)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) xh[c][j][i] = on[j] ? xh[c][j][i] : 0u;
-    }
   float xsel[MC];
   lane_x_scales<MC>(xinv, on, xsel);
   const float mean = kDQ ? *sc.mean : 0.0f;
