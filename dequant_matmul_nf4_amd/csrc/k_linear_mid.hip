@@ -91,6 +91,8 @@ __device__ __forceinline__ void adapters(floatx16 (&acc)[MI][kJ], const MidArgs&
   }
 }
 
+__device__ uint4 kZeros[256];  // a step of 32 rows of x, never written
+
 template <int MI, bool kDQ, bool kF8>
 __global__ __launch_bounds__(kThreads, 1) void k_linear_mid(MidArgs a) {
   constexpr int kX = MI < 2 ? 4 : 2;              // steps of x in registers
@@ -153,12 +155,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_linear_mid(MidArgs a) {
     const int64_t b = m0 / 32 + i;
     xb[i] = reinterpret_cast<const char*>(a.x) + (b < last ? b : last) * band;
   }
+  // (steps past the wave's last take zeros: times their scale of zero, an infinity in x would be NaN)
   auto load_x = [&](f16::halfx8 (&x)[MI][4], int k) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+    for (int i = 0; i < MI; ++i) {
+      const char* p = k < ke ? xb[i] + static_cast<int64_t>(k) * 4096 : reinterpret_cast<const char*>(kZeros);
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        x[i][s] = *reinterpret_cast<const f16::halfx8*>(xb[i] + static_cast<int64_t>(clamp(k)) * 4096 + s * 1024 + 16 * lane);
+      for (int s = 0; s < 4; ++s) x[i][s] = *reinterpret_cast<const f16::halfx8*>(p + s * 1024 + 16 * lane);
+    }
   };
 
   // rings of registers

@@ -28,13 +28,16 @@ def same_class(torch, got, want):
             and torch.equal(got == -INF, w == -INF))
 
 
-# one and two rows over one segment and several; a decode batch over both; widths that end inside a segment and whole ones
+# one and two rows over one segment and several; a decode batch over both; cut reductions, whole
+# tiles; widths that end inside what a wave takes and whole ones
 ROW = [(1, 300, 4160), (2, 300, 4160), (1, 301, 2112), (2, 301, 2112), (1, 12301, 704), (2, 12301, 704), (1, 100, 8192), (2, 33, 14400)]
 FEW = [(3, 100, 64), (7, 100, 192), (16, 333, 576), (5, 40, 1088), (9, 300, 4416), (3, 17, 14400), (16, 64, 1024), (40, 70, 320), (2, 33, 576)]
+MID = [(40, 9001, 4416), (150, 2001, 4160), (330, 2001, 4160), (97, 8199, 2112), (300, 9007, 640), (520, 4001, 2112), (200, 14343, 256)]
+TILES = [(1030, 4352, 256), (2100, 4100, 192), (700, 9007, 640)]
 
 
 @pytest.mark.parametrize("scales", ["int8", "fp8", "plain"])
-@pytest.mark.parametrize("m,rows,cols", ROW + FEW)
+@pytest.mark.parametrize("m,rows,cols", ROW + FEW + MID + TILES)
 def test_infinity_anywhere_in_a_row(m, rows, cols, scales):
     torch = need_gpu()
     say("linear infinite", m, rows, cols, scales)
@@ -58,7 +61,8 @@ def test_infinity_anywhere_in_a_row(m, rows, cols, scales):
             assert torch.equal(y[keep], clean[keep]), (places, sign, "other rows")
 
 
-@pytest.mark.parametrize("m,rows,cols", [(1, 300, 4160), (2, 301, 2112), (7, 100, 192), (16, 333, 576)])
+@pytest.mark.parametrize("m,rows,cols", [(1, 300, 4160), (2, 301, 2112), (7, 100, 192), (16, 333, 576), (150, 2001, 4160),
+                                         (1030, 4352, 256)])
 def test_row_of_nan(m, rows, cols):
     """A NaN makes its whole row NaN and touches no other."""
     torch = need_gpu()
