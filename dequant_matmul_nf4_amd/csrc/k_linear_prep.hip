@@ -136,7 +136,7 @@ __device__ __forceinline__ void adapter_row(const PrepArgs& a, int64_t group, fl
     sum = j < d.r ? d.s * sum : 0.0f;
     const uint32_t hi = f32_to_bf16(sum);
     u[j] = static_cast<uint16_t>(hi);
-    u[d.r_pad + j] = static_cast<uint16_t>(f32_to_bf16(sum - bf16_to_f32(hi)));
+    u[d.r_pad + j] = static_cast<uint16_t>(f32_to_bf16(rest_of(sum, bf16_to_f32(hi))));
   }
   if (j0 == 0)
     for (int c = 2 * d.r_pad + threadIdx.x; c < d.kl; c += kThreads) u[c] = 0;

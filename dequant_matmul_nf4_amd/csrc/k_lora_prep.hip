@@ -94,7 +94,7 @@ __global__ __launch_bounds__(kPW * kWave) void k_lora_prep(const uint16_t* __res
       } else {
         uint16_t* urow = static_cast<uint16_t*>(out) + i * kl;
         const __bf16 hi = static_cast<__bf16>(v);
-        const __bf16 lo = static_cast<__bf16>(v - static_cast<float>(hi));
+        const __bf16 lo = static_cast<__bf16>(rest_of(v, static_cast<float>(hi)));
         urow[j] = __builtin_bit_cast(uint16_t, hi);
         urow[r_pad + j] = __builtin_bit_cast(uint16_t, lo);
       }

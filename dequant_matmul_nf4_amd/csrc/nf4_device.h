@@ -18,6 +18,12 @@ __device__ __forceinline__ uint32_t f32_to_bf16(float f) {
   return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
 
+// What v's rounding to bfloat16, `whole`, leaves of it: nothing of an infinity (the
+// difference would be NaN).
+__device__ __forceinline__ float rest_of(float v, float whole) {
+  return fabsf(whole) == INFINITY ? 0.0f : v - whole;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return f32_to_bf16(lo) | (f32_to_bf16(hi) << 16);
 }

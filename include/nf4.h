@@ -544,7 +544,8 @@ size_t nf4_linear_workspace(int64_t m, int64_t rows, int64_t cols, int32_t r);
  *   workspace: at least nf4_linear_workspace(m, rows, cols, r) bytes, 256-byte
  *            aligned (may be NULL when that is 0); overwritten.
  * Sums are float32 in a fixed order, and a row's result depends on its own x
- * alone.  x enters the products in fp16, scaled by powers of two, and keeps all
+ * alone: an infinity in it gives the formula's infinities, and NaN where it
+ * meets a zero (of the weight, of A or of B) or one of the other sign.  x enters the products in fp16, scaled by powers of two, and keeps all
  * of bf16's bits but where it is 2^-29 of its row's largest value or less, or
  * below 2^-126.  Of the weight, few rows of x (a decode batch, or few columns of
  * y) meet its levels rounded to fp16, with the scales, which have to be below

@@ -75,3 +75,33 @@ def test_row_of_nan(m, rows, cols):
         bad[m - 1, p] = float("nan")
         y = nf4.nf4_linear(W, bad, **kw)
         assert y[m - 1].isnan().all() and torch.equal(y[:m - 1], clean[:m - 1])
+
+
+@pytest.mark.parametrize("rank", [1, 3, 17])
+@pytest.mark.parametrize("m,rows,cols", [(1, 300, 4160), (2, 301, 2112), (7, 100, 192), (16, 333, 576), (150, 2001, 4160), (330, 2001, 4160),
+                                         (700, 9007, 640), (1030, 4352, 256), (700, 33, 1088)])
+def test_infinity_through_adapters(m, rows, cols, rank):
+    """The adapters' thin factor of such a row is infinite itself; B decides between its infinities and NaN."""
+    torch = need_gpu()
+    say("linear infinite adapters", m, rows, cols, rank)
+    W = weight(torch, rows, cols)
+    x, kw = inputs(torch, m, rows, cols, "bf16", rank=rank)
+    kw["lora_b"] = kw["lora_b"].abs() + 0.01  # the sum over the rank keeps a sign where all of A's column have one
+    kw["lora_a"][:, -1] = kw["lora_a"][:, -1].abs() + 0.01
+    clean = nf4.nf4_linear(W, x, **kw)
+    wd = nf4.nf4_dequantize(W, out_dtype=torch.float32).double()
+    t = m - 1 if m < 3 else m // 3
+    keep = torch.arange(m, device="cuda") != t
+    seen = 0
+    for place in (cols - 1, 5):
+        for sign in (1.0, -1.0):
+            bad = x.clone()
+            bad[t, place] = sign * INF
+            y, pre = nf4.nf4_linear(W, bad, save_pre=True, **kw)
+            thin = bad[t, place].double() * kw["lora_a"][:, place].double()
+            want = bad[t, place].double() * wd[:, place] + (thin * kw["lora_b"].double()).sum(1)
+            assert same_class(torch, y[t].double(), want), (place, sign, int(y[t].isnan().sum()), int(want.isnan().sum()))
+            assert same_class(torch, pre[t].double(), want), (place, sign, "pre")
+            assert torch.equal(y[keep], clean[keep])
+            seen += int(want.isinf().sum())
+    assert seen > 0
