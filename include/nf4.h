@@ -545,15 +545,17 @@ size_t nf4_linear_workspace(int64_t m, int64_t rows, int64_t cols, int32_t r);
  *            aligned (may be NULL when that is 0); overwritten.
  * Sums are float32 in a fixed order, and a row's result depends on its own x
  * alone: an infinity in it gives the formula's infinities, and NaN where it
- * meets a zero (of the weight, of A or of B) or one of the other sign.  x enters the products in fp16, scaled by powers of two, and keeps all
- * of bf16's bits but where it is 2^-29 of its row's largest value or less, or
- * below 2^-126.  Of the weight, few rows of x (a decode batch, or few columns of
- * y) meet its levels rounded to fp16, with the scales, which have to be below
- * 2^104, applied to the sums in float32; more meet the fp16 product of level and
- * scale, each rounded to fp16: off by 3 2^-11 of the weight at most, and less
- * precise where a block's scale is 2^-24 of its row's largest or below, or below
- * 2^-120 (2^-70 beside adapters).  Both are closer to the weight than its
- * rounding to bf16 in nf4_gemm.  Which one: the sizes alone decide. */
+ * meets a zero (of the weight, of A or of B) or one of the other sign.
+ * Activations below 2^-118 in size may come out as zero.
+ * x enters the products in fp16, scaled by powers of two, and keeps all of bf16's
+ * bits but where it is 2^-29 of its row's largest value or less, or below 2^-126.
+ * Of the weight, few rows of x (a decode batch, or few columns of y) meet its
+ * levels rounded to fp16, with the scales, which have to be below 2^104, applied
+ * to the sums in float32; more meet the fp16 product of level and scale, each
+ * rounded to fp16: off by 3 2^-11 of the weight at most, and less precise where a
+ * block's scale is 2^-24 of its row's largest or below, or below 2^-120 (2^-70
+ * beside adapters).  Both are closer to the weight than its rounding to bf16 in
+ * nf4_gemm.  Which one: the sizes alone decide. */
 int nf4_linear(const nf4_weight* w, const void* x, int64_t m, void* y, const nf4_epilogue* ep, const void* lora_a,
                const void* lora_b, int32_t r, float lora_scale, void* workspace, size_t workspace_bytes, void* stream);
 
@@ -572,7 +574,8 @@ size_t nf4_act_backward_workspace(int64_t m, int64_t rows);
  *   dbias: float32 [rows], or NULL to skip it; not both NULL.
  *   workspace: at least nf4_act_backward_workspace(m, rows) bytes, 4-byte
  *          aligned, where dbias is given (may be NULL when that is 0); overwritten.
- * bf16 arrays 16-byte aligned.  Sums have a fixed order. */
+ * bf16 arrays 16-byte aligned.  Sums have a fixed order.  Slopes below 2^-118 in
+ * size may be taken as zero. */
 int nf4_act_backward(const void* dy, const void* pre, int64_t m, int64_t rows, int32_t act, void* dz, float* dbias,
                      void* workspace, size_t workspace_bytes, void* stream);
 
