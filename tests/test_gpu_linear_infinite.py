@@ -31,8 +31,9 @@ def same_class(torch, got, want):
 # one and two rows over one segment and several; a decode batch over both; cut reductions, whole
 # tiles; widths that end inside what a wave takes and whole ones
 ROW = [(1, 300, 4160), (2, 300, 4160), (1, 301, 2112), (2, 301, 2112), (1, 12301, 704), (2, 12301, 704), (1, 100, 8192), (2, 33, 14400)]
-FEW = [(3, 100, 64), (7, 100, 192), (16, 333, 576), (5, 40, 1088), (9, 300, 4416), (3, 17, 14400), (16, 64, 1024), (40, 70, 320), (2, 33, 576)]
-MID = [(40, 9001, 4416), (150, 2001, 4160), (330, 2001, 4160), (97, 8199, 2112), (300, 9007, 640), (520, 4001, 2112), (200, 14343, 256)]
+FEW = [(3, 100, 64), (7, 100, 192), (16, 333, 576), (5, 40, 1088), (9, 300, 4416), (3, 17, 14400), (16, 64, 1024), (40, 70, 320), (2, 33, 576), (40, 9001, 4416), (150, 2001, 4160),
+       (97, 8199, 2112)]
+MID = [(330, 2001, 4160), (300, 9007, 640), (520, 4001, 2112), (200, 14343, 256)]
 TILES = [(1030, 4352, 256), (2100, 4100, 192), (700, 9007, 640)]
 
 
