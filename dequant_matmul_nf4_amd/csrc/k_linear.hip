@@ -26,8 +26,10 @@
 // sits at slot p ^ (r % 16): no two rows of a store meet in a bank.
 //
 // Measured: 4096 rows of 14336x4096 with adapters, bias, pre and gelu_tanh 559 us (860
-// TFLOP/s; weights rounded to bf16 instead 10 us more), 516 for the whole call without
-// any of them.  Issue bounds it: the matrix cores are busy 40% of the cycles, at 2.05 GHz,
+// TFLOP/s; weights rounded to bf16 instead 10 us more), 504 for the whole call without
+// any of them.  The dense GEMM takes 485 with the same adapters and 467 without, and a
+// pass over y and pre 56 to 71: the fusion saves no time here, it keeps the precision.
+// Issue bounds it: the matrix cores are busy 40% of the cycles, at 2.05 GHz,
 // beside 3.3 vector and 1.1 LDS instructions a product.  Eight waves in place of four,
 // and that work pinned between the products as k_linear_mid.hip has it, were slower.
 #include "gemm_tiles.h"

@@ -21,10 +21,12 @@
 // for the epilogue (four to a thread spilled the walk's registers).
 //
 // Measured (int8 scales, time in a graph over changing weights): 16 rows of 512x512
-// 4.9 us, of 4096x4096 9.8, of 14336x4096 15.6, of 4096x14336 22, of 28672x8192 42.5
-// (2.9 TB/s: issue bounds it, about 100 vector and 40 LDS instructions a step; codes that
-// stay in cache take 29); 8 waves of 512 columns 11.4, 12.1, 15.4, 31 and 51, 8
-// waves of 256 with x a segment ahead and four steps on their way 43.9 for the last.
+// 4.9 us, of 4096x4096 9.8, of 14336x4096 16.7, of 4096x14336 22, of 28672x8192 42 to 44
+// (2.8 TB/s: issue bounds it, 191 vector and 49 LDS instructions a step in all, x's
+// conversion among them, which a wave of two segments makes for each of its two batches
+// of groups, four times in 14 steps; codes that stay in cache take 29); 8 waves of 512
+// columns 11.4, 12.1, 15.4, 31 and 51, 8 waves of 256 with x a segment ahead and four
+// steps on their way 43.9 for the last.
 #include "linear_epilogue.h"
 #include "linear_f16.h"
 #include "skinny_tile.h"
