@@ -321,11 +321,12 @@ __global__ __launch_bounds__(1024) void k_gemv_m1(const uint8_t* __restrict__ pa
 //    segments of each row are added in a fixed order, so the result does not
 //    depend on timing.
 
+__device__ uint4 kZeros[4];  // 32 values of x, never written
+
 // MC rows of x per launch (x points at the first of them, cols apart).
 // out.store(c, 1, row, s): takes the finished sum of x row c and weight row `row`.
 // Out::kZeroTail: lanes past a segment's end, whose codes repeat its last block, take zeros for x; without
 // it they take that block's x and their sums are multiplied by zero, which an infinity in it turns into NaN.
-__device__ uint4 kZeros[4];  // 32 values of x, never written
 template <int U, int kWaves, int MC, bool kDQ, bool kF8, class Out>
 __device__ __forceinline__ void gemv_rows(const uint8_t* packed, int64_t rows, int64_t cols, const Scales& sc,
                                           const uint16_t* x, const Out& out, const Codebook& cb, const RowsPlan& pl) {
